@@ -388,6 +388,111 @@ typedef struct {
 
 int fp8_grouped_gemm(const fp8_gemm_args_t* args, void* stream);
 
+/* ------------------------------------------------------------------------
+ * nvfp4_moe_decode -- a whole MoE FFN layer for a few tokens (a decode step)
+ * on the NVFP4 expert weights: routing, gate/up product, SiLU*mul, down
+ * product and weighted combine.  At this size the layer costs the bytes of
+ * the routed experts' weights, so the activations are not quantized at all:
+ * the layer computes with the values that the trainer's forward has (blog,
+ * "Two fixes": fake-quantized weights, activations left alone), which the
+ * W4A4 + RAC calls approximate for large batches.
+ *
+ * For token t with logits row l = logits[t, :] (a NaN counts as -inf):
+ *   topk_ids[t, :]     the k experts with the largest logit, ties toward the
+ *                      lower expert index, in (logit desc, index asc) order;
+ *   topk_weights[t, s] softmax(l) at that expert (not renormalized), 0 where
+ *                      the logit is -inf;
+ *   out[t, :] = sum over slots s with weight > 0, in slot order, of
+ *      topk_weights[t, s] * s_d[e] * W_d[e] h,
+ *      h = silu(g) * u,  [g; u] = s_gu[e] * W_gu[e] x[t, :]
+ * with W the exact dequantized values g * s_b.  A slot of weight 0 costs
+ * nothing and adds nothing, so rows that pad a batch to a captured size are
+ * given logits of -inf: their out row is 0 and their x row is not read.
+ * Products are exact and sums are FP32; x and h enter the matrix cores as
+ * fp16 pieces scaled per row and K range by a power of two: one piece (11
+ * bits, which holds a bf16 x exactly) for bf16, two (22 bits) for FP32.
+ *
+ * x [T, H] (row stride ldx) and out [T, H] (row stride ldo) have x_dtype;
+ * logits is float [T, E] (row stride ld_logits).  gu_* hold [E, 2I, H] with
+ * the gate in rows [0, I), d_* hold [E, H, I], in the layout of
+ * nvfp4_quantize, tensor scales [E].  topk_ids / topk_weights [T, k] are
+ * nullable.  Requires 0 <= T <= 64, 1 <= k <= min(E, 16), E <= 1024, H and I
+ * multiples of 32 up to 65536, ldx and ldo multiples of 8, x, out, codes and
+ * scales 16-byte aligned, ws 16-byte aligned.  Inputs and out may not
+ * overlap.  Finite x is a precondition for the row it is in only.  The
+ * result is deterministic.  With T == 0 nothing is enqueued.
+ * ------------------------------------------------------------------------ */
+typedef struct {
+  int64_t T, E, k, H, I;
+  const void* x;              /* [T, H] */
+  int64_t x_dtype, ldx;       /* nvfp4_in_dtype_t; elements */
+  const float* logits;        /* [T, E] */
+  int64_t ld_logits;
+  const uint8_t* gu_codes;    /* [E, 2I, H/2] */
+  const uint8_t* gu_scales;   /* [E, 2I, H/16] */
+  const float* gu_tscale;     /* [E] */
+  const uint8_t* d_codes;     /* [E, H, I/2] */
+  const uint8_t* d_scales;    /* [E, H, I/16] */
+  const float* d_tscale;      /* [E] */
+  void* out;                  /* [T, H], x_dtype */
+  int64_t ldo;
+  int32_t* topk_ids;          /* [T, k], nullable */
+  float* topk_weights;        /* [T, k], nullable */
+} nvfp4_moe_decode_args_t;
+
+size_t nvfp4_moe_decode_workspace_size(const nvfp4_moe_decode_args_t* args);
+int nvfp4_moe_decode(const nvfp4_moe_decode_args_t* args, void* ws, size_t ws_bytes,
+                     void* stream);
+
+/* ------------------------------------------------------------------------
+ * token_logprobs -- what a rollout records of each sampled token and a
+ * trainer scores again (the pages measure the rollout-trainer log-prob gap:
+ * blog post, section "What it buys"): the token's log-probability, the
+ * entropy of its distribution and the largest alternatives, in one pass over
+ * the logits.
+ *
+ * Per row t, with z_j = logits[t, j] * inv_temperature[t] (1 where NULL):
+ *   lse = log sum_j exp(z_j),  log p_j = z_j - lse
+ *   logprobs[t]  = log p_y, y = targets[t]; 0 where y < 0 (ignored
+ *                  position), NaN where y >= V
+ *   entropy[t]   = -sum_j p_j log p_j (a term with p_j = 0 is 0)
+ *   norm[t]      = {m, L}: m = max_j logits[t, j] (0 if all are -inf) and
+ *                  lse = m * inv_temperature[t] + L ln 2; what
+ *                  token_logprobs_backward reads
+ *   top_ids[t, :], top_logprobs[t, :]  the top_k largest logits in (logit
+ *                  desc, index asc) order and their log p; a NaN ranks as -inf
+ * Logits of -inf are masked tokens (probability 0).  A row of nothing else
+ * has logprobs -inf (0 where ignored), entropy 0, top_ids 0, 1, .. and
+ * top_logprobs -inf.  A NaN or +inf logit makes its row's statistics NaN.
+ *
+ * logits [T, V] float or bf16, row stride ld elements (any ld >= V, no
+ * alignment beyond the element's).  targets and logprobs are given together
+ * or both NULL; entropy, norm and inv_temperature are nullable; top_ids and
+ * top_logprobs are required if top_k > 0.  inv_temperature must be positive
+ * and finite.  Requires 1 <= V < 2^31, 0 <= top_k <= min(V, 32), T < 2^31.
+ * Sums are FP32; the result is deterministic.
+ *
+ * token_logprobs_backward -- the gradient of the logits:
+ *   grad[t, j] = inv_temperature[t] * ( a ([j = y] - p_j)
+ *                                       - b p_j (log p_j + entropy[t]) )
+ * with a = grad_logprobs[t] (0 where NULL, where y < 0, or where the whole
+ * row is masked) and b = grad_entropy[t] (0 where NULL), rounded once to the
+ * logits' dtype; 0 for masked tokens, NaN for a row with y >= V.  targets is
+ * required with grad_logprobs, entropy with grad_entropy.  grad_logits has
+ * row stride ldg >= V and may be the logits themselves (same ld).  No
+ * workspace.
+ * ------------------------------------------------------------------------ */
+size_t token_logprobs_workspace_size(int64_t T, int64_t V, int64_t top_k);
+int token_logprobs(const void* logits, int dtype, int64_t T, int64_t V, int64_t ld,
+                   const int64_t* targets, const float* inv_temperature, int64_t top_k,
+                   float* logprobs, float* entropy, float* norm, int32_t* top_ids,
+                   float* top_logprobs, void* ws, size_t ws_bytes, void* stream);
+int token_logprobs_backward(const void* logits, int dtype, int64_t T, int64_t V, int64_t ld,
+                            const int64_t* targets, const float* inv_temperature,
+                            const float* norm, const float* entropy,
+                            const float* grad_logprobs, const float* grad_entropy,
+                            void* grad_logits, int64_t ldg, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -51,6 +51,18 @@ class Fp8GemmArgs(ctypes.Structure):
     ]
 
 
+class MoEDecodeArgs(ctypes.Structure):
+    """Mirror of nvfp4_moe_decode_args_t."""
+    _fields_ = [
+        ("T", _I64), ("E", _I64), ("k", _I64), ("H", _I64), ("I", _I64),
+        ("x", _P), ("x_dtype", _I64), ("ldx", _I64),
+        ("logits", _P), ("ld_logits", _I64),
+        ("gu_codes", _P), ("gu_scales", _P), ("gu_tscale", _P),
+        ("d_codes", _P), ("d_scales", _P), ("d_tscale", _P),
+        ("out", _P), ("ldo", _I64), ("topk_ids", _P), ("topk_weights", _P),
+    ]
+
+
 _SIGS = {
     "nvfp4_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "nvfp4_quantize_workspace_size": (_SZ, [_I64, _I64]),
@@ -80,6 +92,13 @@ _SIGS = {
     "nvfp4_check_groups": (ctypes.c_int, [_P, _I64, _I64, _P, _I64]),
     "nvfp4_quantize_rac_static": (ctypes.c_int, [_P, ctypes.c_int, _I64, _I64, _I64, _P, _P, _P,
                                                  _P, _P, _P, _I64, _P, _P, _P, _P, _P, _P]),
+    "nvfp4_moe_decode_workspace_size": (_SZ, [ctypes.POINTER(MoEDecodeArgs)]),
+    "nvfp4_moe_decode": (ctypes.c_int, [ctypes.POINTER(MoEDecodeArgs), _P, _SZ, _P]),
+    "token_logprobs_workspace_size": (_SZ, [_I64, _I64, _I64]),
+    "token_logprobs": (ctypes.c_int, [_P, ctypes.c_int, _I64, _I64, _I64, _P, _P, _I64, _P, _P,
+                                      _P, _P, _P, _P, _SZ, _P]),
+    "token_logprobs_backward": (ctypes.c_int, [_P, ctypes.c_int, _I64, _I64, _I64, _P, _P, _P,
+                                               _P, _P, _P, _P, _I64, _P]),
 }
 EXPORTS = tuple(_SIGS)
 
@@ -152,6 +171,20 @@ class RacOut(NamedTuple):
     r: NVFP4
     selected: torch.Tensor       # int32 [n_select]
     kblock_active: torch.Tensor  # uint8 [K/16]
+
+
+class MoEDecodeOut(NamedTuple):
+    out: torch.Tensor           # [T, H], x's dtype
+    topk_ids: torch.Tensor      # int32 [T, k]
+    topk_weights: torch.Tensor  # float32 [T, k]
+
+
+class LogprobsOut(NamedTuple):
+    logprobs: Optional[torch.Tensor]      # float32 [T]
+    entropy: torch.Tensor                 # float32 [T]
+    norm: torch.Tensor                    # float32 [T, 2], for the backward call
+    top_ids: Optional[torch.Tensor]       # int32 [T, top_k]
+    top_logprobs: Optional[torch.Tensor]  # float32 [T, top_k]
 
 
 class RouteOut(NamedTuple):
@@ -432,3 +465,140 @@ def fp8_grouped_gemm(a: FP8, w: FP8, group_offsets: torch.Tensor, *, N: int, K: 
         epilogue=epilogue, out=_ptr(out))
     _check(lib().fp8_grouped_gemm(ctypes.byref(args), _stream(dev)))
     return out
+
+
+# --------------------------------------------- decode step: layer and tokens
+def _require(cond: bool, what: str):
+    if not cond:
+        raise ValueError(what)
+
+
+def _vector(t: Optional[torch.Tensor], n: int, dtype: torch.dtype, dev, name: str):
+    """A contiguous [n] tensor of one dtype on one device (or None)."""
+    _require(t is None or (t.dtype == dtype and t.shape == (n,) and t.device == dev
+                           and t.is_contiguous()), f"{name}: contiguous {dtype} [{n}] on {dev}")
+
+
+def _call(dev: torch.device, fn, *args):
+    """Runs fn(*args, stream) with dev current, on its current stream."""
+    if torch.cuda.current_device() == dev.index:
+        return _check(fn(*args, torch.cuda.current_stream(dev).cuda_stream))
+    with torch.cuda.device(dev):
+        _check(fn(*args, torch.cuda.current_stream(dev).cuda_stream))
+
+
+def _nvfp4_experts(w: NVFP4, E: int, N: int, K: int, dev, name: str):
+    for t, shape, dt in ((w.codes, (E, N, K // 2), torch.uint8),
+                         (w.scales, (E, N, K // 16), torch.uint8),
+                         (w.tscale, (E,), torch.float32)):
+        _require(t.dtype == dt and t.shape == shape and t.device == dev and t.is_contiguous(),
+                 f"{name}: contiguous {dt} {shape} on {dev}")
+
+
+def nvfp4_moe_decode(x: torch.Tensor, logits: torch.Tensor, wgu: NVFP4, wd: NVFP4, k: int, *,
+                     out: Optional[torch.Tensor] = None) -> MoEDecodeOut:
+    """The whole MoE FFN layer for up to 64 tokens on NVFP4 expert weights
+    wgu [E, 2I, H] (gate rows first) and wd [E, H, I], with unquantized
+    activations x [T, H] (bf16 or FP32, row stride honoured) and router logits
+    [T, E] (FP32, row stride honoured).  Rows whose logits are all -inf cost
+    nothing and give 0."""
+    _require(x.dim() == 2 and logits.dim() == 2 and x.shape[0] == logits.shape[0],
+             "x [T, H] and logits [T, E]")
+    T, H = x.shape
+    E = logits.shape[1]
+    dev = x.device
+    xd = _dtype_code(x)
+    _require(dev.type == "cuda" and logits.device == dev, "x and logits on one GPU")
+    _require(logits.dtype == torch.float32, "logits are float32")
+    _require(wd.codes.dim() == 3, "wd codes [E, H, I/2]")
+    I = wd.codes.shape[2] * 2
+    _nvfp4_experts(wgu, E, 2 * I, H, dev, "wgu")
+    _nvfp4_experts(wd, E, H, I, dev, "wd")
+    if out is None:
+        out = torch.empty((T, H), dtype=x.dtype, device=dev)
+    _require(out.shape == x.shape and out.dtype == x.dtype and out.device == dev,
+             "out like x")
+    ids = torch.empty((T, k), dtype=torch.int32, device=dev)
+    wts = torch.empty((T, k), dtype=torch.float32, device=dev)
+    ldx, ldl, ldo = (_row_stride(t, n) for t, n in ((x, "x"), (logits, "logits"), (out, "out")))
+    args = MoEDecodeArgs(
+        T, E, k, H, I, x.data_ptr(), xd, ldx, logits.data_ptr(), ldl,
+        wgu.codes.data_ptr(), wgu.scales.data_ptr(), wgu.tscale.data_ptr(),
+        wd.codes.data_ptr(), wd.scales.data_ptr(), wd.tscale.data_ptr(),
+        out.data_ptr(), ldo, ids.data_ptr(), wts.data_ptr())
+    L = lib()
+    ref = ctypes.byref(args)
+    ws = _ws(L.nvfp4_moe_decode_workspace_size(ref), dev)
+    _call(dev, L.nvfp4_moe_decode, ref, ws.data_ptr(), ws.numel())
+    return MoEDecodeOut(out, ids, wts)
+
+
+def _row_stride(t: torch.Tensor, name: str) -> int:
+    """Row stride of a 2-D tensor whose rows are contiguous and do not overlap."""
+    rows, cols = t.shape
+    _require(rows == 0 or cols <= 1 or t.stride(1) == 1, f"{name}: contiguous rows")
+    if rows <= 1:
+        return cols + -cols % 8
+    _require(t.stride(0) >= cols, f"{name}: rows overlap")
+    return t.stride(0)
+
+
+def token_logprobs(logits: torch.Tensor, targets: Optional[torch.Tensor] = None, *,
+                   top_k: int = 0, inv_temperature: Optional[torch.Tensor] = None) -> LogprobsOut:
+    """Log-probability of targets [T] (int64; negative = ignored, giving 0),
+    entropy and the top_k largest alternatives of each row of logits [T, V]
+    (bf16 or FP32, row stride honoured), at a temperature per row
+    (inv_temperature, float32 [T]).  Logits of -inf are masked tokens."""
+    _require(logits.dim() == 2, "logits [T, V]")
+    T, V = logits.shape
+    dev = logits.device
+    dt = _dtype_code(logits)
+    _require(dev.type == "cuda", "logits on a GPU")
+    _vector(targets, T, torch.int64, dev, "targets")
+    _vector(inv_temperature, T, torch.float32, dev, "inv_temperature")
+    lp = torch.empty(T, dtype=torch.float32, device=dev) if targets is not None else None
+    ent = torch.empty(T, dtype=torch.float32, device=dev)
+    norm = torch.empty((T, 2), dtype=torch.float32, device=dev)
+    ids = torch.empty((T, top_k), dtype=torch.int32, device=dev) if top_k > 0 else None
+    tlp = torch.empty((T, top_k), dtype=torch.float32, device=dev) if top_k > 0 else None
+    L = lib()
+    ws = _ws(L.token_logprobs_workspace_size(T, V, top_k), dev)
+    _call(dev, L.token_logprobs, logits.data_ptr(), dt, T, V, _row_stride(logits, "logits"),
+          _addr(targets), _addr(inv_temperature), top_k, _addr(lp), ent.data_ptr(),
+          norm.data_ptr(), _addr(ids), _addr(tlp), ws.data_ptr(), ws.numel())
+    return LogprobsOut(lp, ent, norm, ids, tlp)
+
+
+def token_logprobs_backward(logits: torch.Tensor, targets: Optional[torch.Tensor],
+                            norm: torch.Tensor, entropy: Optional[torch.Tensor],
+                            grad_logprobs: Optional[torch.Tensor],
+                            grad_entropy: Optional[torch.Tensor] = None, *,
+                            inv_temperature: Optional[torch.Tensor] = None,
+                            out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Gradient of the logits from those of token_logprobs's logprobs and
+    entropy (either may be None), with its norm and entropy.  out: where to
+    write it, which may be logits itself."""
+    _require(logits.dim() == 2, "logits [T, V]")
+    T, V = logits.shape
+    dev = logits.device
+    dt = _dtype_code(logits)
+    _require(dev.type == "cuda", "logits on a GPU")
+    _vector(targets, T, torch.int64, dev, "targets")
+    for t, n in ((inv_temperature, "inv_temperature"), (entropy, "entropy"),
+                 (grad_logprobs, "grad_logprobs"), (grad_entropy, "grad_entropy")):
+        _vector(t, T, torch.float32, dev, n)
+    _require(norm.shape == (T, 2) and norm.dtype == torch.float32 and norm.device == dev
+             and norm.is_contiguous(), "norm: float32 [T, 2]")
+    if out is None:
+        out = torch.empty((T, V), dtype=logits.dtype, device=dev)
+    _require(out.shape == logits.shape and out.dtype == logits.dtype and out.device == dev,
+             "out like logits")
+    ld, ldg = _row_stride(logits, "logits"), _row_stride(out, "out")
+    _call(dev, lib().token_logprobs_backward, logits.data_ptr(), dt, T, V, ld, _addr(targets),
+          _addr(inv_temperature), norm.data_ptr(), _addr(entropy), _addr(grad_logprobs),
+          _addr(grad_entropy), out.data_ptr(), ldg)
+    return out
+
+
+def _addr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()

@@ -143,6 +143,14 @@ def moe_block(x: torch.Tensor, logits: torch.Tensor, wgu: QuantWeights, wd: Quan
     return d
 
 
+def moe_decode(x: torch.Tensor, logits: torch.Tensor, wgu: QuantWeights, wd: QuantWeights,
+               topk: int, out: Optional[torch.Tensor] = None) -> L.MoEDecodeOut:
+    """The MoE FFN layer for up to 64 tokens, in token order, on the same
+    quantized weights as moe_block but with unquantized activations (what the
+    trainer's fake-quantized forward computes)."""
+    return L.nvfp4_moe_decode(x, logits, wgu.w, wd.w, topk, out=out)
+
+
 class GraphedMoEBlock:
     """moe_block captured once as a HIP graph (torch.cuda.CUDAGraph) for fixed
     T, H, E.  The graph reads its inputs from two static buffers: its own, or
@@ -226,3 +234,34 @@ class NVFP4WeightFakeQuant(torch.autograd.Function):
     @staticmethod
     def backward(ctx, grad: torch.Tensor) -> torch.Tensor:
         return grad
+
+
+class _TokenLogprobs(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, targets, inv_temperature):
+        r = L.token_logprobs(logits, targets, inv_temperature=inv_temperature)
+        ctx.save_for_backward(logits, targets, inv_temperature, r.norm, r.entropy)
+        ctx.set_materialize_grads(False)
+        return r.logprobs, r.entropy
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, g_logprobs, g_entropy):
+        logits, targets, inv_temperature, norm, entropy = ctx.saved_tensors
+        if g_logprobs is None and g_entropy is None:
+            return None, None, None
+        g = L.token_logprobs_backward(
+            logits, targets, norm, entropy,
+            None if g_logprobs is None else g_logprobs.contiguous(),
+            None if g_entropy is None else g_entropy.contiguous(),
+            inv_temperature=inv_temperature)
+        return g, None, None
+
+
+def token_logprobs(logits: torch.Tensor, targets: torch.Tensor,
+                   inv_temperature: Optional[torch.Tensor] = None
+                   ) -> Tuple[torch.Tensor, torch.Tensor]:
+    """(log-probabilities of targets, entropies) of logits [T, V], with the
+    gradient of the logits (the trainer's side of the rollout-trainer
+    log-prob gap).  Targets and temperatures get no gradient."""
+    return _TokenLogprobs.apply(logits, targets, inv_temperature)
