@@ -16,15 +16,57 @@
 namespace {
 
 constexpr int kLpMaxTop = 32;
+constexpr int kLpCand = 1024;  // candidates of a chunk before the ranking
+constexpr int kLpBwdU = 4;     // 16-byte pieces of a thread in the backward pass
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kInf = __builtin_inff();
 
-__device__ __forceinline__ float lp_load(const float* p) { return *p; }
-__device__ __forceinline__ float lp_load(const uint16_t* p) { return nv_bf16_to_f32(*p); }
+// 16 bytes of logits and what an absent element counts as.
+template <typename E>
+struct Lanes;
+template <>
+struct Lanes<float> {
+  static constexpr int N = 4;
+  static constexpr uint32_t kNone = 0xFF800000u;
+  static __device__ __forceinline__ float get(const uint4& v, int i) {
+    return __uint_as_float(i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w);
+  }
+  static __device__ __forceinline__ float load(const float* p) { return *p; }
+  static __device__ __forceinline__ void store(float* p, float v) { *p = v; }
+  static __device__ __forceinline__ uint4 pack(const float* f) {
+    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                      __float_as_uint(f[3]));
+  }
+};
+typedef __bf16 lp_bf16x2 __attribute__((ext_vector_type(2)));
+template <>
+struct Lanes<uint16_t> {
+  static constexpr int N = 8;
+  static constexpr uint32_t kNone = 0xFF80FF80u;
+  static __device__ __forceinline__ float get(const uint4& v, int i) {
+    const uint32_t w = i < 2 ? v.x : i < 4 ? v.y : i < 6 ? v.z : v.w;
+    return __uint_as_float((i & 1) ? (w & 0xFFFF0000u) : (w << 16));
+  }
+  static __device__ __forceinline__ float load(const uint16_t* p) { return nv_bf16_to_f32(*p); }
+  static __device__ __forceinline__ uint32_t pair(float a, float b) {  // nearest even, NaN kept
+    const lp_bf16x2 r = {(__bf16)a, (__bf16)b};
+    return __builtin_bit_cast(uint32_t, r);
+  }
+  static __device__ __forceinline__ void store(uint16_t* p, float v) { *p = (uint16_t)pair(v, v); }
+  static __device__ __forceinline__ uint4 pack(const float* f) {
+    return make_uint4(pair(f[0], f[1]), pair(f[2], f[3]), pair(f[4], f[5]), pair(f[6], f[7]));
+  }
+};
 
 __device__ __forceinline__ bool lp_better(float va, int ia, float vb, int ib) {
   return va > vb || (va == vb && ia < ib);
+}
+
+// Hides a piece's origin from the compiler, so that unpacked values of one
+// phase are not kept in registers for the next.
+__device__ __forceinline__ void lp_opaque(uint4& v) {
+  asm volatile("" : "+v"(v.x), "+v"(v.y), "+v"(v.z), "+v"(v.w));
 }
 
 // log p of a logit from the row's maximum m and L = log2 S.
@@ -32,138 +74,556 @@ __device__ __forceinline__ float lp_value(float l, float m, float it, float L) {
   return l == -kInf ? l : __builtin_fmaf(-kLn2, L, (l - m) * it);
 }
 
-// One workgroup per row; top_k further passes for the alternatives.
-template <typename E>
-__global__ __launch_bounds__(256) void k_logprob(const E* __restrict__ logits, int V, int64_t ld,
-                                                 const int64_t* __restrict__ targets,
-                                                 const float* __restrict__ inv_t, int top_k,
-                                                 float* __restrict__ logprobs,
-                                                 float* __restrict__ entropy,
-                                                 float* __restrict__ norm,
-                                                 int32_t* __restrict__ top_ids,
-                                                 float* __restrict__ top_lp) {
-  __shared__ float sa[256], sb[256];
-  __shared__ int si[256];
-  const int64_t t = blockIdx.x;
-  const E* row = logits + t * ld;
-  const float it = inv_t ? inv_t[t] : 1.0f, c = it * kLog2e;
-  const int tid = threadIdx.x;
-  float m = -kInf;
-  bool bad = false;
-  for (int j = tid; j < V; j += 256) {
-    const float l = lp_load(row + j);
-    bad |= l != l;
-    m = __builtin_fmaxf(m, l);
+// (m, S, Q) relative to its own maximum, brought to the maximum M.
+__device__ __forceinline__ void lp_rebase(float m, float M, float c, float& S, float& Q) {
+  const float delta = (m - M) * c;
+  const float f = m == -kInf ? 0.0f : __builtin_amdgcn_exp2f(delta);
+  Q = f > 0.0f ? f * __builtin_fmaf(S, delta, Q) : 0.0f;
+  S *= f;  // a NaN stays
+}
+
+__device__ __forceinline__ float lp_wave_max(float v) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) v = __builtin_fmaxf(v, __shfl_xor(v, o, 64));
+  return v;
+}
+__device__ __forceinline__ float lp_wave_sum(float v) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
+  return v;
+}
+
+// Float order as unsigned order (no NaN).
+__device__ __forceinline__ uint32_t lp_key(float v) {
+  const uint32_t u = __float_as_uint(v + 0.0f);  // -0 equals +0
+  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+
+// A bound that at least k of the wave's 64 values reach and that the k-th
+// largest is not far above: bisection on the upper 16 bits of the order key.
+// Returns the smallest float of the key prefix; -inf if fewer than k values
+// are above -inf.
+__device__ __forceinline__ float lp_wave_threshold(float v, int k) {
+  const uint32_t key = lp_key(v);
+  uint32_t lo = 0;
+#pragma unroll
+  for (int b = 31; b >= 16; --b) {
+    const uint32_t t = lo | (1u << b);
+    if (__popcll(__ballot(key >= t)) >= k) lo = t;
   }
-  sa[tid] = bad ? __builtin_nanf("") : m;
-  __syncthreads();
-  m = -kInf;
-  for (int i = 0; i < 256; ++i) m = (sa[i] != sa[i] || m != m) ? __builtin_nanf("") : __builtin_fmaxf(m, sa[i]);
-  __syncthreads();
-  const bool empty = m == -kInf;
-  if (empty) m = 0.0f;
-  float s = 0.0f, q = 0.0f;
-  for (int j = tid; j < V; j += 256) {
-    const float d = (lp_load(row + j) - m) * c;
-    const float e = __builtin_amdgcn_exp2f(d);
-    s += e;
-    if (e > 0.0f || e != e) q = __builtin_fmaf(d, e, q);
-  }
-  sa[tid] = s;
-  sb[tid] = q;
-  __syncthreads();
-  for (int o = 128; o > 0; o >>= 1) {
-    if (tid < o) {
-      sa[tid] += sa[tid + o];
-      sb[tid] += sb[tid + o];
+  const float f = __uint_as_float((lo & 0x80000000u) ? (lo ^ 0x80000000u) : ~lo);
+  return f == f ? f : -kInf;  // below the key of -inf
+}
+
+struct LpShared {
+  float val[kLpMaxTop];  // the best so far, ordered
+  int idx[kLpMaxTop];
+  int n;                 // how many
+  int cand;              // candidates of this chunk (may exceed the list)
+  float cval[kLpCand];
+  int cidx[kLpCand];
+};
+
+// Merges the first n candidates into the best list (one wave).  Each batch
+// puts the list and 64 - k candidates on the lanes; a lane's rank among them is
+// the number of lanes ahead of it.
+__device__ __forceinline__ void lp_merge(LpShared& sh, int n, int k) {
+  const int lane = threadIdx.x & 63;
+  int have = sh.n;
+  for (int c0 = 0; c0 < n; c0 += 64 - k) {
+    const int take = min(64 - k, n - c0), live = have + take;
+    float v = -kInf;
+    int i = 0x7fffffff;
+    if (lane < have) {
+      v = sh.val[lane];
+      i = sh.idx[lane];
+    } else if (lane < live) {
+      v = sh.cval[c0 + lane - have];
+      i = sh.cidx[c0 + lane - have];
     }
-    __syncthreads();
+    int rank = 0;
+    for (int o = 0; o < live; ++o) {
+      const float ov = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), o));
+      const int oi = __builtin_amdgcn_readlane(i, o);
+      rank += lp_better(ov, oi, v, i) ? 1 : 0;
+    }
+    if (lane < live && rank < k) {
+      sh.val[rank] = v;
+      sh.idx[rank] = i;
+    }
+    have = min(k, live);
   }
-  s = sa[0];
-  q = sb[0];
-  const float L = empty ? -kInf : __builtin_log2f(s);
-  __syncthreads();
-  if (tid == 0) {
+  if (lane == 0) sh.n = have;
+}
+
+// The best list of a row completed with masked tokens (one wave): fewer than
+// top_k logits are above -inf, so the first 2 top_k <= 64 tokens hold enough.
+template <typename E>
+__device__ __forceinline__ void lp_fill_masked(LpShared& sh, const E* row, int V, int k) {
+  const int lane = threadIdx.x & 63;
+  const int have = sh.n;
+  if (have >= k) return;
+  const float l = lane < V ? Lanes<E>::load(row + lane) : kInf;
+  const bool none = !(l > -kInf);  // -inf or NaN
+  const uint64_t bal = __ballot(none);
+  const int at = have + __popcll(bal & ((1ull << lane) - 1));
+  if (none && at < k) {
+    sh.val[at] = -kInf;
+    sh.idx[at] = lane;
+  }
+}
+
+// What one workgroup knows of a row, or of a part of one.
+struct LpPart {
+  float m, S, Q;
+  int n;
+};
+
+__host__ __device__ inline size_t lp_part_bytes(int top_k) {
+  return sizeof(LpPart) + 8 * (size_t)top_k;
+}
+
+// Writes a row's results (one wave).
+template <typename E>
+__device__ __forceinline__ void lp_finish(LpShared& sh, const E* row, int V, int64_t t, float gm,
+                                          float S, float Q, float it,
+                                          const int64_t* targets, int top_k, float* logprobs,
+                                          float* entropy, float* norm, int32_t* top_ids,
+                                          float* top_lp) {
+  const int lane = threadIdx.x & 63;
+  const bool empty = gm == -kInf && S == S;
+  const float m = gm == -kInf ? 0.0f : gm;
+  const float L = empty ? -kInf : __builtin_log2f(S);
+  if (lane == 0) {
     if (logprobs) {
       const int64_t y = targets[t];
       float lp = 0.0f;
       if (y >= V) lp = __builtin_nanf("");
-      else if (y >= 0) {
-        lp = lp_value(lp_load(row + y), m, it, L);
-      }
+      else if (y >= 0) lp = S == S ? lp_value(Lanes<E>::load(row + y), m, it, L) : S;
       logprobs[t] = lp;
     }
-    if (entropy) entropy[t] = empty ? 0.0f : (L - q / s) * kLn2;
+    if (entropy) entropy[t] = empty ? 0.0f : (L - Q / S) * kLn2;
     if (norm) {
       norm[2 * t] = m;
       norm[2 * t + 1] = L;
     }
   }
-  float pv = kInf;
-  int pi = -1;  // the last alternative written
-  for (int k = 0; k < top_k; ++k) {
-    float bv = -kInf;
-    int bi = 0x7fffffff;
-    for (int j = tid; j < V; j += 256) {
-      float l = lp_load(row + j);
-      if (l != l) l = -kInf;
-      const bool left = pi < 0 || lp_better(pv, pi, l, j);  // ranked after the last one
-      if (left && lp_better(l, j, bv, bi)) {
-        bv = l;
-        bi = j;
-      }
-    }
-    sa[tid] = bv;
-    si[tid] = bi;
-    __syncthreads();
-    for (int i = 0; i < 256; ++i)
-      if (lp_better(sa[i], si[i], bv, bi)) {
-        bv = sa[i];
-        bi = si[i];
-      }
-    __syncthreads();
-    pv = bv;
-    pi = bi;
-    if (tid == 0) {
-      top_ids[t * top_k + k] = bi;
-      top_lp[t * top_k + k] = s == s ? lp_value(bv, m, it, L) : s;
-    }
+  if (lane < top_k) {
+    top_ids[t * top_k + lane] = sh.idx[lane];
+    top_lp[t * top_k + lane] = S == S ? lp_value(sh.val[lane], m, it, L) : S;
   }
 }
 
-__device__ __forceinline__ void lp_store(float* p, float v) { *p = v; }
-__device__ __forceinline__ void lp_store(uint16_t* p, float v) {
-  *p = v != v ? (uint16_t)0x7FC0 : (uint16_t)nv_f32_to_bf16(v);
+// One workgroup of NT threads per (row, part).  A thread holds U 16-byte
+// pieces of the logits in registers: their maximum is known before the first
+// exponential, so each element costs one exponential and the memory is read
+// once.  The alternatives come from the same registers: the 64 maxima over
+// lanes give a bound that at least top_k elements reach, and the few elements
+// at or above it (and above the worst of the best so far) become candidates;
+// one wave ranks them.  Rows start at any element: the pieces are those that
+// lie wholly inside the row at 16-byte addresses, and the up to N - 1 elements
+// before and after them go one to a thread.
+template <typename E, int NT, bool TOP>
+__global__ __launch_bounds__(NT, 4) void k_logprob(
+    const E* __restrict__ logits, int V, int64_t ld, const int64_t* __restrict__ targets,
+    const float* __restrict__ inv_t, int top_k, int parts, float* __restrict__ logprobs,
+    float* __restrict__ entropy, float* __restrict__ norm, int32_t* __restrict__ top_ids,
+    float* __restrict__ top_lp, uint8_t* __restrict__ ws) {
+  typedef Lanes<E> LE;
+  constexpr int N = LE::N, U = 16, NW = NT / 64;
+  __shared__ float lane_max[TOP ? NW * 64 : 1];
+  __shared__ float red[3 * NW];
+  __shared__ LpShared sh;
+  const int64_t t = blockIdx.x / parts;
+  const int part = (int)(blockIdx.x % parts);
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const E* row = logits + t * ld;
+  const float it = inv_t ? inv_t[t] : 1.0f, c = it * kLog2e;
+  const int head = min((int)((16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15) / (int)sizeof(E), V);
+  const int nv = (V - head) / N, tail = head + nv * N;  // pieces; first element after them
+  const uint4* vec = reinterpret_cast<const uint4*>(row + head);
+  const int per = (nv + parts - 1) / parts, v0 = min(part * per, nv), v1 = min(v0 + per, nv);
+
+  float m = -kInf, S = 0.0f, Q = 0.0f;
+  if (TOP && tid == 0) sh.n = sh.cand = 0;
+  if (TOP) __syncthreads();
+  bool first = true;
+  for (int b = v0; first || b < v1; b += NT * U) {
+    uint4 x[U];
+    float pm[U], tm = -kInf;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = b + u * NT + tid;
+      x[u] = make_uint4(LE::kNone, LE::kNone, LE::kNone, LE::kNone);
+      if (i < v1) x[u] = vec[i];
+    }
+    // elements outside the pieces, with the first part's first chunk
+    float ev = -kInf;
+    int ei = -1;
+    if (first && part == 0) {
+      if (tid < head) ei = tid;
+      else if (tid >= 32 && tail + tid - 32 < V && tid < 32 + N) ei = tail + tid - 32;
+      if (ei >= 0) ev = LE::load(row + ei);
+    }
+    first = false;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      float v = -kInf;
+      if (b + u * NT + wave * 64 < v1) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v = __builtin_fmaxf(v, LE::get(x[u], i));
+      }
+      pm[u] = v;
+      tm = __builtin_fmaxf(tm, v);
+      lp_opaque(x[u]);
+    }
+    tm = __builtin_fmaxf(tm, ev);
+    const float M = __builtin_fmaxf(m, tm);
+    if (M > m && m != -kInf) lp_rebase(m, M, c, S, Q);
+    m = M;
+    const float ref = m == -kInf ? 0.0f : m;
+    auto add = [&](float l) {
+      const float d = (l - ref) * c;
+      const float e = __builtin_amdgcn_exp2f(d);
+      S += e;
+      Q = __builtin_fmaf(__builtin_fmaxf(d, -1e4f), e, Q);  // 2^-1e4 is 0; no 0 * inf
+    };
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (b + u * NT + wave * 64 < v1) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) add(LE::get(x[u], i));
+        lp_opaque(x[u]);
+      }
+    if (ei >= 0) add(ev);
+
+    if constexpr (TOP) {
+      lane_max[wave * 64 + lane] = tm;
+      __syncthreads();
+      float g = -kInf;
+#pragma unroll
+      for (int w = 0; w < NW; ++w) g = __builtin_fmaxf(g, lane_max[w * 64 + lane]);
+      float tau = lp_wave_threshold(g, top_k);
+      if (sh.n == top_k) tau = __builtin_fmaxf(tau, sh.val[top_k - 1]);
+      auto offer = [&](float l, int j) {
+        if (l >= tau && l > -kInf) {
+          const int at = atomicAdd(&sh.cand, 1);
+          if (at < kLpCand) {
+            sh.cval[at] = l;
+            sh.cidx[at] = j;
+          }
+        }
+      };
+      if (__ballot(tm >= tau && tm > -kInf)) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (__ballot(pm[u] >= tau && pm[u] > -kInf)) {
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+              offer(LE::get(x[u], i), head + (b + u * NT + tid) * N + i);
+          }
+        if (ei >= 0) offer(ev, ei);
+      }
+      __syncthreads();
+      const int n = sh.cand;
+      if (n > kLpCand) {
+        // many ties at the bound: top_k rounds of an arg-max over the chunk
+        float pv = kInf;
+        int pi = -1;
+        const int j0 = head + b * N, j1 = head + min(b + NT * U, v1) * N;
+        for (int k = 0; k < top_k; ++k) {
+          float bv = -kInf;
+          int bi = 0x7fffffff;
+          auto seen = [&](float l, int j) {
+            if (l > -kInf && lp_better(pv, pi, l, j) && lp_better(l, j, bv, bi)) {
+              bv = l;
+              bi = j;
+            }
+          };
+          for (int j = j0 + tid; j < j1; j += NT) seen(LE::load(row + j), j);
+          if (ei >= 0) seen(ev, ei);
+#pragma unroll
+          for (int o = 32; o > 0; o >>= 1) {
+            const float ov = __shfl_xor(bv, o, 64);
+            const int oi = __shfl_xor(bi, o, 64);
+            if (lp_better(ov, oi, bv, bi)) {
+              bv = ov;
+              bi = oi;
+            }
+          }
+          __syncthreads();  // the list may still be read
+          if (lane == 0) {
+            sh.cval[kLpMaxTop + wave] = bv;
+            sh.cidx[kLpMaxTop + wave] = bi;
+          }
+          __syncthreads();
+          for (int w = 0; w < NW; ++w)
+            if (lp_better(sh.cval[kLpMaxTop + w], sh.cidx[kLpMaxTop + w], bv, bi)) {
+              bv = sh.cval[kLpMaxTop + w];
+              bi = sh.cidx[kLpMaxTop + w];
+            }
+          if (tid == 0) {
+            sh.cval[k] = bv;
+            sh.cidx[k] = bi;
+          }
+          pv = bv;
+          pi = bi;
+        }
+        __syncthreads();
+      }
+      if (wave == 0) {
+        lp_merge(sh, n > kLpCand ? top_k : n, top_k);
+        if (lane == 0) sh.cand = 0;
+      }
+      __syncthreads();
+    }
+  }
+
+  // the workgroup's (m, S, Q)
+  const float wm = lp_wave_max(m);
+  if (wm > -kInf || S != S) lp_rebase(m, wm, c, S, Q);
+  S = lp_wave_sum(S);
+  Q = lp_wave_sum(Q);
+  float gm = wm;
+  if constexpr (NW > 1) {
+    if (lane == 0) {
+      red[3 * wave] = wm;
+      red[3 * wave + 1] = S;
+      red[3 * wave + 2] = Q;
+    }
+    __syncthreads();
+    if (wave > 0) return;
+    const float a = lane < NW ? red[3 * lane] : -kInf;
+    S = lane < NW ? red[3 * lane + 1] : 0.0f;
+    Q = lane < NW ? red[3 * lane + 2] : 0.0f;
+    gm = lp_wave_max(a);
+    if (gm > -kInf || S != S) lp_rebase(a, gm, c, S, Q);
+    S = lp_wave_sum(S);
+    Q = lp_wave_sum(Q);
+  }
+  if (parts > 1) {
+    uint8_t* out = ws + blockIdx.x * lp_part_bytes(TOP ? top_k : 0);
+    if (lane == 0) *reinterpret_cast<LpPart*>(out) = LpPart{gm, S, Q, TOP ? sh.n : 0};
+    if (TOP && lane < sh.n) {
+      reinterpret_cast<float*>(out + sizeof(LpPart))[lane] = sh.val[lane];
+      reinterpret_cast<int*>(out + sizeof(LpPart))[top_k + lane] = sh.idx[lane];
+    }
+    return;
+  }
+  if (TOP) lp_fill_masked(sh, row, V, top_k);
+  lp_finish<E>(sh, row, V, t, gm, S, Q, it, targets, TOP ? top_k : 0, logprobs, entropy, norm,
+               top_ids, top_lp);
 }
 
+// Joins the parts of a row: one wave per row.
 template <typename E>
-__global__ __launch_bounds__(256) void k_logprob_bwd(
-    const E* logits, int V, int64_t ld, const int64_t* __restrict__ targets,
+__global__ __launch_bounds__(64) void k_logprob_join(
+    const E* __restrict__ logits, int V, int64_t ld, const int64_t* __restrict__ targets,
+    const float* __restrict__ inv_t, int top_k, int parts, float* __restrict__ logprobs,
+    float* __restrict__ entropy, float* __restrict__ norm, int32_t* __restrict__ top_ids,
+    float* __restrict__ top_lp, const uint8_t* __restrict__ ws) {
+  __shared__ LpShared sh;
+  const int64_t t = blockIdx.x;
+  const int lane = threadIdx.x;
+  const E* row = logits + t * ld;
+  const float it = inv_t ? inv_t[t] : 1.0f, c = it * kLog2e;
+  const size_t step = lp_part_bytes(top_k);
+  const uint8_t* in = ws + t * parts * step;
+  LpPart p{-kInf, 0.0f, 0.0f, 0};  // parts <= 64
+  if (lane < parts) p = *reinterpret_cast<const LpPart*>(in + lane * step);
+  const float gm = lp_wave_max(p.m);
+  if (gm > -kInf || p.S != p.S) lp_rebase(p.m, gm, c, p.S, p.Q);
+  const float S = lp_wave_sum(p.S), Q = lp_wave_sum(p.Q);
+  if (top_k) {
+    // a bound that top_k of the parts' entries reach: the top_k-th best of
+    // their heads would do for many parts; the lists are short, so all of them
+    // go through the candidates, 64 parts x 32 entries at most
+    int at = p.n;  // exclusive sum over the lanes
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int v = __shfl_up(at, o, 64);
+      if (lane >= o) at += v;
+    }
+    const int total = __shfl(at, 63, 64);
+    at -= p.n;
+    if (lane == 0) sh.n = 0;
+    for (int c0 = 0; c0 < total; c0 += kLpCand) {
+      __syncthreads();
+      const float* val = reinterpret_cast<const float*>(in + lane * step + sizeof(LpPart));
+      for (int i = 0; i < p.n; ++i)
+        if (at + i >= c0 && at + i < c0 + kLpCand) {
+          sh.cval[at + i - c0] = val[i];
+          sh.cidx[at + i - c0] = reinterpret_cast<const int*>(val)[top_k + i];
+        }
+      __syncthreads();
+      lp_merge(sh, min(kLpCand, total - c0), top_k);
+    }
+    __syncthreads();
+    lp_fill_masked(sh, row, V, top_k);
+  }
+  lp_finish<E>(sh, row, V, t, gm, S, Q, it, targets, top_k, logprobs, entropy, norm, top_ids,
+               top_lp);
+}
+
+// The gradient: one pass, each element read and written by the same thread
+// (so the gradient may replace the logits).  With k0 = -it (a + b H) and
+// k1 = -it b ln 2, grad_j = p_j (k0 + k1 d_j), plus it a at the target.
+template <typename E, int NT, bool VEC>
+__global__ __launch_bounds__(NT) void k_logprob_bwd(
+    const E* logits, int64_t T, int V, int64_t ld, const int64_t* __restrict__ targets,
     const float* __restrict__ inv_t, const float* __restrict__ norm,
     const float* __restrict__ entropy, const float* __restrict__ g_lp,
     const float* __restrict__ g_ent, E* grad, int64_t ldg) {
-  const int64_t t = blockIdx.x;
-  const float it = inv_t ? inv_t[t] : 1.0f;
-  const float m = norm[2 * t], L = norm[2 * t + 1], c = it * kLog2e;
-  const bool empty = L == -kInf;
-  const int64_t y = targets ? targets[t] : -1;
-  float a = (g_lp && y >= 0 && !empty) ? g_lp[t] : 0.0f;
-  if (g_lp && y >= V) a = __builtin_nanf("");
-  const float b = g_ent ? g_ent[t] : 0.0f, h = g_ent ? entropy[t] : 0.0f;
-  for (int j = threadIdx.x; j < V; j += 256) {
-    const float d = empty ? -kInf : (lp_load(logits + t * ld + j) - m) * c - L;
-    const float p = __builtin_amdgcn_exp2f(d);
-    float g = (j == y ? a : 0.0f) - p * a;
-    if (p > 0.0f) g -= b * p * (d * kLn2 + h);
-    lp_store(grad + t * ldg + j, it * g);
+  typedef Lanes<E> LE;
+  constexpr int N = LE::N;
+  for (int64_t t = blockIdx.y; t < T; t += gridDim.y) {
+    const E* row = logits + t * ld;
+    E* out = grad + t * ldg;
+    const float it = inv_t ? inv_t[t] : 1.0f, c = it * kLog2e;
+    const float m = norm[2 * t], L = norm[2 * t + 1];
+    const bool empty = L == -kInf;
+    const int64_t y = targets ? targets[t] : -1;
+    float a = (g_lp && y >= 0 && !empty) ? g_lp[t] : 0.0f;
+    if ((g_lp && y >= V) || L != L) a = __builtin_nanf("");
+    const float b = (g_ent && !empty) ? g_ent[t] : 0.0f;
+    const float k0 = -it * (a + (g_ent && !empty ? b * entropy[t] : 0.0f)), k1 = -it * kLn2 * b;
+    const float Lf = empty ? kInf : L;
+    auto value = [&](float l) {
+      const float d = __builtin_fmaxf(__builtin_fmaf(l - m, c, -Lf), -1e4f);  // 2^-1e4 is 0
+      return __builtin_amdgcn_exp2f(d) * __builtin_fmaf(k1, d, k0);
+    };
+    auto one = [&](int j) {
+      const float g = value(LE::load(row + j));
+      LE::store(out + j, j == y ? __builtin_fmaf(it, a, g) : g);
+    };
+    if constexpr (!VEC) {
+      for (int64_t j = (int64_t)blockIdx.x * NT + threadIdx.x; j < V; j += (int64_t)gridDim.x * NT)
+        one((int)j);
+    } else {
+      const int head =
+          min((int)((16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15) / (int)sizeof(E), V);
+      const int nv = (V - head) / N, tail = head + nv * N;
+      const uint4* vec = reinterpret_cast<const uint4*>(row + head);
+      uint4* dst = reinterpret_cast<uint4*>(out + head);
+      for (int i0 = blockIdx.x * (NT * kLpBwdU); i0 < nv; i0 += gridDim.x * (NT * kLpBwdU)) {
+        uint4 x[kLpBwdU];
+#pragma unroll
+        for (int u = 0; u < kLpBwdU; ++u) {
+          const int i = i0 + u * NT + threadIdx.x;
+          if (i < nv) x[u] = vec[i];
+        }
+#pragma unroll
+        for (int u = 0; u < kLpBwdU; ++u) {
+          const int i = i0 + u * NT + threadIdx.x;
+          if (i < nv) {
+            float g[N];
+#pragma unroll
+            for (int e = 0; e < N; ++e) g[e] = value(LE::get(x[u], e));
+            const int64_t rel = y - (head + (int64_t)i * N);
+            if (rel >= 0 && rel < N) {
+#pragma unroll
+              for (int e = 0; e < N; ++e)
+                if (e == rel) g[e] = __builtin_fmaf(it, a, g[e]);
+            }
+            dst[i] = LE::pack(g);
+          }
+        }
+      }
+      if (blockIdx.x == 0) {
+        if ((int)threadIdx.x < head) one(threadIdx.x);
+        else if (threadIdx.x >= 32 && tail + (int)threadIdx.x - 32 < V) one(tail + threadIdx.x - 32);
+      }
+    }
   }
+}
+
+struct LpCall {
+  const void* logits;
+  int64_t T;
+  int V;
+  int64_t ld;
+  const int64_t* targets;
+  const float* inv_t;
+  int top_k, parts;
+  float *logprobs, *entropy, *norm;
+  int32_t* top_ids;
+  float* top_lp;
+  uint8_t* ws;
+};
+
+// Parts of a row: with few long rows the chip is filled by splitting them, at
+// the price of a second launch.
+inline int lp_parts(int64_t T, int64_t V) {
+  if (V <= 65536 || T >= 128) return 1;
+  return (int)((V + 16383) / 16384 < 64 ? (V + 16383) / 16384 : 64);
+}
+
+template <typename E, int NT, bool TOP>
+void lp_launch_nt(const LpCall& a, hipStream_t s) {
+  hipLaunchKernelGGL((k_logprob<E, NT, TOP>), dim3((unsigned)(a.T * a.parts)), dim3(NT), 0, s,
+                     (const E*)a.logits, a.V, a.ld, a.targets, a.inv_t, a.top_k, a.parts,
+                     a.logprobs, a.entropy, a.norm, a.top_ids, a.top_lp, a.ws);
+}
+
+template <typename E>
+int lp_launch(const LpCall& a, hipStream_t s) {
+  const bool small = a.V <= 64 * 16 * Lanes<E>::N;  // one chunk of one wave
+  if (a.top_k) {
+    if (small) lp_launch_nt<E, 64, true>(a, s);
+    else lp_launch_nt<E, 256, true>(a, s);
+  } else {
+    if (small) lp_launch_nt<E, 64, false>(a, s);
+    else lp_launch_nt<E, 256, false>(a, s);
+  }
+  if (a.parts > 1)
+    hipLaunchKernelGGL(k_logprob_join<E>, dim3((unsigned)a.T), dim3(64), 0, s,
+                       (const E*)a.logits, a.V, a.ld, a.targets, a.inv_t, a.top_k, a.parts,
+                       a.logprobs, a.entropy, a.norm, a.top_ids, a.top_lp, a.ws);
+  return nv_launch_status();
+}
+
+struct LpGradCall {
+  const void* logits;
+  int64_t T;
+  int V;
+  int64_t ld;
+  const int64_t* targets;
+  const float *inv_t, *norm, *entropy, *g_lp, *g_ent;
+  void* grad;
+  int64_t ldg;
+};
+
+template <typename E, int NT, bool VEC>
+void lp_launch_bwd_nt(const LpGradCall& a, hipStream_t s) {
+  const int64_t per = VEC ? (int64_t)NT * kLpBwdU * Lanes<E>::N : NT;
+  const dim3 grid((unsigned)((a.V + per - 1) / per), (unsigned)(a.T < 65535 ? a.T : 65535));
+  hipLaunchKernelGGL((k_logprob_bwd<E, NT, VEC>), grid, dim3(NT), 0, s, (const E*)a.logits, a.T,
+                     a.V, a.ld, a.targets, a.inv_t, a.norm, a.entropy, a.g_lp, a.g_ent,
+                     (E*)a.grad, a.ldg);
+}
+
+// 16-byte pieces where every row of the gradient starts at the same place of
+// a 16-byte block as its row of logits; single elements otherwise.
+template <typename E>
+int lp_launch_bwd(const LpGradCall& a, hipStream_t s) {
+  const bool vec = ((reinterpret_cast<uintptr_t>(a.logits) ^ reinterpret_cast<uintptr_t>(a.grad)) & 15) == 0 &&
+                   (((a.ld - a.ldg) * (int64_t)sizeof(E)) & 15) == 0;
+  if (!vec) lp_launch_bwd_nt<E, 256, false>(a, s);
+  else if (a.V <= 64 * kLpBwdU * Lanes<E>::N) lp_launch_bwd_nt<E, 64, true>(a, s);
+  else lp_launch_bwd_nt<E, 256, true>(a, s);
+  return nv_launch_status();
 }
 
 }  // namespace
 
 extern "C" {
 
-size_t token_logprobs_workspace_size(int64_t, int64_t, int64_t) { return 256; }
+size_t token_logprobs_workspace_size(int64_t T, int64_t V, int64_t top_k) {
+  if (T < 1 || T > INT32_MAX || V < 1 || V > INT32_MAX || top_k < 0 || top_k > kLpMaxTop) return 256;
+  const int parts = lp_parts(T, V);
+  return parts > 1 ? nv_round256((size_t)T * parts * lp_part_bytes((int)top_k)) : 256;
+}
 
 int token_logprobs(const void* logits, int dtype, int64_t T, int64_t V, int64_t ld,
                    const int64_t* targets, const float* inv_temperature, int64_t top_k,
@@ -177,22 +637,18 @@ int token_logprobs(const void* logits, int dtype, int64_t T, int64_t V, int64_t 
   NV_RETURN_IF(!logits || (targets == nullptr) != (logprobs == nullptr) ||
                    (top_k > 0 && (!top_ids || !top_logprobs)),
                NVFP4_ERR_NULL);
-  NV_RETURN_IF((reinterpret_cast<uintptr_t>(logits) & (dtype == NVFP4_IN_F32 ? 3 : 1)),
+  NV_RETURN_IF((reinterpret_cast<uintptr_t>(logits) & (dtype == NVFP4_IN_F32 ? 3 : 1)) ||
+                   (reinterpret_cast<uintptr_t>(targets) & 7) ||
+                   (reinterpret_cast<uintptr_t>(inv_temperature) & 3),
                NVFP4_ERR_ALIGN);
   NV_RETURN_IF(!ws || ws_bytes < token_logprobs_workspace_size(T, V, top_k) ||
                    (reinterpret_cast<uintptr_t>(ws) & 15),
                NVFP4_ERR_WORKSPACE);
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-  const dim3 grid((unsigned)T);
-  if (dtype == NVFP4_IN_F32)
-    hipLaunchKernelGGL(k_logprob<float>, grid, dim3(256), 0, s, (const float*)logits, (int)V, ld,
-                       targets, inv_temperature, (int)top_k, logprobs, entropy, norm, top_ids,
-                       top_logprobs);
-  else
-    hipLaunchKernelGGL(k_logprob<uint16_t>, grid, dim3(256), 0, s, (const uint16_t*)logits, (int)V,
-                       ld, targets, inv_temperature, (int)top_k, logprobs, entropy, norm, top_ids,
-                       top_logprobs);
-  return nv_launch_status();
+  const LpCall a{logits, T, (int)V, ld, targets, inv_temperature, (int)top_k, lp_parts(T, V),
+                 logprobs, entropy, norm, top_ids, top_logprobs, reinterpret_cast<uint8_t*>(ws)};
+  if (dtype == NVFP4_IN_F32) return lp_launch<float>(a, s);
+  return lp_launch<uint16_t>(a, s);
 }
 
 int token_logprobs_backward(const void* logits, int dtype, int64_t T, int64_t V, int64_t ld,
@@ -210,19 +666,15 @@ int token_logprobs_backward(const void* logits, int dtype, int64_t T, int64_t V,
                NVFP4_ERR_NULL);
   const uintptr_t mask = dtype == NVFP4_IN_F32 ? 3 : 1;
   NV_RETURN_IF((reinterpret_cast<uintptr_t>(logits) & mask) ||
-                   (reinterpret_cast<uintptr_t>(grad_logits) & mask),
+                   (reinterpret_cast<uintptr_t>(grad_logits) & mask) ||
+                   (reinterpret_cast<uintptr_t>(targets) & 7) ||
+                   (reinterpret_cast<uintptr_t>(norm) & 7),
                NVFP4_ERR_ALIGN);
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-  const dim3 grid((unsigned)T);
-  if (dtype == NVFP4_IN_F32)
-    hipLaunchKernelGGL(k_logprob_bwd<float>, grid, dim3(256), 0, s, (const float*)logits, (int)V,
-                       ld, targets, inv_temperature, norm, entropy, grad_logprobs, grad_entropy,
-                       (float*)grad_logits, ldg);
-  else
-    hipLaunchKernelGGL(k_logprob_bwd<uint16_t>, grid, dim3(256), 0, s, (const uint16_t*)logits,
-                       (int)V, ld, targets, inv_temperature, norm, entropy, grad_logprobs,
-                       grad_entropy, (uint16_t*)grad_logits, ldg);
-  return nv_launch_status();
+  const LpGradCall a{logits, T, (int)V, ld, targets, inv_temperature, norm, entropy,
+                     grad_logprobs, grad_entropy, grad_logits, ldg};
+  if (dtype == NVFP4_IN_F32) return lp_launch_bwd<float>(a, s);
+  return lp_launch_bwd<uint16_t>(a, s);
 }
 
 }  // extern "C"
