@@ -470,7 +470,8 @@ int nvfp4_moe_decode(const nvfp4_moe_decode_args_t* args, void* ws, size_t ws_by
  * or both NULL; entropy, norm and inv_temperature are nullable; top_ids and
  * top_logprobs are required if top_k > 0.  inv_temperature must be positive
  * and finite.  Requires 1 <= V < 2^31, 0 <= top_k <= min(V, 32), T < 2^31.
- * Sums are FP32; the result is deterministic.
+ * ws may be NULL where its size is 0.  Sums are FP32; the result is
+ * deterministic.
  *
  * token_logprobs_backward -- the gradient of the logits:
  *   grad[t, j] = inv_temperature[t] * ( a ([j = y] - p_j)

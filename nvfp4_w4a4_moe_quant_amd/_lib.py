@@ -468,31 +468,54 @@ def fp8_grouped_gemm(a: FP8, w: FP8, group_offsets: torch.Tensor, *, N: int, K: 
 
 
 # --------------------------------------------- decode step: layer and tokens
-def _require(cond: bool, what: str):
-    if not cond:
-        raise ValueError(what)
+# These calls take a few microseconds on the GPU, so the host side is kept to
+# plain attribute checks; messages are only built for a call that is refused.
+def _refuse(what: str):
+    raise ValueError(what)
 
 
 def _vector(t: Optional[torch.Tensor], n: int, dtype: torch.dtype, dev, name: str):
-    """A contiguous [n] tensor of one dtype on one device (or None)."""
-    _require(t is None or (t.dtype == dtype and t.shape == (n,) and t.device == dev
-                           and t.is_contiguous()), f"{name}: contiguous {dtype} [{n}] on {dev}")
+    """Address of a contiguous [n] tensor of one dtype on one device (or None)."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.dim() != 1 or t.numel() != n or t.device != dev \
+            or not t.is_contiguous():
+        _refuse(f"{name}: contiguous {dtype} [{n}] on {dev}")
+    return t.data_ptr()
+
+
+def _row_stride(t: torch.Tensor, name: str) -> int:
+    """Row stride of a 2-D tensor whose rows are contiguous and do not overlap."""
+    rows, cols = t.shape
+    if rows <= 1:
+        if rows and cols > 1 and t.stride(1) != 1:
+            _refuse(f"{name}: contiguous rows")
+        return cols + -cols % 8
+    st, one = t.stride()
+    if cols > 1 and one != 1:
+        _refuse(f"{name}: contiguous rows")
+    if st < cols:
+        _refuse(f"{name}: rows overlap")
+    return st
 
 
 def _call(dev: torch.device, fn, *args):
     """Runs fn(*args, stream) with dev current, on its current stream."""
     if torch.cuda.current_device() == dev.index:
-        return _check(fn(*args, torch.cuda.current_stream(dev).cuda_stream))
-    with torch.cuda.device(dev):
-        _check(fn(*args, torch.cuda.current_stream(dev).cuda_stream))
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+    if status:
+        _check(status)
 
 
 def _nvfp4_experts(w: NVFP4, E: int, N: int, K: int, dev, name: str):
     for t, shape, dt in ((w.codes, (E, N, K // 2), torch.uint8),
                          (w.scales, (E, N, K // 16), torch.uint8),
                          (w.tscale, (E,), torch.float32)):
-        _require(t.dtype == dt and t.shape == shape and t.device == dev and t.is_contiguous(),
-                 f"{name}: contiguous {dt} {shape} on {dev}")
+        if t.shape != shape or t.dtype != dt or t.device != dev or not t.is_contiguous():
+            _refuse(f"{name}: contiguous {dt} {shape} on {dev}")
 
 
 def nvfp4_moe_decode(x: torch.Tensor, logits: torch.Tensor, wgu: NVFP4, wd: NVFP4, k: int, *,
@@ -502,45 +525,38 @@ def nvfp4_moe_decode(x: torch.Tensor, logits: torch.Tensor, wgu: NVFP4, wd: NVFP
     activations x [T, H] (bf16 or FP32, row stride honoured) and router logits
     [T, E] (FP32, row stride honoured).  Rows whose logits are all -inf cost
     nothing and give 0."""
-    _require(x.dim() == 2 and logits.dim() == 2 and x.shape[0] == logits.shape[0],
-             "x [T, H] and logits [T, E]")
+    if x.dim() != 2 or logits.dim() != 2 or x.shape[0] != logits.shape[0]:
+        _refuse("x [T, H] and logits [T, E]")
     T, H = x.shape
     E = logits.shape[1]
     dev = x.device
     xd = _dtype_code(x)
-    _require(dev.type == "cuda" and logits.device == dev, "x and logits on one GPU")
-    _require(logits.dtype == torch.float32, "logits are float32")
-    _require(wd.codes.dim() == 3, "wd codes [E, H, I/2]")
+    if dev.type != "cuda" or logits.device != dev:
+        _refuse("x and logits on one GPU")
+    if logits.dtype != torch.float32:
+        _refuse("logits are float32")
+    if wd.codes.dim() != 3:
+        _refuse("wd codes [E, H, I/2]")
     I = wd.codes.shape[2] * 2
     _nvfp4_experts(wgu, E, 2 * I, H, dev, "wgu")
     _nvfp4_experts(wd, E, H, I, dev, "wd")
     if out is None:
         out = torch.empty((T, H), dtype=x.dtype, device=dev)
-    _require(out.shape == x.shape and out.dtype == x.dtype and out.device == dev,
-             "out like x")
+    elif out.shape != x.shape or out.dtype != x.dtype or out.device != dev:
+        _refuse("out like x")
     ids = torch.empty((T, k), dtype=torch.int32, device=dev)
     wts = torch.empty((T, k), dtype=torch.float32, device=dev)
-    ldx, ldl, ldo = (_row_stride(t, n) for t, n in ((x, "x"), (logits, "logits"), (out, "out")))
     args = MoEDecodeArgs(
-        T, E, k, H, I, x.data_ptr(), xd, ldx, logits.data_ptr(), ldl,
+        T, E, k, H, I, x.data_ptr(), xd, _row_stride(x, "x"),
+        logits.data_ptr(), _row_stride(logits, "logits"),
         wgu.codes.data_ptr(), wgu.scales.data_ptr(), wgu.tscale.data_ptr(),
         wd.codes.data_ptr(), wd.scales.data_ptr(), wd.tscale.data_ptr(),
-        out.data_ptr(), ldo, ids.data_ptr(), wts.data_ptr())
+        out.data_ptr(), _row_stride(out, "out"), ids.data_ptr(), wts.data_ptr())
     L = lib()
     ref = ctypes.byref(args)
     ws = _ws(L.nvfp4_moe_decode_workspace_size(ref), dev)
     _call(dev, L.nvfp4_moe_decode, ref, ws.data_ptr(), ws.numel())
     return MoEDecodeOut(out, ids, wts)
-
-
-def _row_stride(t: torch.Tensor, name: str) -> int:
-    """Row stride of a 2-D tensor whose rows are contiguous and do not overlap."""
-    rows, cols = t.shape
-    _require(rows == 0 or cols <= 1 or t.stride(1) == 1, f"{name}: contiguous rows")
-    if rows <= 1:
-        return cols + -cols % 8
-    _require(t.stride(0) >= cols, f"{name}: rows overlap")
-    return t.stride(0)
 
 
 def token_logprobs(logits: torch.Tensor, targets: Optional[torch.Tensor] = None, *,
@@ -549,23 +565,27 @@ def token_logprobs(logits: torch.Tensor, targets: Optional[torch.Tensor] = None,
     entropy and the top_k largest alternatives of each row of logits [T, V]
     (bf16 or FP32, row stride honoured), at a temperature per row
     (inv_temperature, float32 [T]).  Logits of -inf are masked tokens."""
-    _require(logits.dim() == 2, "logits [T, V]")
+    if logits.dim() != 2:
+        _refuse("logits [T, V]")
     T, V = logits.shape
     dev = logits.device
     dt = _dtype_code(logits)
-    _require(dev.type == "cuda", "logits on a GPU")
-    _vector(targets, T, torch.int64, dev, "targets")
-    _vector(inv_temperature, T, torch.float32, dev, "inv_temperature")
+    if dev.type != "cuda":
+        _refuse("logits on a GPU")
+    y = _vector(targets, T, torch.int64, dev, "targets")
+    it = _vector(inv_temperature, T, torch.float32, dev, "inv_temperature")
     lp = torch.empty(T, dtype=torch.float32, device=dev) if targets is not None else None
     ent = torch.empty(T, dtype=torch.float32, device=dev)
     norm = torch.empty((T, 2), dtype=torch.float32, device=dev)
     ids = torch.empty((T, top_k), dtype=torch.int32, device=dev) if top_k > 0 else None
     tlp = torch.empty((T, top_k), dtype=torch.float32, device=dev) if top_k > 0 else None
     L = lib()
-    ws = _ws(L.token_logprobs_workspace_size(T, V, top_k), dev)
+    n = L.token_logprobs_workspace_size(T, V, top_k)
+    ws = _ws(n, dev) if n else None
     _call(dev, L.token_logprobs, logits.data_ptr(), dt, T, V, _row_stride(logits, "logits"),
-          _addr(targets), _addr(inv_temperature), top_k, _addr(lp), ent.data_ptr(),
-          norm.data_ptr(), _addr(ids), _addr(tlp), ws.data_ptr(), ws.numel())
+          y, it, top_k, None if lp is None else lp.data_ptr(), ent.data_ptr(), norm.data_ptr(),
+          None if ids is None else ids.data_ptr(), None if tlp is None else tlp.data_ptr(),
+          None if ws is None else ws.data_ptr(), n)
     return LogprobsOut(lp, ent, norm, ids, tlp)
 
 
@@ -578,27 +598,26 @@ def token_logprobs_backward(logits: torch.Tensor, targets: Optional[torch.Tensor
     """Gradient of the logits from those of token_logprobs's logprobs and
     entropy (either may be None), with its norm and entropy.  out: where to
     write it, which may be logits itself."""
-    _require(logits.dim() == 2, "logits [T, V]")
+    if logits.dim() != 2:
+        _refuse("logits [T, V]")
     T, V = logits.shape
     dev = logits.device
     dt = _dtype_code(logits)
-    _require(dev.type == "cuda", "logits on a GPU")
-    _vector(targets, T, torch.int64, dev, "targets")
-    for t, n in ((inv_temperature, "inv_temperature"), (entropy, "entropy"),
-                 (grad_logprobs, "grad_logprobs"), (grad_entropy, "grad_entropy")):
-        _vector(t, T, torch.float32, dev, n)
-    _require(norm.shape == (T, 2) and norm.dtype == torch.float32 and norm.device == dev
-             and norm.is_contiguous(), "norm: float32 [T, 2]")
+    if dev.type != "cuda":
+        _refuse("logits on a GPU")
+    f32 = torch.float32
+    y = _vector(targets, T, torch.int64, dev, "targets")
+    it = _vector(inv_temperature, T, f32, dev, "inv_temperature")
+    h = _vector(entropy, T, f32, dev, "entropy")
+    ga = _vector(grad_logprobs, T, f32, dev, "grad_logprobs")
+    gb = _vector(grad_entropy, T, f32, dev, "grad_entropy")
+    if norm.shape != (T, 2) or norm.dtype != f32 or norm.device != dev or not norm.is_contiguous():
+        _refuse("norm: float32 [T, 2]")
     if out is None:
         out = torch.empty((T, V), dtype=logits.dtype, device=dev)
-    _require(out.shape == logits.shape and out.dtype == logits.dtype and out.device == dev,
-             "out like logits")
-    ld, ldg = _row_stride(logits, "logits"), _row_stride(out, "out")
-    _call(dev, lib().token_logprobs_backward, logits.data_ptr(), dt, T, V, ld, _addr(targets),
-          _addr(inv_temperature), norm.data_ptr(), _addr(entropy), _addr(grad_logprobs),
-          _addr(grad_entropy), out.data_ptr(), ldg)
+    elif out.shape != logits.shape or out.dtype != logits.dtype or out.device != dev:
+        _refuse("out like logits")
+    _call(dev, lib().token_logprobs_backward, logits.data_ptr(), dt, T, V,
+          _row_stride(logits, "logits"), y, it, norm.data_ptr(), h, ga, gb, out.data_ptr(),
+          _row_stride(out, "out"))
     return out
-
-
-def _addr(t: Optional[torch.Tensor]):
-    return None if t is None else t.data_ptr()

@@ -16,7 +16,10 @@
 namespace {
 
 constexpr int kLpMaxTop = 32;
-constexpr int kLpCand = 1024;  // candidates of a chunk before the ranking
+constexpr int kLpCand = 128;   // candidates that are ranked at a time
+constexpr int kLpPieces = 512; // pieces of a row that wait for the ranking
+constexpr float kLpLowest = -3.402823466e38f;  // masked tokens (-inf) are below it
+constexpr int kLpU = 4;        // 16-byte pieces of a thread in flight, and as many in work
 constexpr int kLpBwdU = 4;     // 16-byte pieces of a thread in the backward pass
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
@@ -63,12 +66,6 @@ __device__ __forceinline__ bool lp_better(float va, int ia, float vb, int ib) {
   return va > vb || (va == vb && ia < ib);
 }
 
-// Hides a piece's origin from the compiler, so that unpacked values of one
-// phase are not kept in registers for the next.
-__device__ __forceinline__ void lp_opaque(uint4& v) {
-  asm volatile("" : "+v"(v.x), "+v"(v.y), "+v"(v.z), "+v"(v.w));
-}
-
 // log p of a logit from the row's maximum m and L = log2 S.
 __device__ __forceinline__ float lp_value(float l, float m, float it, float L) {
   return l == -kInf ? l : __builtin_fmaf(-kLn2, L, (l - m) * it);
@@ -76,8 +73,8 @@ __device__ __forceinline__ float lp_value(float l, float m, float it, float L) {
 
 // (m, S, Q) relative to its own maximum, brought to the maximum M.
 __device__ __forceinline__ void lp_rebase(float m, float M, float c, float& S, float& Q) {
-  const float delta = (m - M) * c;
-  const float f = m == -kInf ? 0.0f : __builtin_amdgcn_exp2f(delta);
+  const float delta = m == -kInf ? -kInf : (m - M) * c;
+  const float f = __builtin_amdgcn_exp2f(delta);
   Q = f > 0.0f ? f * __builtin_fmaf(S, delta, Q) : 0.0f;
   S *= f;  // a NaN stays
 }
@@ -115,23 +112,30 @@ __device__ __forceinline__ float lp_wave_threshold(float v, int k) {
   return f == f ? f : -kInf;  // below the key of -inf
 }
 
+// What the lanes of a wave wrote to LDS before it, all of them read after it.
+__device__ __forceinline__ void lp_wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 struct LpShared {
   float val[kLpMaxTop];  // the best so far, ordered
   int idx[kLpMaxTop];
   int n;                 // how many
-  int cand;              // candidates of this chunk (may exceed the list)
-  float cval[kLpCand];
+  float cval[kLpCand];   // candidates of one wave
   int cidx[kLpCand];
 };
 
-// Merges the first n candidates into the best list (one wave).  Each batch
-// puts the list and 64 - k candidates on the lanes; a lane's rank among them is
-// the number of lanes ahead of it.
-__device__ __forceinline__ void lp_merge(LpShared& sh, int n, int k) {
+// Merges the first n candidates into the best list (one wave).  The list and
+// up to 64 - k candidates lie on the lanes, and a lane's rank is the number
+// of lanes ahead of it: one unsigned comparison of value and inverted index.
+__device__ __forceinline__ void lp_rank(LpShared& sh, int n, int k) {
   const int lane = threadIdx.x & 63;
+  lp_wave_sync();
   int have = sh.n;
   for (int c0 = 0; c0 < n; c0 += 64 - k) {
-    const int take = min(64 - k, n - c0), live = have + take;
+    const int live = have + min(64 - k, n - c0);
     float v = -kInf;
     int i = 0x7fffffff;
     if (lane < have) {
@@ -141,19 +145,78 @@ __device__ __forceinline__ void lp_merge(LpShared& sh, int n, int k) {
       v = sh.cval[c0 + lane - have];
       i = sh.cidx[c0 + lane - have];
     }
+    const uint32_t hi = lp_key(v), lo = ~(uint32_t)i;
+    const uint64_t key = ((uint64_t)hi << 32) | lo;
     int rank = 0;
     for (int o = 0; o < live; ++o) {
-      const float ov = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), o));
-      const int oi = __builtin_amdgcn_readlane(i, o);
-      rank += lp_better(ov, oi, v, i) ? 1 : 0;
+      const uint64_t other = ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)hi, o) << 32) |
+                             (uint32_t)__builtin_amdgcn_readlane((int)lo, o);
+      rank += other > key ? 1 : 0;
     }
+    lp_wave_sync();
     if (lane < live && rank < k) {
       sh.val[rank] = v;
       sh.idx[rank] = i;
     }
+    lp_wave_sync();
     have = min(k, live);
   }
   if (lane == 0) sh.n = have;
+  lp_wave_sync();
+}
+
+// Adds the lanes' kept values to the cnt candidates, ranking those first if
+// the list would not hold them (one wave).  Returns the new count.
+__device__ __forceinline__ int lp_push(LpShared& sh, int cnt, bool keep, float v, int i, int k) {
+  const uint64_t bal = __ballot(keep);
+  const int more = __popcll(bal);
+  if (cnt + more > kLpCand) {
+    lp_rank(sh, cnt, k);
+    cnt = 0;
+  }
+  if (keep) {
+    const int at = cnt + __popcll(bal & ((1ull << (threadIdx.x & 63)) - 1));
+    sh.cval[at] = v;
+    sh.cidx[at] = i;
+  }
+  return cnt + more;
+}
+
+// Pieces in which some logit reaches the bound.
+template <int N>
+struct LpPieces {
+  float v[kLpPieces][N];
+  int id[kLpPieces];  // piece, or -1 - element for a single element in v[0]
+  int n;              // may exceed the list
+};
+
+// Ranks the elements of the first n pieces (one wave).
+template <int N>
+__device__ __forceinline__ void lp_take(LpShared& sh, const LpPieces<N>& pc, int n, int head,
+                                        int k) {
+  const int lane = threadIdx.x & 63;
+  float g = -kInf;
+  for (int c = lane; c < n; c += 64) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) g = __builtin_fmaxf(g, pc.v[c][i]);
+  }
+  float tau = __builtin_fmaxf(lp_wave_threshold(g, k), kLpLowest);
+  if (sh.n == k) tau = __builtin_fmaxf(tau, sh.val[k - 1]);
+  int cnt = 0;
+  for (int c0 = 0; c0 < n; c0 += 64) {
+    const int c = c0 + lane, id = c < n ? pc.id[c] : 0;
+    float v[N], m = -kInf;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      v[i] = c < n ? pc.v[c][i] : -kInf;
+      m = __builtin_fmaxf(m, v[i]);
+    }
+    if (!__ballot(m >= tau)) continue;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      cnt = lp_push(sh, cnt, v[i] >= tau, v[i], id < 0 ? -1 - id : head + id * N + i, k);
+  }
+  lp_rank(sh, cnt, k);
 }
 
 // The best list of a row completed with masked tokens (one wave): fewer than
@@ -171,12 +234,12 @@ __device__ __forceinline__ void lp_fill_masked(LpShared& sh, const E* row, int V
     sh.val[at] = -kInf;
     sh.idx[at] = lane;
   }
+  lp_wave_sync();
 }
 
 // What one workgroup knows of a row, or of a part of one.
 struct LpPart {
-  float m, S, Q;
-  int n;
+  float m, S, Q, pad;
 };
 
 __host__ __device__ inline size_t lp_part_bytes(int top_k) {
@@ -186,8 +249,8 @@ __host__ __device__ inline size_t lp_part_bytes(int top_k) {
 // Writes a row's results (one wave).
 template <typename E>
 __device__ __forceinline__ void lp_finish(LpShared& sh, const E* row, int V, int64_t t, float gm,
-                                          float S, float Q, float it,
-                                          const int64_t* targets, int top_k, float* logprobs,
+                                          float S, float Q, float it, int64_t y, float ly,
+                                          int top_k, float* logprobs,
                                           float* entropy, float* norm, int32_t* top_ids,
                                           float* top_lp) {
   const int lane = threadIdx.x & 63;
@@ -196,10 +259,9 @@ __device__ __forceinline__ void lp_finish(LpShared& sh, const E* row, int V, int
   const float L = empty ? -kInf : __builtin_log2f(S);
   if (lane == 0) {
     if (logprobs) {
-      const int64_t y = targets[t];
       float lp = 0.0f;
       if (y >= V) lp = __builtin_nanf("");
-      else if (y >= 0) lp = S == S ? lp_value(Lanes<E>::load(row + y), m, it, L) : S;
+      else if (y >= 0) lp = S == S ? lp_value(ly, m, it, L) : S;
       logprobs[t] = lp;
     }
     if (entropy) entropy[t] = empty ? 0.0f : (L - Q / S) * kLn2;
@@ -214,15 +276,24 @@ __device__ __forceinline__ void lp_finish(LpShared& sh, const E* row, int V, int
   }
 }
 
-// One workgroup of NT threads per (row, part).  A thread holds U 16-byte
-// pieces of the logits in registers: their maximum is known before the first
-// exponential, so each element costs one exponential and the memory is read
-// once.  The alternatives come from the same registers: the 64 maxima over
-// lanes give a bound that at least top_k elements reach, and the few elements
-// at or above it (and above the worst of the best so far) become candidates;
-// one wave ranks them.  Rows start at any element: the pieces are those that
-// lie wholly inside the row at 16-byte addresses, and the up to N - 1 elements
-// before and after them go one to a thread.
+// The target of a row and its logit, fetched before the row is read.
+template <typename E>
+__device__ __forceinline__ void lp_target(const E* row, int V, const int64_t* targets, int64_t t,
+                                          int64_t& y, float& ly) {
+  y = targets ? targets[t] : -1;
+  ly = y >= 0 && y < V ? Lanes<E>::load(row + y) : 0.0f;
+}
+
+// One workgroup of NT threads per (row, part).  A thread takes U 16-byte
+// pieces at a time into registers, the next ones in flight behind them: their
+// maximum is known before the first exponential, so each element costs one
+// exponential and the memory is read once.  The alternatives come from the
+// same registers: in the first chunk the 64 maxima over lanes give a bound
+// that at least top_k elements reach, later the worst of the best so far is
+// one; the few elements at or above it become candidates, which one wave
+// ranks when there are many.  Rows start at any element: the pieces are those
+// that lie wholly inside the row at 16-byte addresses, and the up to N - 1
+// elements before and after them go one to a thread.
 template <typename E, int NT, bool TOP>
 __global__ __launch_bounds__(NT, 4) void k_logprob(
     const E* __restrict__ logits, int V, int64_t ld, const int64_t* __restrict__ targets,
@@ -230,10 +301,11 @@ __global__ __launch_bounds__(NT, 4) void k_logprob(
     float* __restrict__ entropy, float* __restrict__ norm, int32_t* __restrict__ top_ids,
     float* __restrict__ top_lp, uint8_t* __restrict__ ws) {
   typedef Lanes<E> LE;
-  constexpr int N = LE::N, U = 16, NW = NT / 64;
+  constexpr int N = LE::N, U = kLpU, NW = NT / 64;
   __shared__ float lane_max[TOP ? NW * 64 : 1];
   __shared__ float red[3 * NW];
   __shared__ LpShared sh;
+  __shared__ __attribute__((aligned(16))) LpPieces<N> pc;
   const int64_t t = blockIdx.x / parts;
   const int part = (int)(blockIdx.x % parts);
   const int tid = threadIdx.x, lane = tid & 63;
@@ -245,93 +317,137 @@ __global__ __launch_bounds__(NT, 4) void k_logprob(
   const uint4* vec = reinterpret_cast<const uint4*>(row + head);
   const int per = (nv + parts - 1) / parts, v0 = min(part * per, nv), v1 = min(v0 + per, nv);
 
-  float m = -kInf, S = 0.0f, Q = 0.0f;
-  if (TOP && tid == 0) sh.n = sh.cand = 0;
-  if (TOP) __syncthreads();
-  bool first = true;
-  for (int b = v0; first || b < v1; b += NT * U) {
-    uint4 x[U];
-    float pm[U], tm = -kInf;
+  uint4 x[U];
+  auto fetch = [&](int b) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int i = b + u * NT + tid;
       x[u] = make_uint4(LE::kNone, LE::kNone, LE::kNone, LE::kNone);
       if (i < v1) x[u] = vec[i];
     }
-    // elements outside the pieces, with the first part's first chunk
-    float ev = -kInf;
-    int ei = -1;
-    if (first && part == 0) {
-      if (tid < head) ei = tid;
-      else if (tid >= 32 && tail + tid - 32 < V && tid < 32 + N) ei = tail + tid - 32;
-      if (ei >= 0) ev = LE::load(row + ei);
-    }
-    first = false;
+  };
+  fetch(v0);
+  // elements outside the pieces, with the first part's first chunk
+  float ev = -kInf;
+  int ei = -1;
+  if (part == 0) {
+    if (tid < head) ei = tid;
+    else if (tid >= 32 && tail + tid - 32 < V && tid < 32 + N) ei = tail + tid - 32;
+    if (ei >= 0) ev = LE::load(row + ei);
+  }
+  int64_t y = -1;
+  float ly = 0.0f;
+  if (wave == 0) lp_target(row, V, targets, t, y, ly);
+  if (TOP) {
+    if (tid == 0) sh.n = pc.n = 0;
+    __syncthreads();
+  }
+  float m = -kInf, S = 0.0f, Q = 0.0f;
+  float tau = -kInf;
+  int b = v0, chunk = 0, sync = 8;
+  do {
+    float f[U * N], pm[U], tm = ev;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       float v = -kInf;
-      if (b + u * NT + wave * 64 < v1) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) v = __builtin_fmaxf(v, LE::get(x[u], i));
+      for (int i = 0; i < N; ++i) {
+        f[u * N + i] = LE::get(x[u], i);
+        v = __builtin_fmaxf(v, f[u * N + i]);
       }
       pm[u] = v;
       tm = __builtin_fmaxf(tm, v);
-      lp_opaque(x[u]);
     }
-    tm = __builtin_fmaxf(tm, ev);
+    const int next = b + NT * U;
+    if (next < v1) fetch(next);
     const float M = __builtin_fmaxf(m, tm);
-    if (M > m && m != -kInf) lp_rebase(m, M, c, S, Q);
-    m = M;
+    if (M > m) {
+      if (m != -kInf) lp_rebase(m, M, c, S, Q);
+      m = M;
+    }
     const float ref = m == -kInf ? 0.0f : m;
-    auto add = [&](float l) {
-      const float d = (l - ref) * c;
-      const float e = __builtin_amdgcn_exp2f(d);
-      S += e;
-      Q = __builtin_fmaf(__builtin_fmaxf(d, -1e4f), e, Q);  // 2^-1e4 is 0; no 0 * inf
-    };
+    const float S0 = S, Q0 = Q;
 #pragma unroll
     for (int u = 0; u < U; ++u)
-      if (b + u * NT + wave * 64 < v1) {
+      if (b + u * NT + tid < v1) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) add(LE::get(x[u], i));
-        lp_opaque(x[u]);
+        for (int i = 0; i < N; ++i) {
+          const float d = (f[u * N + i] - ref) * c, e = __builtin_amdgcn_exp2f(d);
+          S += e;
+          Q = __builtin_fmaf(d, e, Q);
+        }
       }
-    if (ei >= 0) add(ev);
+    if (ei >= 0) {
+      const float d = (ev - ref) * c, e = __builtin_amdgcn_exp2f(d);
+      S += e;
+      Q = __builtin_fmaf(d, e, Q);
+    }
+    if (__ballot(Q != Q)) {
+      // masked logits (0 times -inf above) or NaN: again with the factor d
+      // bounded below, where 2^d is 0
+      auto add = [&](float l) {
+        const float d = (l - ref) * c, e = __builtin_amdgcn_exp2f(d);
+        S += e;
+        Q = __builtin_fmaf(__builtin_fmaxf(d, -1e4f), e, Q);
+      };
+      S = S0;
+      Q = Q0;
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (b + u * NT + tid < v1) {
+#pragma unroll
+          for (int i = 0; i < N; ++i) add(f[u * N + i]);
+        }
+      if (ei >= 0) add(ev);
+    }
 
     if constexpr (TOP) {
-      lane_max[wave * 64 + lane] = tm;
-      __syncthreads();
-      float g = -kInf;
+      if (b == v0) {
+        lane_max[wave * 64 + lane] = tm;
+        __syncthreads();
+        float g = -kInf;
 #pragma unroll
-      for (int w = 0; w < NW; ++w) g = __builtin_fmaxf(g, lane_max[w * 64 + lane]);
-      float tau = lp_wave_threshold(g, top_k);
-      if (sh.n == top_k) tau = __builtin_fmaxf(tau, sh.val[top_k - 1]);
-      auto offer = [&](float l, int j) {
-        if (l >= tau && l > -kInf) {
-          const int at = atomicAdd(&sh.cand, 1);
-          if (at < kLpCand) {
-            sh.cval[at] = l;
-            sh.cidx[at] = j;
-          }
+        for (int w = 0; w < NW; ++w) g = __builtin_fmaxf(g, lane_max[w * 64 + lane]);
+        tau = lp_wave_threshold(g, top_k);
+      } else if (sh.n == top_k) {
+        tau = sh.val[top_k - 1];
+      }
+      tau = __builtin_fmaxf(tau, kLpLowest);
+      auto wait = [&](int id, const float* l) {
+        const int at = atomicAdd(&pc.n, 1);
+        if (at < kLpPieces) {
+          pc.id[at] = id;
+#pragma unroll
+          for (int i = 0; i < N; ++i) pc.v[at][i] = l[i];
         }
       };
-      if (__ballot(tm >= tau && tm > -kInf)) {
+      if (__ballot(tm >= tau)) {
 #pragma unroll
         for (int u = 0; u < U; ++u)
-          if (__ballot(pm[u] >= tau && pm[u] > -kInf)) {
+          if (pm[u] >= tau) wait(b + u * NT + tid, f + u * N);
+        if (ev >= tau) {
+          float l[N];
 #pragma unroll
-            for (int i = 0; i < N; ++i)
-              offer(LE::get(x[u], i), head + (b + u * NT + tid) * N + i);
-          }
-        if (ei >= 0) offer(ev, ei);
+          for (int i = 0; i < N; ++i) l[i] = i ? -kInf : ev;
+          wait(-1 - ei, l);
+        }
       }
+    }
+    // The waiting pieces are ranked after the last chunk, and in rows of many
+    // chunks after 8, 64, ..: a bound that some 1.4 top_k of n tokens reach
+    // lets through as many of each further n, and the waves need not wait for
+    // each other in between.
+    ++chunk;
+    if constexpr (TOP) if (chunk == sync || next >= v1) {
+      sync *= 8;
       __syncthreads();
-      const int n = sh.cand;
-      if (n > kLpCand) {
-        // many ties at the bound: top_k rounds of an arg-max over the chunk
+      const int n = pc.n;
+      if (n > kLpPieces) {
+        // more than can wait (ties, rising rows): top_k rounds of an arg-max
+        // over everything read so far
         float pv = kInf;
         int pi = -1;
-        const int j0 = head + b * N, j1 = head + min(b + NT * U, v1) * N;
+        const int j0 = head + v0 * N, j1 = head + min(next, v1) * N;
         for (int k = 0; k < top_k; ++k) {
           float bv = -kInf;
           int bi = 0x7fffffff;
@@ -342,7 +458,11 @@ __global__ __launch_bounds__(NT, 4) void k_logprob(
             }
           };
           for (int j = j0 + tid; j < j1; j += NT) seen(LE::load(row + j), j);
-          if (ei >= 0) seen(ev, ei);
+          if (part == 0) {
+            if (tid < head) seen(LE::load(row + tid), tid);
+            else if (tid >= 32 && tail + tid - 32 < V && tid < 32 + N)
+              seen(LE::load(row + tail + tid - 32), tail + tid - 32);
+          }
 #pragma unroll
           for (int o = 32; o > 0; o >>= 1) {
             const float ov = __shfl_xor(bv, o, 64);
@@ -354,35 +474,40 @@ __global__ __launch_bounds__(NT, 4) void k_logprob(
           }
           __syncthreads();  // the list may still be read
           if (lane == 0) {
-            sh.cval[kLpMaxTop + wave] = bv;
-            sh.cidx[kLpMaxTop + wave] = bi;
+            sh.cval[wave] = bv;
+            sh.cidx[wave] = bi;
           }
           __syncthreads();
           for (int w = 0; w < NW; ++w)
-            if (lp_better(sh.cval[kLpMaxTop + w], sh.cidx[kLpMaxTop + w], bv, bi)) {
-              bv = sh.cval[kLpMaxTop + w];
-              bi = sh.cidx[kLpMaxTop + w];
+            if (lp_better(sh.cval[w], sh.cidx[w], bv, bi)) {
+              bv = sh.cval[w];
+              bi = sh.cidx[w];
             }
           if (tid == 0) {
-            sh.cval[k] = bv;
-            sh.cidx[k] = bi;
+            sh.val[k] = bv;
+            sh.idx[k] = bi;
           }
           pv = bv;
           pi = bi;
         }
-        __syncthreads();
-      }
-      if (wave == 0) {
-        lp_merge(sh, n > kLpCand ? top_k : n, top_k);
-        if (lane == 0) sh.cand = 0;
+        if (tid == 0) {
+          sh.n = top_k;
+          pc.n = 0;
+        }
+      } else if (wave == 0 && n > 0) {
+        lp_take<N>(sh, pc, n, head, top_k);
+        if (lane == 0) pc.n = 0;
       }
       __syncthreads();
     }
-  }
+    ev = -kInf;
+    ei = -1;
+    b = next;
+  } while (b < v1);
 
   // the workgroup's (m, S, Q)
   const float wm = lp_wave_max(m);
-  if (wm > -kInf || S != S) lp_rebase(m, wm, c, S, Q);
+  if (wm > -kInf) lp_rebase(m, wm, c, S, Q);
   S = lp_wave_sum(S);
   Q = lp_wave_sum(Q);
   float gm = wm;
@@ -398,21 +523,21 @@ __global__ __launch_bounds__(NT, 4) void k_logprob(
     S = lane < NW ? red[3 * lane + 1] : 0.0f;
     Q = lane < NW ? red[3 * lane + 2] : 0.0f;
     gm = lp_wave_max(a);
-    if (gm > -kInf || S != S) lp_rebase(a, gm, c, S, Q);
+    if (gm > -kInf) lp_rebase(a, gm, c, S, Q);
     S = lp_wave_sum(S);
     Q = lp_wave_sum(Q);
   }
   if (parts > 1) {
     uint8_t* out = ws + blockIdx.x * lp_part_bytes(TOP ? top_k : 0);
-    if (lane == 0) *reinterpret_cast<LpPart*>(out) = LpPart{gm, S, Q, TOP ? sh.n : 0};
-    if (TOP && lane < sh.n) {
-      reinterpret_cast<float*>(out + sizeof(LpPart))[lane] = sh.val[lane];
+    if (lane == 0) *reinterpret_cast<LpPart*>(out) = LpPart{gm, S, Q};
+    if (TOP && lane < top_k) {
+      reinterpret_cast<float*>(out + sizeof(LpPart))[lane] = lane < sh.n ? sh.val[lane] : -kInf;
       reinterpret_cast<int*>(out + sizeof(LpPart))[top_k + lane] = sh.idx[lane];
     }
     return;
   }
   if (TOP) lp_fill_masked(sh, row, V, top_k);
-  lp_finish<E>(sh, row, V, t, gm, S, Q, it, targets, TOP ? top_k : 0, logprobs, entropy, norm,
+  lp_finish<E>(sh, row, V, t, gm, S, Q, it, y, ly, TOP ? top_k : 0, logprobs, entropy, norm,
                top_ids, top_lp);
 }
 
@@ -430,39 +555,36 @@ __global__ __launch_bounds__(64) void k_logprob_join(
   const float it = inv_t ? inv_t[t] : 1.0f, c = it * kLog2e;
   const size_t step = lp_part_bytes(top_k);
   const uint8_t* in = ws + t * parts * step;
+  int64_t y;
+  float ly;
+  lp_target(row, V, targets, t, y, ly);
   LpPart p{-kInf, 0.0f, 0.0f, 0};  // parts <= 64
   if (lane < parts) p = *reinterpret_cast<const LpPart*>(in + lane * step);
   const float gm = lp_wave_max(p.m);
-  if (gm > -kInf || p.S != p.S) lp_rebase(p.m, gm, c, p.S, p.Q);
+  if (gm > -kInf) lp_rebase(p.m, gm, c, p.S, p.Q);
   const float S = lp_wave_sum(p.S), Q = lp_wave_sum(p.Q);
   if (top_k) {
-    // a bound that top_k of the parts' entries reach: the top_k-th best of
-    // their heads would do for many parts; the lists are short, so all of them
-    // go through the candidates, 64 parts x 32 entries at most
-    int at = p.n;  // exclusive sum over the lanes
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const int v = __shfl_up(at, o, 64);
-      if (lane >= o) at += v;
-    }
-    const int total = __shfl(at, 63, 64);
-    at -= p.n;
     if (lane == 0) sh.n = 0;
-    for (int c0 = 0; c0 < total; c0 += kLpCand) {
-      __syncthreads();
-      const float* val = reinterpret_cast<const float*>(in + lane * step + sizeof(LpPart));
-      for (int i = 0; i < p.n; ++i)
-        if (at + i >= c0 && at + i < c0 + kLpCand) {
-          sh.cval[at + i - c0] = val[i];
-          sh.cidx[at + i - c0] = reinterpret_cast<const int*>(val)[top_k + i];
-        }
-      __syncthreads();
-      lp_merge(sh, min(kLpCand, total - c0), top_k);
+    lp_wave_sync();
+    const int total = parts * top_k;
+    float g = -kInf;
+    auto entry = [&](int c, int& i) -> float {
+      const int q = c / top_k, e = c - q * top_k;
+      const float* val = reinterpret_cast<const float*>(in + q * step + sizeof(LpPart));
+      i = reinterpret_cast<const int*>(val)[top_k + e];
+      return val[e];
+    };
+    int i = 0, cnt = 0;
+    for (int c = lane; c < total; c += 64) g = __builtin_fmaxf(g, entry(c, i));
+    const float tau = __builtin_fmaxf(lp_wave_threshold(g, top_k), kLpLowest);
+    for (int c0 = 0; c0 < total; c0 += 64) {
+      const float v = c0 + lane < total ? entry(c0 + lane, i) : -kInf;
+      cnt = lp_push(sh, cnt, v >= tau, v, i, top_k);
     }
-    __syncthreads();
+    lp_rank(sh, cnt, top_k);
     lp_fill_masked(sh, row, V, top_k);
   }
-  lp_finish<E>(sh, row, V, t, gm, S, Q, it, targets, top_k, logprobs, entropy, norm, top_ids,
+  lp_finish<E>(sh, row, V, t, gm, S, Q, it, y, ly, top_k, logprobs, entropy, norm, top_ids,
                top_lp);
 }
 
@@ -552,11 +674,15 @@ struct LpCall {
   uint8_t* ws;
 };
 
-// Parts of a row: with few long rows the chip is filled by splitting them, at
-// the price of a second launch.
+// Parts of a row.  One row keeps one CU busy for some 10 us per 131072 logits
+// (the exponentials), so few long rows are split over more CUs and joined by a
+// second launch.  Measured with 20 alternatives, bf16, in a graph: 16 x 131072
+// 14.4 us split by four, 17.6 us whole; 1 x 65536 13.1 against 11.1 us; 128 x
+// 131072 20.2 against 17.9 us.
 inline int lp_parts(int64_t T, int64_t V) {
-  if (V <= 65536 || T >= 128) return 1;
-  return (int)((V + 16383) / 16384 < 64 ? (V + 16383) / 16384 : 64);
+  if (T > 64 || V <= 98304) return 1;
+  const int64_t n = (V + 32767) / 32768;
+  return (int)(n < 64 ? n : 64);
 }
 
 template <typename E, int NT, bool TOP>
@@ -568,12 +694,19 @@ void lp_launch_nt(const LpCall& a, hipStream_t s) {
 
 template <typename E>
 int lp_launch(const LpCall& a, hipStream_t s) {
-  const bool small = a.V <= 64 * 16 * Lanes<E>::N;  // one chunk of one wave
+  // One wave where the row is one chunk of it; sixteen where the rows do not
+  // outnumber the CUs (1 x 32768 with 8 alternatives: 8.1 us against 9.6 us
+  // with four); else four, so that several rows share a CU and one row's
+  // loads run behind another's arithmetic.
+  const bool small = a.V <= 64 * kLpU * Lanes<E>::N;
+  const bool wide = !small && a.T * a.parts <= 256;
   if (a.top_k) {
     if (small) lp_launch_nt<E, 64, true>(a, s);
+    else if (wide) lp_launch_nt<E, 1024, true>(a, s);
     else lp_launch_nt<E, 256, true>(a, s);
   } else {
     if (small) lp_launch_nt<E, 64, false>(a, s);
+    else if (wide) lp_launch_nt<E, 1024, false>(a, s);
     else lp_launch_nt<E, 256, false>(a, s);
   }
   if (a.parts > 1)
@@ -620,9 +753,9 @@ int lp_launch_bwd(const LpGradCall& a, hipStream_t s) {
 extern "C" {
 
 size_t token_logprobs_workspace_size(int64_t T, int64_t V, int64_t top_k) {
-  if (T < 1 || T > INT32_MAX || V < 1 || V > INT32_MAX || top_k < 0 || top_k > kLpMaxTop) return 256;
+  if (T < 1 || T > INT32_MAX || V < 1 || V > INT32_MAX || top_k < 0 || top_k > kLpMaxTop) return 0;
   const int parts = lp_parts(T, V);
-  return parts > 1 ? nv_round256((size_t)T * parts * lp_part_bytes((int)top_k)) : 256;
+  return parts > 1 ? nv_round256((size_t)T * parts * lp_part_bytes((int)top_k)) : 0;
 }
 
 int token_logprobs(const void* logits, int dtype, int64_t T, int64_t V, int64_t ld,
@@ -641,8 +774,8 @@ int token_logprobs(const void* logits, int dtype, int64_t T, int64_t V, int64_t 
                    (reinterpret_cast<uintptr_t>(targets) & 7) ||
                    (reinterpret_cast<uintptr_t>(inv_temperature) & 3),
                NVFP4_ERR_ALIGN);
-  NV_RETURN_IF(!ws || ws_bytes < token_logprobs_workspace_size(T, V, top_k) ||
-                   (reinterpret_cast<uintptr_t>(ws) & 15),
+  const size_t need = token_logprobs_workspace_size(T, V, top_k);
+  NV_RETURN_IF((need && !ws) || ws_bytes < need || (reinterpret_cast<uintptr_t>(ws) & 15),
                NVFP4_ERR_WORKSPACE);
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   const LpCall a{logits, T, (int)V, ld, targets, inv_temperature, (int)top_k, lp_parts(T, V),

@@ -245,17 +245,18 @@ class _TokenLogprobs(torch.autograd.Function):
         return r.logprobs, r.entropy
 
     @staticmethod
-    @torch.autograd.function.once_differentiable
     def backward(ctx, g_logprobs, g_entropy):
+        if torch.is_grad_enabled():  # under create_graph
+            raise RuntimeError("token_logprobs has no second derivative")
         logits, targets, inv_temperature, norm, entropy = ctx.saved_tensors
         if g_logprobs is None and g_entropy is None:
             return None, None, None
-        g = L.token_logprobs_backward(
-            logits, targets, norm, entropy,
-            None if g_logprobs is None else g_logprobs.contiguous(),
-            None if g_entropy is None else g_entropy.contiguous(),
-            inv_temperature=inv_temperature)
-        return g, None, None
+        if g_logprobs is not None and not g_logprobs.is_contiguous():
+            g_logprobs = g_logprobs.contiguous()
+        if g_entropy is not None and not g_entropy.is_contiguous():
+            g_entropy = g_entropy.contiguous()
+        return L.token_logprobs_backward(logits, targets, norm, entropy, g_logprobs, g_entropy,
+                                         inv_temperature=inv_temperature), None, None
 
 
 def token_logprobs(logits: torch.Tensor, targets: torch.Tensor,

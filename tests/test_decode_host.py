@@ -71,8 +71,8 @@ def _fwd(lib, logits=FAKE, dtype=1, T=4, V=100, ld=100, y=FAKE, it=None, k=2, lp
     (ESHAPE, dict(k=33)), (ESHAPE, dict(V=3, k=4)), (ENULL, dict(logits=None)),
     (ENULL, dict(y=None)), (ENULL, dict(lp=None)), (ENULL, dict(ids=None)),
     (ENULL, dict(tlp=None)), (EALIGN, dict(logits=FAKE + 1)),
-    (EALIGN, dict(logits=FAKE + 2, dtype=0)), (EWS, dict(ws=None)), (EWS, dict(n=0)),
-    (EWS, dict(ws=MIS)), (OK, dict(T=0, logits=None, y=None, lp=None, ids=None)),
+    (EALIGN, dict(logits=FAKE + 2, dtype=0)), (EWS, dict(ws=None, V=2 ** 20, ld=2 ** 20)),
+    (EWS, dict(n=0, V=2 ** 20, ld=2 ** 20)), (EWS, dict(ws=MIS)), (OK, dict(T=0, logits=None, y=None, lp=None, ids=None)),
 ])
 def test_logprobs_refusals(lib, want, kw):
     assert _fwd(lib, **kw) == want
