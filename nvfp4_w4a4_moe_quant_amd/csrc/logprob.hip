@@ -344,6 +344,7 @@ __global__ __launch_bounds__(NT, 4) void k_logprob(
   }
   float m = -kInf, S = 0.0f, Q = 0.0f;
   float tau = -kInf;
+  bool masked = false;
   int b = v0, chunk = 0, sync = 8;
   do {
     float f[U * N], pm[U], tm = ev;
@@ -366,32 +367,32 @@ __global__ __launch_bounds__(NT, 4) void k_logprob(
       m = M;
     }
     const float ref = m == -kInf ? 0.0f : m;
-    const float S0 = S, Q0 = Q;
+    if (!masked) {
+      const float S0 = S, Q0 = Q;
+      auto add = [&](float l) {
+        const float d = (l - ref) * c, e = __builtin_amdgcn_exp2f(d);
+        S += e;
+        Q = __builtin_fmaf(d, e, Q);
+      };
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (b + u * NT + tid < v1) {
+      for (int u = 0; u < U; ++u)
+        if (b + u * NT + tid < v1) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-          const float d = (f[u * N + i] - ref) * c, e = __builtin_amdgcn_exp2f(d);
-          S += e;
-          Q = __builtin_fmaf(d, e, Q);
+          for (int i = 0; i < N; ++i) add(f[u * N + i]);
         }
-      }
-    if (ei >= 0) {
-      const float d = (ev - ref) * c, e = __builtin_amdgcn_exp2f(d);
-      S += e;
-      Q = __builtin_fmaf(d, e, Q);
+      if (ei >= 0) add(ev);
+      masked = __ballot(Q != Q) != 0;
+      S = masked ? S0 : S;
+      Q = masked ? Q0 : Q;
     }
-    if (__ballot(Q != Q)) {
-      // masked logits (0 times -inf above) or NaN: again with the factor d
-      // bounded below, where 2^d is 0
+    if (masked) {
+      // masked logits (0 times -inf above) or NaN: again, and from here on,
+      // with the factor d bounded below, where 2^d is 0
       auto add = [&](float l) {
         const float d = (l - ref) * c, e = __builtin_amdgcn_exp2f(d);
         S += e;
         Q = __builtin_fmaf(__builtin_fmaxf(d, -1e4f), e, Q);
       };
-      S = S0;
-      Q = Q0;
 #pragma unroll
       for (int u = 0; u < U; ++u)
         if (b + u * NT + tid < v1) {
