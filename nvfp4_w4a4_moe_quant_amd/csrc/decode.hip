@@ -5,14 +5,47 @@
 // of tokens the layer costs the bytes of the routed experts' weights whatever
 // the activations are, so this path multiplies unquantized activations and
 // needs neither the quantizer nor the residual pass.
+//
+//   k_dc_route    one wave per token: top-k, softmax weights (only where the
+//                 gate/up kernel does not route by itself)
+//   k_dc_gate_up  routing (few tokens), then h = silu(g) u of every routed
+//                 (token, slot) pair, FP32 in the workspace
+//   k_dc_down     the down product, weighted and summed over each token's
+//                 experts, to the output
+//
+// Both products stream W once, straight into registers in the layout of
+// v_mfma_f32_16x16x32_f16 (16 tokens x 16 columns): lane (c, q) of a wave
+// takes column c and, of each group of 128 k, the 16 code bytes of k = 32 q ..
+// 32 q + 31 for four MFMA steps of 8 k -- the same permutation of k for both
+// operands.  g * s_b is exact in fp16.  Activations enter as fp16 pieces: a
+// row's values in one K range are scaled by a power of two to just below
+// 2^15, so that one piece holds a bf16 value exactly (down to 2^-29 of the
+// largest) and two hold 22 bits of an FP32 value; the FP32 sums of the range
+// are scaled back.  A wave stages the rows of its K range through a small LDS
+// buffer of its own and keeps the fragments in registers for every column of
+// its work; W loads run two column slabs ahead of their use.
 #include "common.h"
 
 namespace {
+
+typedef _Float16 half8 __attribute__((ext_vector_type(8)));
+typedef _Float16 half2v __attribute__((ext_vector_type(2)));
+typedef float float4v __attribute__((ext_vector_type(4)));
 
 constexpr int kDcMaxT = 64;
 constexpr int kDcMaxE = 1024;
 constexpr int kDcMaxK = 16;
 constexpr int kDcMaxDim = 65536;
+constexpr int kDcMaxPairs = kDcMaxT * kDcMaxK;
+constexpr int kDcMaxTiles = kDcMaxPairs;  // 16-row tiles: at most one per pair
+constexpr int kDcThreads = 256;
+constexpr int kDcWaves = kDcThreads / 64;
+constexpr int kDcInlineT = 8;    // tokens up to which the gate/up kernel routes
+constexpr int kDcInlineE = 256;
+constexpr int kDcRow = 1024 + 16;  // bytes of a staged row: 512 k x 1 piece or 256 k x 2, padded
+constexpr int kDcStageRows = 8;
+constexpr int kDcAcc = 2048;       // output sums of a wave of k_dc_down
+constexpr int kDcMaxParts = 16;
 
 struct DecodeParams {
   int T, E, k, H, I;
@@ -28,111 +61,799 @@ struct DecodeParams {
   int64_t ldo;
   int32_t *user_ids, *ids;  // caller's (nullable), workspace's
   float *user_wts, *wts;
-  float* h;  // [T k, I]
+  float* h;     // [T k, I]
+  float* part;  // [parts, T, H]
+  int32_t* count;  // per column block of k_dc_down
+  int blocks;      // column blocks
 };
 
-__device__ __forceinline__ float dc_logit(float l) { return l != l ? -__builtin_inff() : l; }
+// What the lanes of a wave wrote to LDS before it, all of them read after it.
+__device__ __forceinline__ void dc_wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
 
-// One wave per token: k rounds of a wave arg-max.
-__global__ __launch_bounds__(64) void k_dc_route(DecodeParams p) {
-  const int t = blockIdx.x, lane = threadIdx.x;
+// ---------------------------------------------------------------- routing
+// Float order as unsigned order; a NaN counts as -inf, and 0 is below both.
+__device__ __forceinline__ uint32_t dc_key(float l) {
+  if (l != l) l = -__builtin_inff();
+  const uint32_t u = __float_as_uint(l + 0.0f);  // -0 equals +0
+  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+__device__ __forceinline__ float dc_unkey(uint32_t k) {
+  return __uint_as_float((k & 0x80000000u) ? (k ^ 0x80000000u) : ~k);
+}
+
+// Maximum over the wave: four steps within rows of 16 lanes, then the four
+// rows' values on the scalar unit.
+__device__ __forceinline__ uint32_t dc_wave_max(uint32_t v) {
+  v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0xB1, 0xF, 0xF, false));   // xor 1
+  v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x4E, 0xF, 0xF, false));   // xor 2
+  v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x141, 0xF, 0xF, false));  // half mirror
+  v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x140, 0xF, 0xF, false));  // mirror
+  const uint32_t a = __builtin_amdgcn_readlane((int)v, 0), b = __builtin_amdgcn_readlane((int)v, 16);
+  const uint32_t c = __builtin_amdgcn_readlane((int)v, 32), d = __builtin_amdgcn_readlane((int)v, 48);
+  return max(max(a, b), max(c, d));
+}
+
+// Top-k of token t by one wave, PER logits per lane (E <= 64 PER).  The ids
+// and weights go to sid / swt, and to the workspace and the caller's arrays if
+// `store`.
+template <int PER>
+__device__ __forceinline__ void dc_route_token(const DecodeParams& p, int t, int32_t* sid,
+                                               float* swt, bool store) {
+  const int lane = threadIdx.x & 63;
   const float* row = p.logits + t * p.ldl;
-  float pv = __builtin_inff(), mx = 0.0f, den = 0.0f;
-  int pi = -1;
+  uint32_t key[PER];
+  float l[PER];
+#pragma unroll
+  for (int j = 0; j < PER; ++j) {
+    const int e = lane + 64 * j;
+    l[j] = e < p.E ? row[e] : -__builtin_inff();
+  }
+#pragma unroll
+  for (int j = 0; j < PER; ++j) key[j] = lane + 64 * j < p.E ? dc_key(l[j]) : 0u;
+  uint32_t mx = 0u, mine = 0u;  // lane s keeps the s-th choice
+  int id = 0;
+  float den = 0.0f;
   for (int s = 0; s < p.k; ++s) {
-    float bv = -__builtin_inff();
-    int bi = 0x7fffffff;
-    for (int e = lane; e < p.E; e += 64) {
-      const float l = dc_logit(row[e]);
-      const bool left = pi < 0 || pv > l || (pv == l && pi < e);
-      if (left && (l > bv || (l == bv && e < bi))) {
-        bv = l;
-        bi = e;
-      }
-    }
-    for (int o = 32; o > 0; o >>= 1) {
-      const float ov = __shfl_xor(bv, o, 64);
-      const int oi = __shfl_xor(bi, o, 64);
-      if (ov > bv || (ov == bv && oi < bi)) {
-        bv = ov;
-        bi = oi;
+    uint32_t b = 0u;
+#pragma unroll
+    for (int j = 0; j < PER; ++j) b = max(b, key[j]);
+    b = dc_wave_max(b);
+    int e = 0;
+    bool found = false;
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+      const uint64_t at = __ballot(key[j] == b);
+      if (!found && at) {
+        const int who = __ffsll((unsigned long long)at) - 1;
+        e = 64 * j + who;
+        if (lane == who) key[j] = 0u;
+        found = true;
       }
     }
     if (s == 0) {
-      mx = bv;
-      for (int e = lane; e < p.E; e += 64) den += __expf(dc_logit(row[e]) - mx);
+      mx = b;
+      const float m = dc_unkey(b);
+#pragma unroll
+      for (int j = 0; j < PER; ++j)
+        if (lane + 64 * j < p.E && l[j] == l[j]) den += __expf(l[j] - m);
+#pragma unroll
       for (int o = 32; o > 0; o >>= 1) den += __shfl_xor(den, o, 64);
     }
-    pv = bv;
-    pi = bi;
-    if (lane == 0) {
-      const float w = bv == -__builtin_inff() ? 0.0f : __expf(bv - mx) / den;
-      p.ids[t * p.k + s] = bi;
-      p.wts[t * p.k + s] = w;
-      if (p.user_ids) p.user_ids[t * p.k + s] = bi;
-      if (p.user_wts) p.user_wts[t * p.k + s] = w;
+    if (lane == s) {
+      mine = b;
+      id = e;
+    }
+  }
+  if (lane < p.k) {
+    const float v = dc_unkey(mine);
+    const float w = v == -__builtin_inff() ? 0.0f : __expf(v - dc_unkey(mx)) / den;
+    const int i = t * p.k + lane;
+    if (sid) {
+      sid[i] = id;
+      swt[i] = w;
+    }
+    if (store) {
+      p.ids[i] = id;
+      p.wts[i] = w;
+      if (p.user_ids) p.user_ids[i] = id;
+      if (p.user_wts) p.user_wts[i] = w;
     }
   }
 }
 
-// Dot product of W row (codes, scales) with v over K, spread over a wave.
-template <typename F>
-__device__ __forceinline__ float dc_dot(const uint8_t* codes, const uint8_t* scales, int K, F v) {
-  float acc = 0.0f;
-  for (int k = (threadIdx.x & 63) * 8; k < K; k += 512) {
-    float g[8], s = 0.0f;
-    nv_decode8(*reinterpret_cast<const uint32_t*>(codes + (k >> 1)), g);
+template <int PER>
+__global__ __launch_bounds__(64) void k_dc_route(DecodeParams p) {
+  dc_route_token<PER>(p, blockIdx.x, nullptr, nullptr, true);
+}
+
+// --------------------------------------------------------- rows by expert
+// Every workgroup builds the same tables in LDS: the pairs with a weight, in
+// (expert, token) order, cut into tiles of at most 16 rows of one expert.
+struct DcTables {
+  uint32_t tile[kDcMaxTiles];   // expert << 16 | first row
+  uint16_t pair[kDcMaxPairs];   // row -> (t * k + s) << 6 | t
+  int ntile, nrow;
+  __device__ __forceinline__ int token(int row) const { return pair[row] & 63; }
+  __device__ __forceinline__ int pair_of(int row) const { return pair[row] >> 6; }
+};
+struct DcBuild {  // while building
+  unsigned long long mask[kDcMaxE];  // tokens of an expert
+  uint16_t base[kDcMaxE];            // its first row
+  int wave_rows[kDcWaves], wave_tiles[kDcWaves];
+};
+
+// ids and weights: LDS or the workspace.  row_wt (nullable): each row's weight
+// times its expert's tensor scale ts.
+__device__ __forceinline__ void dc_build(const DecodeParams& p, const int32_t* ids,
+                                         const float* wts, DcTables& tb, DcBuild& bd,
+                                         float* row_wt = nullptr, const float* ts = nullptr) {
+  const int tid = threadIdx.x, P = p.T * p.k;
+  for (int e = tid; e < p.E; e += kDcThreads) bd.mask[e] = 0ull;
+  __syncthreads();
+  int e_of[kDcMaxPairs / kDcThreads];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s = __builtin_fmaf(g[i], v(k + i), s);
-    acc = __builtin_fmaf(s, nv_e4m3_to_f32(scales[k >> 4]), acc);
+  for (int j = 0; j < kDcMaxPairs / kDcThreads; ++j) {
+    const int i = tid + j * kDcThreads;
+    e_of[j] = -1;
+    if (i < P && wts[i] > 0.0f) {
+      e_of[j] = ids[i];
+      atomicOr(&bd.mask[e_of[j]], 1ull << (i / p.k));
+    }
   }
-  for (int o = 32; o > 0; o >>= 1) acc += __shfl_xor(acc, o, 64);
-  return acc;
+  __syncthreads();
+  // thread tid owns experts 4 tid .. 4 tid + 3: rows and tiles, scanned
+  constexpr int kPer = kDcMaxE / kDcThreads;
+  int rows[kPer], mr = 0, mt = 0;
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    const int e = tid * kPer + j;
+    rows[j] = e < p.E ? __popcll(bd.mask[e]) : 0;
+    mr += rows[j];
+    mt += (rows[j] + 15) >> 4;
+  }
+  const int lane = tid & 63, w = tid >> 6;
+  int ir = mr, it = mt;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int a = __shfl_up(ir, o, 64), b = __shfl_up(it, o, 64);
+    if (lane >= o) {
+      ir += a;
+      it += b;
+    }
+  }
+  if (lane == 63) {
+    bd.wave_rows[w] = ir;
+    bd.wave_tiles[w] = it;
+  }
+  __syncthreads();
+  int r = ir - mr, t = it - mt;
+  for (int i = 0; i < w; ++i) {
+    r += bd.wave_rows[i];
+    t += bd.wave_tiles[i];
+  }
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    const int e = tid * kPer + j;
+    if (e < p.E) bd.base[e] = (uint16_t)r;
+    for (int i = 0; i < rows[j]; i += 16) tb.tile[t++] = ((uint32_t)e << 16) | (uint32_t)(r + i);
+    r += rows[j];
+  }
+  if (tid == kDcThreads - 1) {
+    tb.ntile = t;
+    tb.nrow = r;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < kDcMaxPairs / kDcThreads; ++j) {
+    const int i = tid + j * kDcThreads, e = e_of[j];
+    if (e >= 0) {
+      const unsigned long long before = (1ull << (i / p.k)) - 1;
+      const int row = bd.base[e] + __popcll(bd.mask[e] & before);
+      tb.pair[row] = (uint16_t)((i << 6) | (i / p.k));
+      if (row_wt) row_wt[row] = wts[i] * ts[e];
+    }
+  }
+  __syncthreads();
 }
 
-// One wave per (pair, intermediate column).
-template <bool kBf16>
-__global__ __launch_bounds__(256) void k_dc_gate_up(DecodeParams p) {
-  const int pair = blockIdx.y, i = blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (i >= p.I || !(p.wts[pair] > 0.0f)) return;
-  const int e = p.ids[pair];
-  const int64_t row = (int64_t)(pair / p.k) * p.ldx;
-  auto x = [&](int k) -> float {
-    return kBf16 ? nv_bf16_to_f32(reinterpret_cast<const uint16_t*>(p.x)[row + k])
-                 : reinterpret_cast<const float*>(p.x)[row + k];
+// Rows of tile j: until the next tile's first row.
+__device__ __forceinline__ int dc_tile_rows(const DcTables& tb, int j) {
+  const int first = tb.tile[j] & 0xFFFF;
+  const int end = j + 1 < tb.ntile ? (int)(tb.tile[j + 1] & 0xFFFF) : tb.nrow;
+  return end - first;
+}
+
+// ------------------------------------------------------------- products
+// 8 E2M1 codes times an E4M3 scale -> 8 exact fp16 values.
+__device__ __forceinline__ half8 dc_dequant8(uint32_t codes, half2v s2) {
+  half2v p0 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(codes, 1.0f, 0);
+  half2v p1 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(codes, 1.0f, 1);
+  half2v p2 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(codes, 1.0f, 2);
+  half2v p3 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(codes, 1.0f, 3);
+  p0 *= s2;
+  p1 *= s2;
+  p2 *= s2;
+  p3 *= s2;
+  return __builtin_shufflevector(__builtin_shufflevector(p0, p1, 0, 1, 2, 3),
+                                 __builtin_shufflevector(p2, p3, 0, 1, 2, 3), 0, 1, 2, 3, 4,
+                                 5, 6, 7);
+}
+
+// Power of two that brings amax to [2^14, 2^15), and its inverse.  Rows of
+// zeros and of values beyond the FP32 exponent's reach take the nearest.
+__device__ __forceinline__ float dc_row_scale(float amax, float* inv) {
+  int e = (int)((__float_as_uint(amax) >> 23) & 0xFF) - 127;
+  e = e < -106 ? -106 : e;
+  *inv = __uint_as_float((uint32_t)(e - 14 + 127) << 23);
+  return __uint_as_float((uint32_t)(14 - e + 127) << 23);
+}
+
+template <int PIECES>
+struct DcShape {
+  static constexpr int NG = PIECES == 1 ? 4 : 2;  // 128-k groups of a K range
+};
+
+// One K range of a wave: up to NG groups of 128 k from group g.
+template <int PIECES>
+struct DcFrags {
+  half8 a[PIECES][DcShape<PIECES>::NG][4];
+};
+
+// Rows r0 .. r0 + 3 of a tile on the four lane quarters: 16 lanes load a
+// row's values of the K range, 8 consecutive k to a lane.
+template <bool F32, int PIECES>
+struct DcRaw {
+  static constexpr int NL = DcShape<PIECES>::NG;  // 128-k pieces of a row
+  uint4 v[NL][F32 ? 2 : 1];
+};
+// Loads without a branch, so that waits for older loads stay exact: lanes past
+// kend (a multiple of 32) read the last values before it and get zeros.
+template <bool F32, int PIECES>
+__device__ __forceinline__ void dc_fetch_rows(DcRaw<F32, PIECES>& raw, const void* src,
+                                              int64_t row_off, int k0, int kend) {
+  const int l16 = threadIdx.x & 15;
+#pragma unroll
+  for (int j = 0; j < DcRaw<F32, PIECES>::NL; ++j) {
+    const int k = min(k0 + j * 128 + l16 * 8, kend - 8);
+    if constexpr (F32) {
+      const uint4* at = reinterpret_cast<const uint4*>(reinterpret_cast<const float*>(src) + row_off + k);
+      raw.v[j][0] = at[0];
+      raw.v[j][1] = at[1];
+    } else {
+      raw.v[j][0] = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(src) + row_off + k);
+    }
+  }
+}
+
+// Scales the rows and writes their fp16 pieces to the wave's buffer (row
+// `slot` of the quarter) and the inverse scale to inv[slot].
+template <bool F32, int PIECES>
+__device__ __forceinline__ void dc_stage_rows(DcRaw<F32, PIECES>& raw, int k0, int kend,
+                                              uint8_t* buf, float* inv, int slot, int inv_slot) {
+  constexpr int NL = DcRaw<F32, PIECES>::NL;
+  const int l16 = threadIdx.x & 15;
+  auto get = [&](int j, int i) -> float {
+    if constexpr (F32) {
+      const uint4& v = raw.v[j][i >> 2];
+      const int e = i & 3;
+      return __uint_as_float(e == 0 ? v.x : e == 1 ? v.y : e == 2 ? v.z : v.w);
+    } else {
+      const uint4& v = raw.v[j][0];
+      const uint32_t w = i < 2 ? v.x : i < 4 ? v.y : i < 6 ? v.z : v.w;
+      return __uint_as_float((i & 1) ? (w & 0xFFFF0000u) : (w << 16));
+    }
   };
-  float y[2];
-  for (int half = 0; half < 2; ++half) {
-    const int64_t n = (int64_t)e * 2 * p.I + half * p.I + i;
-    y[half] = p.gu_ts[e] * dc_dot(p.gu_codes + n * (p.H >> 1), p.gu_scales + n * (p.H >> 4), p.H, x);
+  if (k0 + NL * 128 > kend) {
+#pragma unroll
+    for (int j = 0; j < NL; ++j)
+      if (k0 + j * 128 + l16 * 8 >= kend) {
+#pragma unroll
+        for (int i = 0; i < (F32 ? 2 : 1); ++i) raw.v[j][i] = make_uint4(0, 0, 0, 0);
+      }
   }
-  if ((threadIdx.x & 63) == 0) p.h[(int64_t)pair * p.I + i] = y[0] / (1.0f + __expf(-y[0])) * y[1];
+  float amax = 0.0f;
+#pragma unroll
+  for (int j = 0; j < NL; ++j)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) amax = __builtin_fmaxf(amax, __builtin_fabsf(get(j, i)));
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) amax = __builtin_fmaxf(amax, __shfl_xor(amax, o, 64));
+  float back;
+  const float s = dc_row_scale(amax, &back);
+#pragma unroll
+  for (int j = 0; j < NL; ++j) {
+    half8 hi, lo;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float v = get(j, i) * s;
+      hi[i] = (_Float16)v;  // nearest even
+      if constexpr (PIECES == 2) lo[i] = (_Float16)(v - (float)hi[i]);
+    }
+    uint8_t* at = buf + slot * kDcRow + j * 256 + l16 * 16;
+    *reinterpret_cast<half8*>(at) = hi;
+    if constexpr (PIECES == 2) *reinterpret_cast<half8*>(at + NL * 256) = lo;
+  }
+  if (l16 == 0) inv[inv_slot] = back;
 }
 
-// One wave per (token, output column).
-template <bool kBf16>
-__global__ __launch_bounds__(256) void k_dc_down(DecodeParams p) {
-  const int t = blockIdx.y, n = blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (n >= p.H) return;
-  float acc = 0.0f;
-  for (int s = 0; s < p.k; ++s) {
-    const int pair = t * p.k + s;
-    const float w = p.wts[pair];
-    if (!(w > 0.0f)) continue;
-    const int e = p.ids[pair];
-    const int64_t r = (int64_t)e * p.H + n;
-    const float* h = p.h + (int64_t)pair * p.I;
-    const float y = dc_dot(p.d_codes + r * (p.I >> 1), p.d_scales + r * (p.I >> 4), p.I,
-                           [&](int k) { return h[k]; });
-    acc += w * (p.d_ts[e] * y);
+// The fragments of a tile's rows in one K range.  `row_off(r)` is the source
+// offset of row r.  raw holds rows 0 .. 3, fetched before.  Rows past the tile
+// are copies of its last one: they only enter sums that nobody reads.
+template <bool F32, int PIECES, typename RowOff>
+__device__ __forceinline__ void dc_fill(DcFrags<PIECES>& fr, DcRaw<F32, PIECES>& raw,
+                                        const void* src, RowOff row_off, int nrows, int k0,
+                                        int kend, uint8_t* buf, float* inv) {
+  constexpr int NG = DcShape<PIECES>::NG;
+  const int lane = threadIdx.x & 63, c = lane & 15, q = lane >> 4;
+  auto rows4 = [&](int r0, int p0, bool fetched) {  // rows r0 .. r0 + 3
+    const int r = r0 + q;
+    if (!fetched) dc_fetch_rows<F32, PIECES>(raw, src, row_off(min(r, nrows - 1)), k0, kend);
+    if (r < nrows) dc_stage_rows<F32, PIECES>(raw, k0, kend, buf, inv, r - p0, r);
+  };
+  auto take = [&](int p0) {
+    dc_wave_sync();
+    const int row = min(c, nrows - 1) - p0;
+    if (row >= 0 && row < kDcStageRows) {
+#pragma unroll
+      for (int pc = 0; pc < PIECES; ++pc)
+#pragma unroll
+        for (int g = 0; g < NG; ++g)
+#pragma unroll
+          for (int st = 0; st < 4; ++st)
+            fr.a[pc][g][st] = *reinterpret_cast<const half8*>(
+                buf + row * kDcRow + pc * NG * 256 + g * 256 + q * 64 + st * 16);
+    }
+    dc_wave_sync();
+  };
+  rows4(0, 0, true);
+  if (nrows > 4) rows4(4, 0, false);
+  take(0);
+  if (nrows > 8) {
+    rows4(8, 8, false);
+    if (nrows > 12) rows4(12, 8, false);
+    take(8);
   }
-  if ((threadIdx.x & 63) == 0) {
-    if (kBf16)
-      reinterpret_cast<uint16_t*>(p.out)[t * p.ldo + n] =
-          acc != acc ? (uint16_t)0x7FC0 : (uint16_t)nv_f32_to_bf16(acc);
-    else
-      reinterpret_cast<float*>(p.out)[t * p.ldo + n] = acc;
+}
+
+// W of one 16-column slab in one K range.  Like the rows, W is loaded without
+// branches: past the end of the work a wave loads its last slab again.
+template <int NG>
+struct DcSlab {
+  uint4 code[NG];
+  uint32_t scale[NG];
+};
+
+// How a wave walks W: lane offsets inside a slab's group of 128 k.  The last
+// group may be short: its lanes stay inside the row (their activations are 0).
+struct DcWalk {
+  int K2, K16, ng;         // bytes of a row of codes and scales, groups
+  uint32_t oc, os, oct, ost;  // lane offsets, and those in the last group
+  __device__ __forceinline__ DcWalk(int K) {
+    const int lane = threadIdx.x & 63, c = lane & 15, q = lane >> 4;
+    K2 = K >> 1;
+    K16 = K >> 4;
+    ng = (K + 127) >> 7;
+    oc = c * K2 + q * 16;
+    os = c * K16 + q * 2;
+    const int dk = min(32 * q, K - 32 - (ng - 1) * 128);
+    oct = c * K2 + (dk >> 1);
+    ost = c * K16 + (dk >> 4);
   }
+  // group g (the i-th of the range) of the slab that starts at W row `row`
+  template <int NG>
+  __device__ __forceinline__ void load(DcSlab<NG>& s, int i, const uint8_t* codes,
+                                       const uint8_t* scales, int64_t row, int g) const {
+    const uint8_t* pc = codes + row * K2 + g * 64;
+    const uint8_t* ps = scales + row * K16 + g * 8;
+    const bool last = g == ng - 1;
+    s.code[i] = *reinterpret_cast<const uint4*>(pc + (last ? oct : oc));
+    s.scale[i] = *reinterpret_cast<const uint16_t*>(ps + (last ? ost : os));
+  }
+};
+
+template <int PIECES, int NG>
+__device__ __forceinline__ void dc_mul(float4v& acc, const DcFrags<PIECES>& fr,
+                                       const DcSlab<NG>& s, int g) {
+  const half2v sc = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(s.scale[g], 1.0f, false);
+  const half2v s0 = __builtin_shufflevector(sc, sc, 0, 0), s1 = __builtin_shufflevector(sc, sc, 1, 1);
+  const uint32_t w[4] = {s.code[g].x, s.code[g].y, s.code[g].z, s.code[g].w};
+#pragma unroll
+  for (int st = 0; st < 4; ++st) {
+    const half8 b = dc_dequant8(w[st], st < 2 ? s0 : s1);
+#pragma unroll
+    for (int pc = 0; pc < PIECES; ++pc)
+      acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(fr.a[pc][g][st], b, acc, 0, 0, 0);
+  }
+}
+
+__device__ __forceinline__ float dc_silu_mul(float g, float u) {
+  return g / (1.0f + __expf(-g)) * u;
+}
+
+// K shares of the four waves (the rest of them share the columns): the most
+// shares among those that pad K the least to whole ranges of NG groups.
+__host__ __device__ inline int dc_k_shares(int K, int NG) {
+  const int ng = (K + 127) / 128;
+  int best = 1, least = (ng + NG - 1) / NG * NG;
+  for (int ks = 2; ks <= kDcWaves; ks *= 2) {
+    const int padded = ((ng + ks - 1) / ks + NG - 1) / NG * NG * ks;
+    if (ng >= ks && padded <= least) {
+      best = ks;
+      least = padded;
+    }
+  }
+  return best;
+}
+
+struct DcGateUpShared {
+  DcTables tb;
+  union {
+    DcBuild bd;
+    struct {
+      uint8_t buf[kDcWaves][kDcStageRows * kDcRow];
+      float4v red[kDcWaves][8][64];
+    };
+  };
+  float inv[kDcWaves][16];
+  int32_t sid[kDcInlineT * kDcMaxK];
+  float swt[kDcInlineT * kDcMaxK];
+};
+
+// Units of (tile, column block): a wave takes NSH / 2 gate slabs and their up
+// slabs over its share of K (ks of KS) and column share (cs of CS).
+template <bool F32, int PIECES, int NSH>
+__device__ __forceinline__ void dc_gate_up(const DecodeParams& p, DcGateUpShared& sh, int KS) {
+  constexpr int NG = DcShape<PIECES>::NG, SPW = NSH / 2;
+  const int lane = threadIdx.x & 63, q = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int ks = wave % KS, cs = wave / KS, CS = kDcWaves / KS;
+  const DcWalk walk(p.H);
+  const int nslab = p.I >> 4, SPU = SPW * CS, nblk = (nslab + SPU - 1) / SPU;
+  const int g0 = walk.ng * ks / KS, g1 = walk.ng * (ks + 1) / KS;
+  const int nph = (g1 - g0 + NG - 1) / NG;
+  const int units = sh.tb.ntile * nblk;
+  const int u0 = (int)((int64_t)units * blockIdx.x / gridDim.x);
+  const int u1 = (int)((int64_t)units * (blockIdx.x + 1) / gridDim.x);
+  if (u0 >= u1) return;
+
+  // where a unit's columns lie: its expert's first W row and the wave's slab
+  struct Pos {
+    int j, blk, n, first, slab;
+    int64_t row;
+  };
+  auto pos = [&](int u) {
+    Pos o;
+    o.j = u / nblk;
+    o.blk = u - o.j * nblk;
+    const uint32_t tile = __builtin_amdgcn_readfirstlane((int)sh.tb.tile[o.j]);
+    o.first = tile & 0xFFFF;
+    o.n = __builtin_amdgcn_readfirstlane(dc_tile_rows(sh.tb, o.j));
+    o.slab = o.blk * SPU + cs * SPW;
+    o.row = (int64_t)(tile >> 16) * 2 * p.I;
+    return o;
+  };
+  DcSlab<NG> w[2];
+  auto load = [&](const Pos& o, int ph, int st, int i) {
+    walk.load<NG>(w[st & 1], i, p.gu_codes, p.gu_scales,
+                  o.row + ((st & 1) ? p.I : 0) + min(o.slab + (st >> 1), nslab - 1) * 16,
+                  min(g0 + ph * NG + i, g1 - 1));
+  };
+  auto row_off = [&](int row) { return (int64_t)sh.tb.token(row) * p.ldx; };
+  DcRaw<F32, PIECES> raw;
+  auto fetch = [&](const Pos& o, int ph) {
+    dc_fetch_rows<F32, PIECES>(raw, p.x, row_off(o.first + min(q, o.n - 1)),
+                               (g0 + ph * NG) * 128, min(g1 * 128, p.H));
+  };
+  DcFrags<PIECES> fr;
+  Pos cur = pos(u0);
+#pragma unroll
+  for (int st = 0; st < 2; ++st)
+#pragma unroll
+    for (int i = 0; i < NG; ++i) load(cur, 0, st, i);
+  fetch(cur, 0);
+  int held = -1;  // tile whose fragments are in registers (one K range only)
+  for (int u = u0; u < u1; ++u) {
+    const Pos next = pos(u + 1 < u1 ? u + 1 : u);
+    const float ts = p.gu_ts[cur.row / (2 * p.I)];
+    float4v tot[NSH];
+#pragma unroll
+    for (int st = 0; st < NSH; ++st) tot[st] = float4v{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int ph = 0; ph < nph; ++ph) {
+      const bool inside = ph + 1 < nph;
+      const Pos& np = inside ? cur : next;
+      const int nph_i = inside ? ph + 1 : 0;
+      if (nph > 1 || held != cur.j)
+        dc_fill<F32, PIECES>(
+            fr, raw, p.x, [&](int r) { return row_off(cur.first + r); }, cur.n,
+            (g0 + ph * NG) * 128, min(g1 * 128, p.H), sh.buf[wave], sh.inv[wave]);
+      held = cur.j;
+      if (nph > 1 || next.j != cur.j) fetch(np, nph_i);
+      const float4v back = *reinterpret_cast<const float4v*>(&sh.inv[wave][4 * q]);
+#pragma unroll
+      for (int st = 0; st < NSH; ++st) {
+        float4v acc = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int i = 0; i < NG; ++i) {
+          dc_mul<PIECES, NG>(acc, fr, w[st & 1], i);
+          // two stages ahead, into the registers just used
+          if (st + 2 < NSH) load(cur, ph, st + 2, i);
+          else load(np, nph_i, st + 2 - NSH, i);
+        }
+        tot[st] += acc * back;
+      }
+    }
+#pragma unroll
+    for (int st = 0; st < NSH; ++st) sh.red[wave][st][lane] = tot[st];
+    __syncthreads();
+    for (int it = threadIdx.x; it < SPU * 64; it += kDcThreads) {
+      const int s = it >> 6, ln = it & 63, w0 = (s / SPW) * KS, st = 2 * (s % SPW);
+      const int slab = cur.blk * SPU + s;
+      if (slab >= nslab) continue;
+      float4v g = sh.red[w0][st][ln], up = sh.red[w0][st + 1][ln];
+      for (int i = 1; i < KS; ++i) {
+        g += sh.red[w0 + i][st][ln];
+        up += sh.red[w0 + i][st + 1][ln];
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = 4 * (ln >> 4) + i;
+        if (r < cur.n)
+          p.h[(int64_t)sh.tb.pair_of(cur.first + r) * p.I + slab * 16 + (ln & 15)] =
+              dc_silu_mul(ts * g[i], ts * up[i]);
+      }
+    }
+    __syncthreads();
+    cur = next;
+  }
+}
+
+template <bool F32, int PIECES, bool ROUTE>
+__global__ __launch_bounds__(kDcThreads, 2) void k_dc_gate_up(DecodeParams p) {
+  __shared__ DcGateUpShared sh;
+  if (blockIdx.x == 0)
+    for (int i = threadIdx.x; i < p.blocks; i += kDcThreads) p.count[i] = 0;
+  if constexpr (ROUTE) {
+    for (int t = threadIdx.x >> 6; t < p.T; t += kDcWaves)
+      dc_route_token<kDcInlineE / 64>(p, t, sh.sid, sh.swt, blockIdx.x == 0);
+    __syncthreads();
+    dc_build(p, sh.sid, sh.swt, sh.tb, sh.bd);
+  } else {
+    dc_build(p, p.ids, p.wts, sh.tb, sh.bd);
+  }
+  const int KS = dc_k_shares(p.H, DcShape<PIECES>::NG), CS = kDcWaves / KS, nslab = p.I >> 4;
+  const int64_t grid = gridDim.x;
+  if ((int64_t)sh.tb.ntile * (nslab / (4 * CS)) >= 2 * grid) dc_gate_up<F32, PIECES, 8>(p, sh, KS);
+  else if ((int64_t)sh.tb.ntile * (nslab / (2 * CS)) >= grid) dc_gate_up<F32, PIECES, 4>(p, sh, KS);
+  else dc_gate_up<F32, PIECES, 2>(p, sh, KS);
+}
+
+// ------------------------------------------------------------------- down
+// A workgroup owns a block of output columns and walks the tiles of its
+// part: W streams without a break, a tile's sums go to the tokens' rows of an
+// LDS accumulator of each wave, and nothing is synchronized until the end.
+// Where the column blocks alone do not fill the chip the tiles are split into
+// parts, and the last workgroup of a block adds the parts in their order.
+struct DcDownShared {
+  DcTables tb;
+  union {
+    DcBuild bd;
+    uint8_t buf[kDcWaves][kDcStageRows * kDcRow];
+  };
+  float inv[kDcWaves][16];
+  float wt[kDcMaxPairs];  // of a row
+  float acc[kDcWaves][kDcAcc];  // [token][NS * 16]
+  int last;
+};
+
+template <int PIECES, int NS, bool BF16>
+__global__ __launch_bounds__(kDcThreads, 2) void k_dc_down(DecodeParams p) {
+  constexpr int NG = DcShape<PIECES>::NG;
+  __shared__ DcDownShared sh;
+  dc_build(p, p.ids, p.wts, sh.tb, sh.bd, sh.wt, p.d_ts);
+  const int lane = threadIdx.x & 63, c = lane & 15, q = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int KS = dc_k_shares(p.I, NG), ks = wave % KS, cs = wave / KS, CS = kDcWaves / KS;
+  const DcWalk walk(p.I);
+  const int nslab = p.H >> 4, SPU = NS * CS, nblk = p.blocks;
+  const int g0 = walk.ng * ks / KS, g1 = walk.ng * (ks + 1) / KS;
+  const int nph = (g1 - g0 + NG - 1) / NG, ntile = sh.tb.ntile;
+  const int parts = max(1, min(min(ntile, kDcMaxParts), (int)gridDim.x / nblk));
+  float* mine = sh.acc[wave];
+
+  for (int id = blockIdx.x; id < nblk * parts; id += gridDim.x) {
+    const int part = id / nblk, blk = id - part * nblk;
+    const int j0 = (int)((int64_t)ntile * part / parts), j1 = (int)((int64_t)ntile * (part + 1) / parts);
+    for (int i = lane; i < p.T * NS * 16; i += 64) mine[i] = 0.0f;
+    struct Pos {
+      int first, n;
+      int64_t row;
+    };
+    auto pos = [&](int j) {
+      Pos o;
+      const uint32_t tile = __builtin_amdgcn_readfirstlane((int)sh.tb.tile[j]);
+      o.first = tile & 0xFFFF;
+      o.n = __builtin_amdgcn_readfirstlane(dc_tile_rows(sh.tb, j));
+      o.row = (int64_t)(tile >> 16) * p.H;
+      return o;
+    };
+    DcSlab<NG> w[2];
+    auto load = [&](const Pos& o, int ph, int st, int i) {
+      walk.load<NG>(w[st & 1], i, p.d_codes, p.d_scales,
+                    o.row + min(blk * SPU + cs * NS + st, nslab - 1) * 16,
+                    min(g0 + ph * NG + i, g1 - 1));
+    };
+    auto row_off = [&](int row) { return (int64_t)sh.tb.pair_of(row) * p.I; };
+    DcRaw<true, PIECES> raw;
+    auto fetch = [&](const Pos& o, int ph) {
+      dc_fetch_rows<true, PIECES>(raw, p.h, row_off(o.first + min(q, o.n - 1)),
+                                  (g0 + ph * NG) * 128, min(g1 * 128, p.I));
+    };
+    DcFrags<PIECES> fr;
+    Pos cur = {0, 0, 0};
+    if (j0 < j1) {
+      cur = pos(j0);
+#pragma unroll
+      for (int st = 0; st < 2; ++st)
+#pragma unroll
+        for (int i = 0; i < NG; ++i) load(cur, 0, st, i);
+      fetch(cur, 0);
+    }
+    for (int j = j0; j < j1; ++j) {
+      const Pos next = pos(j + 1 < j1 ? j + 1 : j);
+      int tok[4];
+      float wt[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = 4 * q + i;
+        tok[i] = r < cur.n ? sh.tb.token(cur.first + r) : -1;
+        wt[i] = r < cur.n ? sh.wt[cur.first + r] : 0.0f;
+      }
+      for (int ph = 0; ph < nph; ++ph) {
+        const bool inside = ph + 1 < nph;
+        const Pos& np = inside ? cur : next;
+        const int nph_i = inside ? ph + 1 : 0;
+        dc_fill<true, PIECES>(
+            fr, raw, p.h, [&](int r) { return row_off(cur.first + r); }, cur.n,
+            (g0 + ph * NG) * 128, min(g1 * 128, p.I), sh.buf[wave], sh.inv[wave]);
+        fetch(np, nph_i);
+        const float4v back = *reinterpret_cast<const float4v*>(&sh.inv[wave][4 * q]);
+  #pragma unroll
+        for (int st = 0; st < NS; ++st) {
+          float4v acc = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+          for (int i = 0; i < NG; ++i) {
+            dc_mul<PIECES, NG>(acc, fr, w[st & 1], i);
+            if (st + 2 < NS) load(cur, ph, st + 2, i);
+            else load(np, nph_i, st + 2 - NS, i);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (tok[i] >= 0) {
+              float* o = mine + tok[i] * (NS * 16) + st * 16 + c;
+              *o = __builtin_fmaf(acc[i], back[i] * wt[i], *o);
+            }
+        }
+      }
+      cur = next;
+    }
+    __syncthreads();
+    // the K shares of each column, in order
+    const int cols = SPU * 16;
+    auto total = [&](int i, int& t, int& col) -> float {
+      t = i / cols;
+      const int b = i - t * cols, w0 = (b / (NS * 16)) * KS;
+      col = blk * cols + b;
+      float s = 0.0f;
+      for (int v = 0; v < KS; ++v)
+        s += sh.acc[w0 + v][t * (NS * 16) + b % (NS * 16)];
+      return s;
+    };
+    auto put = [&](int t, int col, float v) {
+      if constexpr (BF16)
+        reinterpret_cast<__bf16*>(p.out)[t * p.ldo + col] = (__bf16)v;
+      else
+        reinterpret_cast<float*>(p.out)[t * p.ldo + col] = v;
+    };
+    if (parts == 1) {
+      for (int i = threadIdx.x; i < p.T * cols; i += kDcThreads) {
+        int t, col;
+        const float v = total(i, t, col);
+        if (col < p.H) put(t, col, v);
+      }
+    } else {
+      // agent-scope stores go past this XCD's cache; each wave waits for its
+      // own before the workgroup counts itself
+      for (int i = threadIdx.x; i < p.T * cols; i += kDcThreads) {
+        int t, col;
+        const float v = total(i, t, col);
+        if (col < p.H)
+          __hip_atomic_store(p.part + ((int64_t)part * p.T + t) * p.H + col, v, __ATOMIC_RELAXED,
+                             __HIP_MEMORY_SCOPE_AGENT);
+      }
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      __syncthreads();
+      if (threadIdx.x == 0)
+        sh.last = __hip_atomic_fetch_add(p.count + blk, 1, __ATOMIC_ACQ_REL,
+                                         __HIP_MEMORY_SCOPE_AGENT) == parts - 1;
+      __syncthreads();
+      if (sh.last) {
+        for (int i = threadIdx.x; i < p.T * cols; i += kDcThreads) {
+          const int t = i / cols, col = blk * cols + i - t * cols;
+          if (col >= p.H) continue;
+          float v[kDcMaxParts], s = 0.0f;
+#pragma unroll
+          for (int n = 0; n < kDcMaxParts; ++n)
+            v[n] = n < parts ? __hip_atomic_load(p.part + ((int64_t)n * p.T + t) * p.H + col,
+                                                 __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)
+                             : 0.0f;
+#pragma unroll
+          for (int n = 0; n < kDcMaxParts; ++n) s += v[n];
+          put(t, col, s);
+        }
+      }
+    }
+    __syncthreads();  // the accumulators are free again
+  }
+}
+
+constexpr int kDcGrid = 512;  // two workgroups on each of 256 CUs
+
+// Columns of k_dc_down's blocks, in 16-column slabs per wave.
+inline int dc_down_slabs(int64_t T) { return T <= 32 ? 4 : 2; }
+inline int64_t dc_down_blocks(int64_t T, int64_t H, int64_t I, bool f32) {
+  const int ng = f32 ? DcShape<2>::NG : DcShape<1>::NG;
+  const int64_t spu = dc_down_slabs(T) * (kDcWaves / dc_k_shares((int)I, ng));
+  return ((H >> 4) + spu - 1) / spu;
+}
+
+struct DcLayout {
+  size_t ids, wts, count, h, part, bytes;
+};
+inline DcLayout dc_layout(const nvfp4_moe_decode_args_t* a) {
+  const size_t P = (size_t)(a->T * a->k);
+  const int64_t nb = dc_down_blocks(a->T, a->H, a->I, a->x_dtype == NVFP4_IN_F32);
+  const int64_t fill = kDcGrid / nb, parts = fill < 1 ? 1 : fill > kDcMaxParts ? kDcMaxParts : fill;
+  DcLayout l;
+  l.ids = 0;
+  l.wts = l.ids + nv_round256(P * 4);
+  l.count = l.wts + nv_round256(P * 4);
+  l.h = l.count + nv_round256((size_t)nb * 4);
+  l.part = l.h + nv_round256(P * (size_t)a->I * 4);
+  l.bytes = l.part + (parts > 1 ? nv_round256((size_t)parts * a->T * a->H * 4) : 0);
+  return l;
+}
+inline bool dc_shape_ok(const nvfp4_moe_decode_args_t* a) {
+  return a->T >= 0 && a->T <= kDcMaxT && a->E >= 1 && a->E <= kDcMaxE && a->k >= 1 &&
+         a->k <= a->E && a->k <= kDcMaxK && a->H >= 32 && a->H <= kDcMaxDim && a->H % 32 == 0 &&
+         a->I >= 32 && a->I <= kDcMaxDim && a->I % 32 == 0;
+}
+
+template <int PIECES, int NS, bool BF16>
+void dc_launch_down(const DecodeParams& p, hipStream_t s) {
+  static_assert(kDcMaxT * 2 * 16 <= kDcAcc && 32 * 4 * 16 <= kDcAcc, "sums of a wave");
+  hipLaunchKernelGGL((k_dc_down<PIECES, NS, BF16>), dim3(kDcGrid), dim3(kDcThreads), 0, s, p);
+}
+
+template <bool F32>
+void dc_launch(const DecodeParams& p, hipStream_t s) {
+  constexpr int PIECES = F32 ? 2 : 1;
+  const dim3 grid(kDcGrid), wg(kDcThreads);
+  if (p.T <= kDcInlineT && p.E <= kDcInlineE) {
+    hipLaunchKernelGGL((k_dc_gate_up<F32, PIECES, true>), grid, wg, 0, s, p);
+  } else {
+    const dim3 gt((unsigned)p.T);
+    if (p.E <= 64) hipLaunchKernelGGL(k_dc_route<1>, gt, dim3(64), 0, s, p);
+    else if (p.E <= 128) hipLaunchKernelGGL(k_dc_route<2>, gt, dim3(64), 0, s, p);
+    else if (p.E <= 256) hipLaunchKernelGGL(k_dc_route<4>, gt, dim3(64), 0, s, p);
+    else hipLaunchKernelGGL(k_dc_route<16>, gt, dim3(64), 0, s, p);
+    hipLaunchKernelGGL((k_dc_gate_up<F32, PIECES, false>), grid, wg, 0, s, p);
+  }
+  if (dc_down_slabs(p.T) == 4) dc_launch_down<PIECES, 4, !F32>(p, s);
+  else dc_launch_down<PIECES, 2, !F32>(p, s);
 }
 
 }  // namespace
@@ -140,20 +861,13 @@ __global__ __launch_bounds__(256) void k_dc_down(DecodeParams p) {
 extern "C" {
 
 size_t nvfp4_moe_decode_workspace_size(const nvfp4_moe_decode_args_t* a) {
-  if (!a || a->T < 0 || a->T > kDcMaxT || a->k < 1 || a->k > kDcMaxK || a->I < 0 ||
-      a->I > kDcMaxDim)
-    return 0;
-  const size_t P = (size_t)(a->T * a->k);
-  return 2 * nv_round256(P * 4) + nv_round256(P * (size_t)a->I * 4);
+  return a && dc_shape_ok(a) && a->T > 0 ? dc_layout(a).bytes : 0;
 }
 
 int nvfp4_moe_decode(const nvfp4_moe_decode_args_t* a, void* ws, size_t ws_bytes, void* stream) {
   NV_RETURN_IF(!a, NVFP4_ERR_NULL);
   NV_RETURN_IF(a->x_dtype != NVFP4_IN_F32 && a->x_dtype != NVFP4_IN_BF16, NVFP4_ERR_DTYPE);
-  NV_RETURN_IF(a->T < 0 || a->T > kDcMaxT || a->E < 1 || a->E > kDcMaxE || a->k < 1 ||
-                   a->k > a->E || a->k > kDcMaxK || a->H < 32 || a->H > kDcMaxDim || a->H % 32 ||
-                   a->I < 32 || a->I > kDcMaxDim || a->I % 32 || a->ldx < a->H ||
-                   a->ldo < a->H || a->ld_logits < a->E,
+  NV_RETURN_IF(!dc_shape_ok(a) || a->ldx < a->H || a->ldo < a->H || a->ld_logits < a->E,
                NVFP4_ERR_SHAPE);
   if (a->T == 0) return NVFP4_OK;
   NV_RETURN_IF(!a->x || !a->logits || !a->gu_codes || !a->gu_scales || !a->gu_tscale ||
@@ -168,27 +882,20 @@ int nvfp4_moe_decode(const nvfp4_moe_decode_args_t* a, void* ws, size_t ws_bytes
                    (reinterpret_cast<uintptr_t>(a->topk_ids) & 3) ||
                    (reinterpret_cast<uintptr_t>(a->topk_weights) & 3),
                NVFP4_ERR_ALIGN);
-  NV_RETURN_IF(!ws || ws_bytes < nvfp4_moe_decode_workspace_size(a) || !nv_aligned16(ws),
-               NVFP4_ERR_WORKSPACE);
+  const DcLayout l = dc_layout(a);
+  NV_RETURN_IF(!ws || ws_bytes < l.bytes || !nv_aligned16(ws), NVFP4_ERR_WORKSPACE);
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-  const size_t P = (size_t)(a->T * a->k);
   uint8_t* w = reinterpret_cast<uint8_t*>(ws);
-  DecodeParams p{(int)a->T, (int)a->E, (int)a->k, (int)a->H, (int)a->I, a->x, a->ldx,
-                 a->logits, a->ld_logits, a->gu_codes, a->gu_scales, a->gu_tscale,
-                 a->d_codes, a->d_scales, a->d_tscale, a->out, a->ldo,
-                 a->topk_ids, reinterpret_cast<int32_t*>(w),
-                 a->topk_weights, reinterpret_cast<float*>(w + nv_round256(P * 4)),
-                 reinterpret_cast<float*>(w + 2 * nv_round256(P * 4))};
-  const bool bf = a->x_dtype == NVFP4_IN_BF16;
-  const dim3 g1((unsigned)((p.I + 3) / 4), (unsigned)P), g2((unsigned)((p.H + 3) / 4), (unsigned)p.T);
-  hipLaunchKernelGGL(k_dc_route, dim3((unsigned)p.T), dim3(64), 0, s, p);
-  if (bf) {
-    hipLaunchKernelGGL(k_dc_gate_up<true>, g1, dim3(256), 0, s, p);
-    hipLaunchKernelGGL(k_dc_down<true>, g2, dim3(256), 0, s, p);
-  } else {
-    hipLaunchKernelGGL(k_dc_gate_up<false>, g1, dim3(256), 0, s, p);
-    hipLaunchKernelGGL(k_dc_down<false>, g2, dim3(256), 0, s, p);
-  }
+  const DecodeParams p{(int)a->T, (int)a->E, (int)a->k, (int)a->H, (int)a->I, a->x, a->ldx,
+                       a->logits, a->ld_logits, a->gu_codes, a->gu_scales, a->gu_tscale,
+                       a->d_codes, a->d_scales, a->d_tscale, a->out, a->ldo,
+                       a->topk_ids, reinterpret_cast<int32_t*>(w + l.ids),
+                       a->topk_weights, reinterpret_cast<float*>(w + l.wts),
+                       reinterpret_cast<float*>(w + l.h), reinterpret_cast<float*>(w + l.part),
+                       reinterpret_cast<int32_t*>(w + l.count),
+                       (int)dc_down_blocks(a->T, a->H, a->I, a->x_dtype == NVFP4_IN_F32)};
+  if (a->x_dtype == NVFP4_IN_BF16) dc_launch<false>(p, s);
+  else dc_launch<true>(p, s);
   return nv_launch_status();
 }
 
