@@ -419,19 +419,24 @@ __device__ __forceinline__ void dc_fill(DcFrags<PIECES>& fr, DcRaw<F32, PIECES>&
   }
 }
 
-// W of one 16-column slab in one K range.  Like the rows, W is loaded without
-// branches: past the end of the work a wave loads its last slab again.
-template <int NG>
+// W of one 16-column slab in one K range of NG groups.  Like the rows, W is
+// loaded without branches: past the end of the work a wave loads its last
+// slab again, past the end of K its last group (the activations are 0 there).
+// Whole K ranges (WHOLE: K a multiple of 128) take their block scales in one
+// load per slab -- each quarter of the lanes a group's, exchanged in registers
+// when they are used -- because a load costs the cache lines it touches, 16
+// here, however few bytes it takes of them: with one 2-byte load per group the
+// 16-token layer of 256 experts took 748 us.
+template <int NG, bool WHOLE>
 struct DcSlab {
   uint4 code[NG];
-  uint32_t scale[NG];
+  uint32_t scale[WHOLE ? NG / 2 : NG];
 };
 
-// How a wave walks W: lane offsets inside a slab's group of 128 k.  The last
-// group may be short: its lanes stay inside the row (their activations are 0).
+// How a wave walks W: lane offsets inside a slab's group of 128 k.
 struct DcWalk {
   int K2, K16, ng;         // bytes of a row of codes and scales, groups
-  uint32_t oc, os, oct, ost;  // lane offsets, and those in the last group
+  uint32_t oc, os, oct, ost;  // lane offsets, and those in a short last group
   __device__ __forceinline__ DcWalk(int K) {
     const int lane = threadIdx.x & 63, c = lane & 15, q = lane >> 4;
     K2 = K >> 1;
@@ -443,24 +448,72 @@ struct DcWalk {
     oct = c * K2 + (dk >> 1);
     ost = c * K16 + (dk >> 4);
   }
-  // group g (the i-th of the range) of the slab that starts at W row `row`
-  template <int NG>
-  __device__ __forceinline__ void load(DcSlab<NG>& s, int i, const uint8_t* codes,
-                                       const uint8_t* scales, int64_t row, int g) const {
+  // group g, the i-th of the range from g_first, of the slab at W row `row`
+  template <int NG, bool WHOLE>
+  __device__ __forceinline__ void load(DcSlab<NG, WHOLE>& s, int i, const uint8_t* codes,
+                                       const uint8_t* scales, int64_t row, int g,
+                                       int g_first) const {
     const uint8_t* pc = codes + row * K2 + g * 64;
-    const uint8_t* ps = scales + row * K16 + g * 8;
-    const bool last = g == ng - 1;
-    s.code[i] = *reinterpret_cast<const uint4*>(pc + (last ? oct : oc));
-    s.scale[i] = *reinterpret_cast<const uint16_t*>(ps + (last ? ost : os));
+    const uint8_t* ps = scales + row * K16;
+    if constexpr (WHOLE) {
+      s.code[i] = *reinterpret_cast<const uint4*>(pc + oc);
+      if (i == 0) {
+        const int lane = threadIdx.x & 63, c = lane & 15, q = lane >> 4;
+        if constexpr (NG == 4) {
+          const uint2 v = *reinterpret_cast<const uint2*>(
+              ps + (uint32_t)(c * K16 + min((g_first + q) * 8, K16 - 8)));
+          s.scale[0] = v.x;
+          s.scale[1] = v.y;
+        } else {
+          s.scale[0] = *reinterpret_cast<const uint32_t*>(
+              ps + (uint32_t)(c * K16 + min(g_first * 8 + q * 4, K16 - 4)));
+        }
+      }
+    } else {
+      const bool last = g == ng - 1;
+      s.code[i] = *reinterpret_cast<const uint4*>(pc + (last ? oct : oc));
+      s.scale[i] = *reinterpret_cast<const uint16_t*>(ps + g * 8 + (last ? ost : os));
+    }
   }
 };
 
+typedef unsigned dc_uint2 __attribute__((ext_vector_type(2)));
+
+// The lane's two scale bytes (k = 32 q .. 32 q + 31) of each group, in the low
+// half.  WHOLE with four groups: quarter q loaded group q's bytes, two words
+// for lane quarters 0 1 and 2 3.  Swapping the upper half-wave of the first
+// word with the lower one of the second, then odd 16-lane rows of the result
+// with even ones, leaves every row with the pair that holds its own.
+template <int NG, bool WHOLE>
+__device__ __forceinline__ void dc_scales(const DcSlab<NG, WHOLE>& s, uint32_t (&r)[NG]) {
+  const int q = (threadIdx.x & 63) >> 4;
+  const int sh = (q & 1) * 16;
+  if constexpr (!WHOLE) {
+#pragma unroll
+    for (int i = 0; i < NG; ++i) r[i] = s.scale[i];
+  } else if constexpr (NG == 4) {
+    const dc_uint2 h = __builtin_amdgcn_permlane32_swap(s.scale[0], s.scale[1], false, false);
+    const dc_uint2 a = __builtin_amdgcn_permlane16_swap(h[0], h[0], false, false);
+    const dc_uint2 b = __builtin_amdgcn_permlane16_swap(h[1], h[1], false, false);
+    r[0] = a[0] >> sh;
+    r[1] = a[1] >> sh;
+    r[2] = b[0] >> sh;
+    r[3] = b[1] >> sh;
+  } else {  // quarter q loaded half a group: group q / 2, lane quarters 2 (q % 2) and the next
+    const dc_uint2 h = __builtin_amdgcn_permlane32_swap(s.scale[0], s.scale[0], false, false);
+    const dc_uint2 a = __builtin_amdgcn_permlane16_swap(h[0], h[0], false, false);
+    const dc_uint2 b = __builtin_amdgcn_permlane16_swap(h[1], h[1], false, false);
+    r[0] = (q >= 2 ? a[1] : a[0]) >> sh;
+    r[1] = (q >= 2 ? b[1] : b[0]) >> sh;
+  }
+}
+
 template <int PIECES, int NG>
-__device__ __forceinline__ void dc_mul(float4v& acc, const DcFrags<PIECES>& fr,
-                                       const DcSlab<NG>& s, int g) {
-  const half2v sc = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(s.scale[g], 1.0f, false);
+__device__ __forceinline__ void dc_mul(float4v& acc, const DcFrags<PIECES>& fr, const uint4& code,
+                                       uint32_t scale, int g) {
+  const half2v sc = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(scale, 1.0f, false);
   const half2v s0 = __builtin_shufflevector(sc, sc, 0, 0), s1 = __builtin_shufflevector(sc, sc, 1, 1);
-  const uint32_t w[4] = {s.code[g].x, s.code[g].y, s.code[g].z, s.code[g].w};
+  const uint32_t w[4] = {code.x, code.y, code.z, code.w};
 #pragma unroll
   for (int st = 0; st < 4; ++st) {
     const half8 b = dc_dequant8(w[st], st < 2 ? s0 : s1);
@@ -505,7 +558,7 @@ struct DcGateUpShared {
 
 // Units of (tile, column block): a wave takes NSH / 2 gate slabs and their up
 // slabs over its share of K (ks of KS) and column share (cs of CS).
-template <bool F32, int PIECES, int NSH>
+template <bool F32, int PIECES, bool WHOLE, int NSH>
 __device__ __forceinline__ void dc_gate_up(const DecodeParams& p, DcGateUpShared& sh, int KS) {
   constexpr int NG = DcShape<PIECES>::NG, SPW = NSH / 2;
   const int lane = threadIdx.x & 63, q = lane >> 4;
@@ -536,11 +589,11 @@ __device__ __forceinline__ void dc_gate_up(const DecodeParams& p, DcGateUpShared
     o.row = (int64_t)(tile >> 16) * 2 * p.I;
     return o;
   };
-  DcSlab<NG> w[2];
+  DcSlab<NG, WHOLE> w[2];
   auto load = [&](const Pos& o, int ph, int st, int i) {
-    walk.load<NG>(w[st & 1], i, p.gu_codes, p.gu_scales,
+    walk.load<NG, WHOLE>(w[st & 1], i, p.gu_codes, p.gu_scales,
                   o.row + ((st & 1) ? p.I : 0) + min(o.slab + (st >> 1), nslab - 1) * 16,
-                  min(g0 + ph * NG + i, g1 - 1));
+                  min(g0 + ph * NG + i, g1 - 1), g0 + ph * NG);
   };
   auto row_off = [&](int row) { return (int64_t)sh.tb.token(row) * p.ldx; };
   DcRaw<F32, PIECES> raw;
@@ -576,12 +629,15 @@ __device__ __forceinline__ void dc_gate_up(const DecodeParams& p, DcGateUpShared
 #pragma unroll
       for (int st = 0; st < NSH; ++st) {
         float4v acc = {0.0f, 0.0f, 0.0f, 0.0f};
+        uint32_t sc[NG];
+        dc_scales<NG, WHOLE>(w[st & 1], sc);
 #pragma unroll
         for (int i = 0; i < NG; ++i) {
-          dc_mul<PIECES, NG>(acc, fr, w[st & 1], i);
+          dc_mul<PIECES, NG>(acc, fr, w[st & 1].code[i], sc[i], i);
           // two stages ahead, into the registers just used
           if (st + 2 < NSH) load(cur, ph, st + 2, i);
           else load(np, nph_i, st + 2 - NSH, i);
+          __builtin_amdgcn_sched_barrier(0);
         }
         tot[st] += acc * back;
       }
@@ -611,7 +667,7 @@ __device__ __forceinline__ void dc_gate_up(const DecodeParams& p, DcGateUpShared
   }
 }
 
-template <bool F32, int PIECES, bool ROUTE>
+template <bool F32, int PIECES, bool WHOLE, bool ROUTE>
 __global__ __launch_bounds__(kDcThreads, 2) void k_dc_gate_up(DecodeParams p) {
   __shared__ DcGateUpShared sh;
   if (blockIdx.x == 0)
@@ -626,9 +682,9 @@ __global__ __launch_bounds__(kDcThreads, 2) void k_dc_gate_up(DecodeParams p) {
   }
   const int KS = dc_k_shares(p.H, DcShape<PIECES>::NG), CS = kDcWaves / KS, nslab = p.I >> 4;
   const int64_t grid = gridDim.x;
-  if ((int64_t)sh.tb.ntile * (nslab / (4 * CS)) >= 2 * grid) dc_gate_up<F32, PIECES, 8>(p, sh, KS);
-  else if ((int64_t)sh.tb.ntile * (nslab / (2 * CS)) >= grid) dc_gate_up<F32, PIECES, 4>(p, sh, KS);
-  else dc_gate_up<F32, PIECES, 2>(p, sh, KS);
+  if ((int64_t)sh.tb.ntile * (nslab / (4 * CS)) >= 2 * grid) dc_gate_up<F32, PIECES, WHOLE, 8>(p, sh, KS);
+  else if ((int64_t)sh.tb.ntile * (nslab / (2 * CS)) >= grid) dc_gate_up<F32, PIECES, WHOLE, 4>(p, sh, KS);
+  else dc_gate_up<F32, PIECES, WHOLE, 2>(p, sh, KS);
 }
 
 // ------------------------------------------------------------------- down
@@ -649,7 +705,7 @@ struct DcDownShared {
   int last;
 };
 
-template <int PIECES, int NS, bool BF16>
+template <int PIECES, bool WHOLE, int NS, bool BF16>
 __global__ __launch_bounds__(kDcThreads, 2) void k_dc_down(DecodeParams p) {
   constexpr int NG = DcShape<PIECES>::NG;
   __shared__ DcDownShared sh;
@@ -680,11 +736,11 @@ __global__ __launch_bounds__(kDcThreads, 2) void k_dc_down(DecodeParams p) {
       o.row = (int64_t)(tile >> 16) * p.H;
       return o;
     };
-    DcSlab<NG> w[2];
+    DcSlab<NG, WHOLE> w[2];
     auto load = [&](const Pos& o, int ph, int st, int i) {
-      walk.load<NG>(w[st & 1], i, p.d_codes, p.d_scales,
+      walk.load<NG, WHOLE>(w[st & 1], i, p.d_codes, p.d_scales,
                     o.row + min(blk * SPU + cs * NS + st, nslab - 1) * 16,
-                    min(g0 + ph * NG + i, g1 - 1));
+                    min(g0 + ph * NG + i, g1 - 1), g0 + ph * NG);
     };
     auto row_off = [&](int row) { return (int64_t)sh.tb.pair_of(row) * p.I; };
     DcRaw<true, PIECES> raw;
@@ -724,11 +780,14 @@ __global__ __launch_bounds__(kDcThreads, 2) void k_dc_down(DecodeParams p) {
   #pragma unroll
         for (int st = 0; st < NS; ++st) {
           float4v acc = {0.0f, 0.0f, 0.0f, 0.0f};
+          uint32_t sc[NG];
+          dc_scales<NG, WHOLE>(w[st & 1], sc);
 #pragma unroll
           for (int i = 0; i < NG; ++i) {
-            dc_mul<PIECES, NG>(acc, fr, w[st & 1], i);
+            dc_mul<PIECES, NG>(acc, fr, w[st & 1].code[i], sc[i], i);
             if (st + 2 < NS) load(cur, ph, st + 2, i);
             else load(np, nph_i, st + 2 - NS, i);
+            __builtin_amdgcn_sched_barrier(0);
           }
 #pragma unroll
           for (int i = 0; i < 4; ++i)
@@ -832,28 +891,40 @@ inline bool dc_shape_ok(const nvfp4_moe_decode_args_t* a) {
          a->I >= 32 && a->I <= kDcMaxDim && a->I % 32 == 0;
 }
 
-template <int PIECES, int NS, bool BF16>
+template <bool F32, bool WHOLE, int NS>
 void dc_launch_down(const DecodeParams& p, hipStream_t s) {
   static_assert(kDcMaxT * 2 * 16 <= kDcAcc && 32 * 4 * 16 <= kDcAcc, "sums of a wave");
-  hipLaunchKernelGGL((k_dc_down<PIECES, NS, BF16>), dim3(kDcGrid), dim3(kDcThreads), 0, s, p);
+  hipLaunchKernelGGL((k_dc_down<F32 ? 2 : 1, WHOLE, NS, !F32>), dim3(kDcGrid), dim3(kDcThreads), 0,
+                     s, p);
+}
+
+template <bool F32, bool WHOLE>
+void dc_launch_gate_up(const DecodeParams& p, hipStream_t s) {
+  const dim3 grid(kDcGrid), wg(kDcThreads);
+  if (p.T <= kDcInlineT && p.E <= kDcInlineE) {
+    hipLaunchKernelGGL((k_dc_gate_up<F32, F32 ? 2 : 1, WHOLE, true>), grid, wg, 0, s, p);
+    return;
+  }
+  const dim3 gt((unsigned)p.T);
+  if (p.E <= 64) hipLaunchKernelGGL(k_dc_route<1>, gt, dim3(64), 0, s, p);
+  else if (p.E <= 128) hipLaunchKernelGGL(k_dc_route<2>, gt, dim3(64), 0, s, p);
+  else if (p.E <= 256) hipLaunchKernelGGL(k_dc_route<4>, gt, dim3(64), 0, s, p);
+  else hipLaunchKernelGGL(k_dc_route<16>, gt, dim3(64), 0, s, p);
+  hipLaunchKernelGGL((k_dc_gate_up<F32, F32 ? 2 : 1, WHOLE, false>), grid, wg, 0, s, p);
 }
 
 template <bool F32>
 void dc_launch(const DecodeParams& p, hipStream_t s) {
-  constexpr int PIECES = F32 ? 2 : 1;
-  const dim3 grid(kDcGrid), wg(kDcThreads);
-  if (p.T <= kDcInlineT && p.E <= kDcInlineE) {
-    hipLaunchKernelGGL((k_dc_gate_up<F32, PIECES, true>), grid, wg, 0, s, p);
+  if (p.H % 128 == 0) dc_launch_gate_up<F32, true>(p, s);
+  else dc_launch_gate_up<F32, false>(p, s);
+  const bool whole = p.I % 128 == 0;
+  if (dc_down_slabs(p.T) == 4) {
+    if (whole) dc_launch_down<F32, true, 4>(p, s);
+    else dc_launch_down<F32, false, 4>(p, s);
   } else {
-    const dim3 gt((unsigned)p.T);
-    if (p.E <= 64) hipLaunchKernelGGL(k_dc_route<1>, gt, dim3(64), 0, s, p);
-    else if (p.E <= 128) hipLaunchKernelGGL(k_dc_route<2>, gt, dim3(64), 0, s, p);
-    else if (p.E <= 256) hipLaunchKernelGGL(k_dc_route<4>, gt, dim3(64), 0, s, p);
-    else hipLaunchKernelGGL(k_dc_route<16>, gt, dim3(64), 0, s, p);
-    hipLaunchKernelGGL((k_dc_gate_up<F32, PIECES, false>), grid, wg, 0, s, p);
+    if (whole) dc_launch_down<F32, true, 2>(p, s);
+    else dc_launch_down<F32, false, 2>(p, s);
   }
-  if (dc_down_slabs(p.T) == 4) dc_launch_down<PIECES, 4, !F32>(p, s);
-  else dc_launch_down<PIECES, 2, !F32>(p, s);
 }
 
 }  // namespace
