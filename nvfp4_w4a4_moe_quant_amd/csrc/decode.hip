@@ -46,6 +46,7 @@ constexpr int kDcRow = 1024 + 16;  // bytes of a staged row: 512 k x 1 piece or 
 constexpr int kDcStageRows = 8;
 constexpr int kDcAcc = 2048;       // output sums of a wave of k_dc_down
 constexpr int kDcMaxParts = 16;
+__host__ __device__ inline int dc_pad(int I) { return (I + 127) & ~127; }
 
 struct DecodeParams {
   int T, E, k, H, I;
@@ -61,7 +62,10 @@ struct DecodeParams {
   int64_t ldo;
   int32_t *user_ids, *ids;  // caller's (nullable), workspace's
   float *user_wts, *wts;
-  float* h;     // [T k, I]
+  // h of a pair as fp16 pieces [T k, pieces, Ip] and an exponent byte per 16
+  // columns [T k, Ip / 16]; Ip is I rounded up to whole groups of 128
+  uint16_t* h;
+  uint8_t* hexp;
   float* part;  // [parts, T, H]
   int32_t* count;  // per column block of k_dc_down
   int blocks;      // column blocks
@@ -192,6 +196,21 @@ __device__ __forceinline__ void dc_build(const DecodeParams& p, const int32_t* i
                                          const float* wts, DcTables& tb, DcBuild& bd,
                                          float* row_wt = nullptr, const float* ts = nullptr) {
   const int tid = threadIdx.x, P = p.T * p.k;
+  if (p.T == 1) {  // a row and a tile for each slot, in slot order
+    if (tid < 64) {
+      const bool on = tid < P && wts[tid] > 0.0f;
+      const uint64_t bal = __ballot(on);
+      if (on) {
+        const int row = __popcll(bal & ((1ull << tid) - 1)), e = ids[tid];
+        tb.tile[row] = ((uint32_t)e << 16) | (uint32_t)row;
+        tb.pair[row] = (uint16_t)(tid << 6);
+        if (row_wt) row_wt[row] = wts[tid] * ts[e];
+      }
+      if (tid == 0) tb.ntile = tb.nrow = __popcll(bal);
+    }
+    __syncthreads();
+    return;
+  }
   for (int e = tid; e < p.E; e += kDcThreads) bd.mask[e] = 0ull;
   __syncthreads();
   int e_of[kDcMaxPairs / kDcThreads];
@@ -285,9 +304,12 @@ __device__ __forceinline__ half8 dc_dequant8(uint32_t codes, half2v s2) {
 
 // Power of two that brings amax to [2^14, 2^15), and its inverse.  Rows of
 // zeros and of values beyond the FP32 exponent's reach take the nearest.
+__device__ __forceinline__ int dc_exponent(float amax) {
+  const int e = (int)((__float_as_uint(amax) >> 23) & 0xFF) - 127;
+  return e < -106 ? -106 : e;
+}
 __device__ __forceinline__ float dc_row_scale(float amax, float* inv) {
-  int e = (int)((__float_as_uint(amax) >> 23) & 0xFF) - 127;
-  e = e < -106 ? -106 : e;
+  const int e = dc_exponent(amax);
   *inv = __uint_as_float((uint32_t)(e - 14 + 127) << 23);
   return __uint_as_float((uint32_t)(14 - e + 127) << 23);
 }
@@ -569,13 +591,14 @@ __device__ __forceinline__ void dc_gate_up(const DecodeParams& p, DcGateUpShared
   const int g0 = walk.ng * ks / KS, g1 = walk.ng * (ks + 1) / KS;
   const int nph = (g1 - g0 + NG - 1) / NG;
   const int units = sh.tb.ntile * nblk;
+  const int Ip = dc_pad(p.I);
   const int u0 = (int)((int64_t)units * blockIdx.x / gridDim.x);
   const int u1 = (int)((int64_t)units * (blockIdx.x + 1) / gridDim.x);
   if (u0 >= u1) return;
 
   // where a unit's columns lie: its expert's first W row and the wave's slab
   struct Pos {
-    int j, blk, n, first, slab;
+    int j, blk, n, first, slab, e;
     int64_t row;
   };
   auto pos = [&](int u) {
@@ -586,7 +609,8 @@ __device__ __forceinline__ void dc_gate_up(const DecodeParams& p, DcGateUpShared
     o.first = tile & 0xFFFF;
     o.n = __builtin_amdgcn_readfirstlane(dc_tile_rows(sh.tb, o.j));
     o.slab = o.blk * SPU + cs * SPW;
-    o.row = (int64_t)(tile >> 16) * 2 * p.I;
+    o.e = tile >> 16;
+    o.row = (int64_t)o.e * 2 * p.I;
     return o;
   };
   DcSlab<NG, WHOLE> w[2];
@@ -603,15 +627,15 @@ __device__ __forceinline__ void dc_gate_up(const DecodeParams& p, DcGateUpShared
   };
   DcFrags<PIECES> fr;
   Pos cur = pos(u0);
+  fetch(cur, 0);  // before W: loads return in order
 #pragma unroll
   for (int st = 0; st < 2; ++st)
 #pragma unroll
     for (int i = 0; i < NG; ++i) load(cur, 0, st, i);
-  fetch(cur, 0);
   int held = -1;  // tile whose fragments are in registers (one K range only)
   for (int u = u0; u < u1; ++u) {
     const Pos next = pos(u + 1 < u1 ? u + 1 : u);
-    const float ts = p.gu_ts[cur.row / (2 * p.I)];
+    const float ts = p.gu_ts[cur.e];
     float4v tot[NSH];
 #pragma unroll
     for (int st = 0; st < NSH; ++st) tot[st] = float4v{0.0f, 0.0f, 0.0f, 0.0f};
@@ -654,12 +678,34 @@ __device__ __forceinline__ void dc_gate_up(const DecodeParams& p, DcGateUpShared
         g += sh.red[w0 + i][st][ln];
         up += sh.red[w0 + i][st + 1][ln];
       }
+      // fp16 pieces scaled by the row's largest of these 16 columns, at the
+      // place where k_dc_down's lane quarter and step find them
+      const int k = slab * 16 + (ln & 15);
+      const int at = (k & ~127) + ((k >> 3) & 3) * 32 + ((k >> 5) & 3) * 8 + (k & 7);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int r = 4 * (ln >> 4) + i;
-        if (r < cur.n)
-          p.h[(int64_t)sh.tb.pair_of(cur.first + r) * p.I + slab * 16 + (ln & 15)] =
-              dc_silu_mul(ts * g[i], ts * up[i]);
+        const float h = dc_silu_mul(ts * g[i], ts * up[i]);
+        float amax = __builtin_fabsf(h);
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) amax = __builtin_fmaxf(amax, __shfl_xor(amax, o, 64));
+        if (r >= cur.n) continue;
+        const int pair = sh.tb.pair_of(cur.first + r), e = dc_exponent(amax);
+        const float v = h * __uint_as_float((uint32_t)(14 - e + 127) << 23);
+        const _Float16 hi = (_Float16)v;
+        uint16_t* out = p.h + (int64_t)pair * PIECES * Ip + at;
+        out[0] = __builtin_bit_cast(uint16_t, hi);
+        if constexpr (PIECES == 2) out[Ip] = __builtin_bit_cast(uint16_t, (_Float16)(v - (float)hi));
+        if ((ln & 15) == 0) p.hexp[(int64_t)pair * (Ip >> 4) + slab] = (uint8_t)(e + 128);
+        if (slab == nslab - 1) {  // zeros behind I, for the lanes that read them
+          for (int z = p.I + (ln & 15); z < Ip; z += 16) {
+            const int zat = (z & ~127) + ((z >> 3) & 3) * 32 + ((z >> 5) & 3) * 8 + (z & 7);
+            uint16_t* zo = p.h + (int64_t)pair * PIECES * Ip + zat;
+            zo[0] = 0;
+            if constexpr (PIECES == 2) zo[Ip] = 0;
+            if ((ln & 15) == 0) p.hexp[(int64_t)pair * (Ip >> 4) + (z >> 4)] = 0;
+          }
+        }
       }
     }
     __syncthreads();
@@ -695,11 +741,7 @@ __global__ __launch_bounds__(kDcThreads, 2) void k_dc_gate_up(DecodeParams p) {
 // parts, and the last workgroup of a block adds the parts in their order.
 struct DcDownShared {
   DcTables tb;
-  union {
-    DcBuild bd;
-    uint8_t buf[kDcWaves][kDcStageRows * kDcRow];
-  };
-  float inv[kDcWaves][16];
+  DcBuild bd;
   float wt[kDcMaxPairs];  // of a row
   float acc[kDcWaves][kDcAcc];  // [token][NS * 16]
   int last;
@@ -719,6 +761,7 @@ __global__ __launch_bounds__(kDcThreads, 2) void k_dc_down(DecodeParams p) {
   const int nph = (g1 - g0 + NG - 1) / NG, ntile = sh.tb.ntile;
   const int parts = max(1, min(min(ntile, kDcMaxParts), (int)gridDim.x / nblk));
   float* mine = sh.acc[wave];
+  const int Ip = dc_pad(p.I);
 
   for (int id = blockIdx.x; id < nblk * parts; id += gridDim.x) {
     const int part = id / nblk, blk = id - part * nblk;
@@ -742,62 +785,141 @@ __global__ __launch_bounds__(kDcThreads, 2) void k_dc_down(DecodeParams p) {
                     o.row + min(blk * SPU + cs * NS + st, nslab - 1) * 16,
                     min(g0 + ph * NG + i, g1 - 1), g0 + ph * NG);
     };
-    auto row_off = [&](int row) { return (int64_t)sh.tb.pair_of(row) * p.I; };
-    DcRaw<true, PIECES> raw;
-    auto fetch = [&](const Pos& o, int ph) {
-      dc_fetch_rows<true, PIECES>(raw, p.h, row_off(o.first + min(q, o.n - 1)),
-                                  (g0 + ph * NG) * 128, min(g1 * 128, p.I));
+    // Rows of the tile: lane (c, q) takes row c (rows past the tile are copies
+    // of its last one, whose sums nobody reads), quarter q also the exponent
+    // bytes of group q, as the block scales of W.
+    struct Rows {
+      DcFrags<PIECES> fr;
+      DcSlab<NG, true> exps;
     };
-    DcFrags<PIECES> fr;
+    auto fetch = [&](Rows& rw, const Pos& o, int ph) {
+      const int pair = sh.tb.pair_of(o.first + min(c, o.n - 1)), gf = g0 + ph * NG;
+      const uint16_t* row = p.h + (int64_t)pair * PIECES * Ip + q * 8;
+      const uint8_t* ex = p.hexp + (int64_t)pair * (Ip >> 4);
+      if constexpr (NG == 4) {
+        const uint2 v = *reinterpret_cast<const uint2*>(ex + min(gf + q, g1 - 1) * 8);
+        rw.exps.scale[0] = v.x;
+        rw.exps.scale[1] = v.y;
+      } else {
+        rw.exps.scale[0] = *reinterpret_cast<const uint32_t*>(ex + min(gf + (q >> 1), g1 - 1) * 8 + (q & 1) * 4);
+      }
+#pragma unroll
+      for (int g = 0; g < NG; ++g)
+#pragma unroll
+        for (int pc = 0; pc < PIECES; ++pc)
+#pragma unroll
+          for (int st = 0; st < 4; ++st)
+            rw.fr.a[pc][g][st] = *reinterpret_cast<const half8*>(
+                row + pc * Ip + min(gf + g, g1 - 1) * 128 + st * 32);
+    };
+    auto scale_group = [&](Rows& rw, int g, uint32_t f0, uint32_t f1) {
+      const half2v lo = __builtin_bit_cast(half2v, f0 | (f0 << 16));
+      const half2v hi = __builtin_bit_cast(half2v, f1 | (f1 << 16));
+      const half8 a0 = __builtin_shufflevector(lo, lo, 0, 1, 0, 1, 0, 1, 0, 1);
+      const half8 a1 = __builtin_shufflevector(hi, hi, 0, 1, 0, 1, 0, 1, 0, 1);
+#pragma unroll
+      for (int pc = 0; pc < PIECES; ++pc)
+#pragma unroll
+        for (int st = 0; st < 4; ++st) rw.fr.a[pc][g][st] *= st < 2 ? a0 : a1;
+    };
+    // Brings the row to one exponent in this K range (the largest of its
+    // bytes) and groups past the wave's share to zero; returns the inverse
+    // scale of the lane's four result rows.
+    auto settle = [&](Rows& rw, int left) -> float4v {
+      uint32_t b[NG];
+      dc_scales<NG, true>(rw.exps, b);
+      uint32_t top = 0;
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        b[g] = g < left ? b[g] & 0xFFFFu : 0u;
+        top = max(top, max(b[g] & 0xFFu, b[g] >> 8));
+      }
+      top = max(top, (uint32_t)__shfl_xor((int)top, 16, 64));
+      top = max(top, (uint32_t)__shfl_xor((int)top, 32, 64));
+      // 2^(e - top) in a normal factor of at least 2^-14, and in rows of more
+      // than that range a second one, 0 for what is below 2^-38 of the largest
+      int below = 0;
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        const int d0 = (int)top - (int)(b[g] & 0xFFu), d1 = (int)top - (int)(b[g] >> 8);
+        const uint32_t f0 = g < left ? (uint32_t)(15 - min(d0, 14)) << 10 : 0u;
+        const uint32_t f1 = g < left ? (uint32_t)(15 - min(d1, 14)) << 10 : 0u;
+        if (g < left) below = max(below, max(d0, d1));
+        scale_group(rw, g, f0, f1);
+      }
+      if (__ballot(below > 14)) {
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+          const int d0 = (int)top - (int)(b[g] & 0xFFu) - 14, d1 = (int)top - (int)(b[g] >> 8) - 14;
+          auto more = [&](int d) -> uint32_t {
+            return d <= 0 ? 15u << 10 : d <= 14 ? (uint32_t)(15 - d) << 10 : d <= 24 ? 1u << (24 - d) : 0u;
+          };
+          scale_group(rw, g, more(d0), more(d1));
+        }
+      }
+      float4v back;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int e = max(__shfl((int)top, 4 * q + i, 64), 22);
+        back[i] = __uint_as_float((uint32_t)(e - 128 - 14 + 127) << 23);
+      }
+      return back;
+    };
+
+    Rows ra, rb;
     Pos cur = {0, 0, 0};
-    if (j0 < j1) {
-      cur = pos(j0);
-#pragma unroll
-      for (int st = 0; st < 2; ++st)
-#pragma unroll
-        for (int i = 0; i < NG; ++i) load(cur, 0, st, i);
-      fetch(cur, 0);
-    }
-    for (int j = j0; j < j1; ++j) {
-      const Pos next = pos(j + 1 < j1 ? j + 1 : j);
+    int j = j0, ph = 0;
+    // one K range of one tile: rows in `rw`, the next ones go to `nx`
+    auto step = [&](Rows& rw, Rows& nx) -> bool {
+      const bool inside = ph + 1 < nph, more = inside || j + 1 < j1;
+      const int nph_i = inside ? ph + 1 : 0;
+      Pos np = cur;
+      if (!inside && more) np = pos(j + 1);
+      fetch(nx, np, nph_i);
+      const float4v back = settle(rw, g1 - g0 - ph * NG);
       int tok[4];
       float wt[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int r = 4 * q + i;
         tok[i] = r < cur.n ? sh.tb.token(cur.first + r) : -1;
-        wt[i] = r < cur.n ? sh.wt[cur.first + r] : 0.0f;
+        wt[i] = r < cur.n ? sh.wt[cur.first + r] * back[i] : 0.0f;
       }
-      for (int ph = 0; ph < nph; ++ph) {
-        const bool inside = ph + 1 < nph;
-        const Pos& np = inside ? cur : next;
-        const int nph_i = inside ? ph + 1 : 0;
-        dc_fill<true, PIECES>(
-            fr, raw, p.h, [&](int r) { return row_off(cur.first + r); }, cur.n,
-            (g0 + ph * NG) * 128, min(g1 * 128, p.I), sh.buf[wave], sh.inv[wave]);
-        fetch(np, nph_i);
-        const float4v back = *reinterpret_cast<const float4v*>(&sh.inv[wave][4 * q]);
-  #pragma unroll
-        for (int st = 0; st < NS; ++st) {
-          float4v acc = {0.0f, 0.0f, 0.0f, 0.0f};
-          uint32_t sc[NG];
-          dc_scales<NG, WHOLE>(w[st & 1], sc);
 #pragma unroll
-          for (int i = 0; i < NG; ++i) {
-            dc_mul<PIECES, NG>(acc, fr, w[st & 1].code[i], sc[i], i);
-            if (st + 2 < NS) load(cur, ph, st + 2, i);
-            else load(np, nph_i, st + 2 - NS, i);
-            __builtin_amdgcn_sched_barrier(0);
-          }
+      for (int st = 0; st < NS; ++st) {
+        float4v acc = {0.0f, 0.0f, 0.0f, 0.0f};
+        uint32_t sc[NG];
+        dc_scales<NG, WHOLE>(w[st & 1], sc);
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (tok[i] >= 0) {
-              float* o = mine + tok[i] * (NS * 16) + st * 16 + c;
-              *o = __builtin_fmaf(acc[i], back[i] * wt[i], *o);
-            }
+        for (int i = 0; i < NG; ++i) {
+          dc_mul<PIECES, NG>(acc, rw.fr, w[st & 1].code[i], sc[i], i);
+          if (st + 2 < NS) load(cur, ph, st + 2, i);
+          else load(np, nph_i, st + 2 - NS, i);
+          __builtin_amdgcn_sched_barrier(0);
         }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (tok[i] >= 0) {
+            float* o = mine + tok[i] * (NS * 16) + st * 16 + c;
+            *o = __builtin_fmaf(acc[i], wt[i], *o);
+          }
       }
-      cur = next;
+      dc_wave_sync();
+      cur = np;
+      j = inside ? j : j + 1;
+      ph = nph_i;
+      return more;
+    };
+    if (j0 < j1) {
+      cur = pos(j0);
+      fetch(ra, cur, 0);  // before W: loads return in order
+#pragma unroll
+      for (int st = 0; st < 2; ++st)
+#pragma unroll
+        for (int i = 0; i < NG; ++i) load(cur, 0, st, i);
+      dc_wave_sync();
+      while (step(ra, rb) && step(rb, ra)) {
+      }
     }
     __syncthreads();
     // the K shares of each column, in order
@@ -824,8 +946,9 @@ __global__ __launch_bounds__(kDcThreads, 2) void k_dc_down(DecodeParams p) {
         if (col < p.H) put(t, col, v);
       }
     } else {
-      // agent-scope stores go past this XCD's cache; each wave waits for its
-      // own before the workgroup counts itself
+      // agent-scope stores and loads go past this XCD's cache, so no cache has
+      // to be written back or invalidated: each wave waits for its own stores
+      // to complete before the workgroup counts itself
       for (int i = threadIdx.x; i < p.T * cols; i += kDcThreads) {
         int t, col;
         const float v = total(i, t, col);
@@ -836,7 +959,7 @@ __global__ __launch_bounds__(kDcThreads, 2) void k_dc_down(DecodeParams p) {
       asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
       __syncthreads();
       if (threadIdx.x == 0)
-        sh.last = __hip_atomic_fetch_add(p.count + blk, 1, __ATOMIC_ACQ_REL,
+        sh.last = __hip_atomic_fetch_add(p.count + blk, 1, __ATOMIC_RELAXED,
                                          __HIP_MEMORY_SCOPE_AGENT) == parts - 1;
       __syncthreads();
       if (sh.last) {
@@ -870,7 +993,7 @@ inline int64_t dc_down_blocks(int64_t T, int64_t H, int64_t I, bool f32) {
 }
 
 struct DcLayout {
-  size_t ids, wts, count, h, part, bytes;
+  size_t ids, wts, count, h, hexp, part, bytes;
 };
 inline DcLayout dc_layout(const nvfp4_moe_decode_args_t* a) {
   const size_t P = (size_t)(a->T * a->k);
@@ -881,7 +1004,9 @@ inline DcLayout dc_layout(const nvfp4_moe_decode_args_t* a) {
   l.wts = l.ids + nv_round256(P * 4);
   l.count = l.wts + nv_round256(P * 4);
   l.h = l.count + nv_round256((size_t)nb * 4);
-  l.part = l.h + nv_round256(P * (size_t)a->I * 4);
+  const size_t Ip = dc_pad((int)a->I);
+  l.hexp = l.h + nv_round256(P * Ip * (a->x_dtype == NVFP4_IN_F32 ? 4 : 2));
+  l.part = l.hexp + nv_round256(P * (Ip / 16));
   l.bytes = l.part + (parts > 1 ? nv_round256((size_t)parts * a->T * a->H * 4) : 0);
   return l;
 }
@@ -962,7 +1087,8 @@ int nvfp4_moe_decode(const nvfp4_moe_decode_args_t* a, void* ws, size_t ws_bytes
                        a->d_codes, a->d_scales, a->d_tscale, a->out, a->ldo,
                        a->topk_ids, reinterpret_cast<int32_t*>(w + l.ids),
                        a->topk_weights, reinterpret_cast<float*>(w + l.wts),
-                       reinterpret_cast<float*>(w + l.h), reinterpret_cast<float*>(w + l.part),
+                       reinterpret_cast<uint16_t*>(w + l.h), w + l.hexp,
+                       reinterpret_cast<float*>(w + l.part),
                        reinterpret_cast<int32_t*>(w + l.count),
                        (int)dc_down_blocks(a->T, a->H, a->I, a->x_dtype == NVFP4_IN_F32)};
   if (a->x_dtype == NVFP4_IN_BF16) dc_launch<false>(p, s);
