@@ -31,6 +31,7 @@ namespace {
 typedef _Float16 half8 __attribute__((ext_vector_type(8)));
 typedef _Float16 half2v __attribute__((ext_vector_type(2)));
 typedef float float4v __attribute__((ext_vector_type(4)));
+typedef uint32_t word4 __attribute__((ext_vector_type(4)));
 
 constexpr int kDcMaxT = 64;
 constexpr int kDcMaxE = 1024;
@@ -330,7 +331,7 @@ struct DcFrags {
 template <bool F32, int PIECES>
 struct DcRaw {
   static constexpr int NL = DcShape<PIECES>::NG;  // 128-k pieces of a row
-  uint4 v[NL][F32 ? 2 : 1];
+  word4 v[NL][F32 ? 2 : 1];
 };
 // Loads without a branch, so that waits for older loads stay exact: lanes past
 // kend (a multiple of 32) read the last values before it and get zeros.
@@ -342,11 +343,11 @@ __device__ __forceinline__ void dc_fetch_rows(DcRaw<F32, PIECES>& raw, const voi
   for (int j = 0; j < DcRaw<F32, PIECES>::NL; ++j) {
     const int k = min(k0 + j * 128 + l16 * 8, kend - 8);
     if constexpr (F32) {
-      const uint4* at = reinterpret_cast<const uint4*>(reinterpret_cast<const float*>(src) + row_off + k);
+      const word4* at = reinterpret_cast<const word4*>(reinterpret_cast<const float*>(src) + row_off + k);
       raw.v[j][0] = at[0];
       raw.v[j][1] = at[1];
     } else {
-      raw.v[j][0] = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(src) + row_off + k);
+      raw.v[j][0] = *reinterpret_cast<const word4*>(reinterpret_cast<const uint16_t*>(src) + row_off + k);
     }
   }
 }
@@ -360,11 +361,11 @@ __device__ __forceinline__ void dc_stage_rows(DcRaw<F32, PIECES>& raw, int k0, i
   const int l16 = threadIdx.x & 15;
   auto get = [&](int j, int i) -> float {
     if constexpr (F32) {
-      const uint4& v = raw.v[j][i >> 2];
+      const word4& v = raw.v[j][i >> 2];
       const int e = i & 3;
       return __uint_as_float(e == 0 ? v.x : e == 1 ? v.y : e == 2 ? v.z : v.w);
     } else {
-      const uint4& v = raw.v[j][0];
+      const word4& v = raw.v[j][0];
       const uint32_t w = i < 2 ? v.x : i < 4 ? v.y : i < 6 ? v.z : v.w;
       return __uint_as_float((i & 1) ? (w & 0xFFFF0000u) : (w << 16));
     }
@@ -374,7 +375,7 @@ __device__ __forceinline__ void dc_stage_rows(DcRaw<F32, PIECES>& raw, int k0, i
     for (int j = 0; j < NL; ++j)
       if (k0 + j * 128 + l16 * 8 >= kend) {
 #pragma unroll
-        for (int i = 0; i < (F32 ? 2 : 1); ++i) raw.v[j][i] = make_uint4(0, 0, 0, 0);
+        for (int i = 0; i < (F32 ? 2 : 1); ++i) raw.v[j][i] = word4{0u, 0u, 0u, 0u};
       }
   }
   float amax = 0.0f;
@@ -441,97 +442,133 @@ __device__ __forceinline__ void dc_fill(DcFrags<PIECES>& fr, DcRaw<F32, PIECES>&
   }
 }
 
-// W of one 16-column slab in one K range of NG groups.  Like the rows, W is
-// loaded without branches: past the end of the work a wave loads its last
-// slab again, past the end of K its last group (the activations are 0 there).
-// Whole K ranges (WHOLE: K a multiple of 128) take their block scales in one
-// load per slab -- each quarter of the lanes a group's, exchanged in registers
-// when they are used -- because a load costs the cache lines it touches, 16
-// here, however few bytes it takes of them: with one 2-byte load per group the
-// 16-token layer of 256 experts took 748 us.
-template <int NG, bool WHOLE>
+// W of one 16-column slab in one K range of NG groups: NG KiB of codes and
+// their block scales.  A matrix-core fragment wants column c in lane c, so
+// fragments loaded straight from memory take every lane's 16 bytes from
+// another row, and what bounds the kernel then is the number of such pieces
+// (16 tokens of the 256-expert layer: 583 us, and in proportion to the
+// pieces).  So a wave loads whole runs of a row into neighbouring lanes, holds
+// them in registers while they are in flight, and turns them round through a
+// slot of LDS of its own.  Slots are swizzled by row: the 16 rows of a
+// fragment read lie in different banks.  All of it without branches, so that
+// waits for older loads stay exact: past the end of the work a wave loads its
+// last slab again, past the end of K the last pieces (activations are 0 there).
+template <int NG>
 struct DcSlab {
-  uint4 code[NG];
-  uint32_t scale[WHOLE ? NG / 2 : NG];
+  word4 code[NG];
+  uint32_t scale[NG / 2];
 };
 
-// How a wave walks W: lane offsets inside a slab's group of 128 k.
-struct DcWalk {
-  int K2, K16, ng;         // bytes of a row of codes and scales, groups
-  uint32_t oc, os, oct, ost;  // lane offsets, and those in a short last group
-  __device__ __forceinline__ DcWalk(int K) {
-    const int lane = threadIdx.x & 63, c = lane & 15, q = lane >> 4;
-    K2 = K >> 1;
-    K16 = K >> 4;
-    ng = (K + 127) >> 7;
-    oc = c * K2 + q * 16;
-    os = c * K16 + q * 2;
-    const int dk = min(32 * q, K - 32 - (ng - 1) * 128);
-    oct = c * K2 + (dk >> 1);
-    ost = c * K16 + (dk >> 4);
+template <int NG>
+struct DcSlot {
+  static constexpr int kRow = NG * 64;  // code bytes of a row
+  static constexpr int kScales = 16 * kRow, kBytes = kScales + 16 * NG * 8;
+  static constexpr int kPieces = NG * 4;  // 16-byte pieces of a row
+  static __device__ __forceinline__ int swizzle(int row) {
+    return kPieces == 16 ? row & 15 : (row >> 1) & 7;
   }
-  // group g, the i-th of the range from g_first, of the slab at W row `row`
-  template <int NG, bool WHOLE>
-  __device__ __forceinline__ void load(DcSlab<NG, WHOLE>& s, int i, const uint8_t* codes,
-                                       const uint8_t* scales, int64_t row, int g,
-                                       int g_first) const {
-    const uint8_t* pc = codes + row * K2 + g * 64;
-    const uint8_t* ps = scales + row * K16;
-    if constexpr (WHOLE) {
-      s.code[i] = *reinterpret_cast<const uint4*>(pc + oc);
-      if (i == 0) {
-        const int lane = threadIdx.x & 63, c = lane & 15, q = lane >> 4;
-        if constexpr (NG == 4) {
-          const uint2 v = *reinterpret_cast<const uint2*>(
-              ps + (uint32_t)(c * K16 + min((g_first + q) * 8, K16 - 8)));
-          s.scale[0] = v.x;
-          s.scale[1] = v.y;
-        } else {
-          s.scale[0] = *reinterpret_cast<const uint32_t*>(
-              ps + (uint32_t)(c * K16 + min(g_first * 8 + q * 4, K16 - 4)));
-        }
-      }
+};
+
+// WHOLE: K a multiple of 128, so that a row's block scales are whole groups.
+template <int NG, bool WHOLE>
+struct DcWalk {
+  typedef DcSlot<NG> Slot;
+  static constexpr int kRows = 64 / Slot::kPieces;  // rows of one load
+  int K2, K16, ng;  // bytes of a row of codes and scales, groups
+  __device__ __forceinline__ explicit DcWalk(int K) : K2(K >> 1), K16(K >> 4), ng((K + 127) >> 7) {}
+  // the slab at W row `row`, from group g on
+  __device__ __forceinline__ void load(DcSlab<NG>& s, const uint8_t* codes, const uint8_t* scales,
+                                       int64_t row, int g) const {
+    const int lane = threadIdx.x & 63;
+    const int piece = min(g * 4 + lane % Slot::kPieces, (K2 >> 4) - 1);
+    const uint32_t oc = (lane / Slot::kPieces) * K2 + piece * 16;
+#pragma unroll
+    for (int i = 0; i < NG; ++i)
+      s.code[i] = *reinterpret_cast<const word4*>(codes + (row + i * kRows) * K2 + oc);
+    const uint8_t* ps = scales + row * K16 + (uint32_t)((lane >> 2) * K16);
+    const int os = g * 8 + (lane & 3) * (2 * NG);
+    if constexpr (!WHOLE) {
+#pragma unroll
+      for (int i = 0; i < NG / 2; ++i)
+        s.scale[i] = *reinterpret_cast<const uint16_t*>(ps + min(os + 4 * i, K16 - 2)) |
+                     (uint32_t)*reinterpret_cast<const uint16_t*>(ps + min(os + 4 * i + 2, K16 - 2)) << 16;
+    } else if constexpr (NG == 4) {
+      const uint2 v = *reinterpret_cast<const uint2*>(ps + min(os, K16 - 8));
+      s.scale[0] = v.x;
+      s.scale[1] = v.y;
     } else {
-      const bool last = g == ng - 1;
-      s.code[i] = *reinterpret_cast<const uint4*>(pc + (last ? oct : oc));
-      s.scale[i] = *reinterpret_cast<const uint16_t*>(ps + g * 8 + (last ? ost : os));
+      s.scale[0] = *reinterpret_cast<const uint32_t*>(ps + min(os, K16 - 4));
     }
+  }
+  static __device__ __forceinline__ void put(const DcSlab<NG>& s, uint8_t* slot) {
+    const int lane = threadIdx.x & 63, piece = lane % Slot::kPieces;
+#pragma unroll
+    for (int i = 0; i < NG; ++i) {
+      const int r = i * kRows + lane / Slot::kPieces;
+      *reinterpret_cast<word4*>(slot + r * Slot::kRow + (piece ^ Slot::swizzle(r)) * 16) = s.code[i];
+    }
+    uint8_t* ps = slot + Slot::kScales + lane * (2 * NG);
+    if constexpr (NG == 4)
+      *reinterpret_cast<uint2*>(ps) = make_uint2(s.scale[0], s.scale[1]);
+    else
+      *reinterpret_cast<uint32_t*>(ps) = s.scale[0];
   }
 };
 
 typedef unsigned dc_uint2 __attribute__((ext_vector_type(2)));
 
-// The lane's two scale bytes (k = 32 q .. 32 q + 31) of each group, in the low
-// half.  WHOLE with four groups: quarter q loaded group q's bytes, two words
-// for lane quarters 0 1 and 2 3.  Swapping the upper half-wave of the first
-// word with the lower one of the second, then odd 16-lane rows of the result
-// with even ones, leaves every row with the pair that holds its own.
-template <int NG, bool WHOLE>
-__device__ __forceinline__ void dc_scales(const DcSlab<NG, WHOLE>& s, uint32_t (&r)[NG]) {
+// Two bytes of each of NG groups (32 k: a lane quarter's share) from words
+// that hold them by group: with four groups, quarter q has group q's eight
+// bytes, two words for quarters 0 1 and 2 3.  Swapping the upper half-wave of
+// the first word with the lower one of the second, then odd 16-lane rows of
+// the result with even ones, leaves every row with the pair that holds its
+// own.  With two groups, quarter q has half of group q / 2, for quarters 2 (q %
+// 2) and the next.
+template <int NG>
+__device__ __forceinline__ void dc_by_quarter(const uint32_t (&w)[NG / 2], uint32_t (&r)[NG]) {
   const int q = (threadIdx.x & 63) >> 4;
   const int sh = (q & 1) * 16;
-  if constexpr (!WHOLE) {
-#pragma unroll
-    for (int i = 0; i < NG; ++i) r[i] = s.scale[i];
-  } else if constexpr (NG == 4) {
-    const dc_uint2 h = __builtin_amdgcn_permlane32_swap(s.scale[0], s.scale[1], false, false);
-    const dc_uint2 a = __builtin_amdgcn_permlane16_swap(h[0], h[0], false, false);
-    const dc_uint2 b = __builtin_amdgcn_permlane16_swap(h[1], h[1], false, false);
+  const dc_uint2 h = __builtin_amdgcn_permlane32_swap(w[0], w[NG / 2 - 1], false, false);
+  const dc_uint2 a = __builtin_amdgcn_permlane16_swap(h[0], h[0], false, false);
+  const dc_uint2 b = __builtin_amdgcn_permlane16_swap(h[1], h[1], false, false);
+  if constexpr (NG == 4) {
     r[0] = a[0] >> sh;
     r[1] = a[1] >> sh;
     r[2] = b[0] >> sh;
     r[3] = b[1] >> sh;
-  } else {  // quarter q loaded half a group: group q / 2, lane quarters 2 (q % 2) and the next
-    const dc_uint2 h = __builtin_amdgcn_permlane32_swap(s.scale[0], s.scale[0], false, false);
-    const dc_uint2 a = __builtin_amdgcn_permlane16_swap(h[0], h[0], false, false);
-    const dc_uint2 b = __builtin_amdgcn_permlane16_swap(h[1], h[1], false, false);
+  } else {
     r[0] = (q >= 2 ? a[1] : a[0]) >> sh;
     r[1] = (q >= 2 ? b[1] : b[0]) >> sh;
   }
 }
 
+// The lane's fragments of a slab from its slot.
+template <int NG>
+struct DcCols {
+  word4 code[NG];
+  uint32_t scale[NG];
+  __device__ __forceinline__ void take(const uint8_t* slot) {
+    typedef DcSlot<NG> Slot;
+    const int lane = threadIdx.x & 63, c = lane & 15, q = lane >> 4;
+    uint32_t w[NG / 2];
+    const uint8_t* ps = slot + Slot::kScales + c * (NG * 8) + q * (NG * 2);
+    if constexpr (NG == 4) {
+      const uint2 v = *reinterpret_cast<const uint2*>(ps);
+      w[0] = v.x;
+      w[1] = v.y;
+    } else {
+      w[0] = *reinterpret_cast<const uint32_t*>(ps);
+    }
+#pragma unroll
+    for (int g = 0; g < NG; ++g)
+      code[g] = *reinterpret_cast<const word4*>(slot + c * Slot::kRow +
+                                                ((4 * g + q) ^ Slot::swizzle(c)) * 16);
+    dc_by_quarter<NG>(w, scale);
+  }
+};
+
 template <int PIECES, int NG>
-__device__ __forceinline__ void dc_mul(float4v& acc, const DcFrags<PIECES>& fr, const uint4& code,
+__device__ __forceinline__ void dc_mul(float4v& acc, const DcFrags<PIECES>& fr, const word4& code,
                                        uint32_t scale, int g) {
   const half2v sc = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(scale, 1.0f, false);
   const half2v s0 = __builtin_shufflevector(sc, sc, 0, 0), s1 = __builtin_shufflevector(sc, sc, 1, 1);
@@ -564,14 +601,20 @@ __host__ __device__ inline int dc_k_shares(int K, int NG) {
   return best;
 }
 
+constexpr int kDcSlot = DcSlot<4>::kBytes;
+static_assert(DcSlot<2>::kBytes <= kDcSlot, "a slot holds a slab of either shape");
+
 struct DcGateUpShared {
+  __attribute__((aligned(16))) uint8_t slot[kDcWaves][2][kDcSlot];
   DcTables tb;
+  // a wave's rows while it fills its fragments, and its sums at the unit's end
+  union Own {
+    uint8_t buf[kDcStageRows * kDcRow];
+    float4v red[8][64];
+  };
   union {
     DcBuild bd;
-    struct {
-      uint8_t buf[kDcWaves][kDcStageRows * kDcRow];
-      float4v red[kDcWaves][8][64];
-    };
+    Own own[kDcWaves];
   };
   float inv[kDcWaves][16];
   int32_t sid[kDcInlineT * kDcMaxK];
@@ -586,7 +629,7 @@ __device__ __forceinline__ void dc_gate_up(const DecodeParams& p, DcGateUpShared
   const int lane = threadIdx.x & 63, q = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int ks = wave % KS, cs = wave / KS, CS = kDcWaves / KS;
-  const DcWalk walk(p.H);
+  const DcWalk<NG, WHOLE> walk(p.H);
   const int nslab = p.I >> 4, SPU = SPW * CS, nblk = (nslab + SPU - 1) / SPU;
   const int g0 = walk.ng * ks / KS, g1 = walk.ng * (ks + 1) / KS;
   const int nph = (g1 - g0 + NG - 1) / NG;
@@ -613,12 +656,12 @@ __device__ __forceinline__ void dc_gate_up(const DecodeParams& p, DcGateUpShared
     o.row = (int64_t)o.e * 2 * p.I;
     return o;
   };
-  DcSlab<NG, WHOLE> w[2];
-  auto load = [&](const Pos& o, int ph, int st, int i) {
-    walk.load<NG, WHOLE>(w[st & 1], i, p.gu_codes, p.gu_scales,
-                  o.row + ((st & 1) ? p.I : 0) + min(o.slab + (st >> 1), nslab - 1) * 16,
-                  min(g0 + ph * NG + i, g1 - 1), g0 + ph * NG);
+  DcSlab<NG> w[2];
+  auto load = [&](const Pos& o, int ph, int st) {
+    walk.load(w[st & 1], p.gu_codes, p.gu_scales,
+              o.row + ((st & 1) ? p.I : 0) + min(o.slab + (st >> 1), nslab - 1) * 16, g0 + ph * NG);
   };
+  uint8_t* slot = sh.slot[wave][0];
   auto row_off = [&](int row) { return (int64_t)sh.tb.token(row) * p.ldx; };
   DcRaw<F32, PIECES> raw;
   auto fetch = [&](const Pos& o, int ph) {
@@ -628,10 +671,9 @@ __device__ __forceinline__ void dc_gate_up(const DecodeParams& p, DcGateUpShared
   DcFrags<PIECES> fr;
   Pos cur = pos(u0);
   fetch(cur, 0);  // before W: loads return in order
-#pragma unroll
-  for (int st = 0; st < 2; ++st)
-#pragma unroll
-    for (int i = 0; i < NG; ++i) load(cur, 0, st, i);
+  load(cur, 0, 0);
+  load(cur, 0, 1);
+  walk.put(w[0], slot);
   int held = -1;  // tile whose fragments are in registers (one K range only)
   for (int u = u0; u < u1; ++u) {
     const Pos next = pos(u + 1 < u1 ? u + 1 : u);
@@ -646,37 +688,44 @@ __device__ __forceinline__ void dc_gate_up(const DecodeParams& p, DcGateUpShared
       if (nph > 1 || held != cur.j)
         dc_fill<F32, PIECES>(
             fr, raw, p.x, [&](int r) { return row_off(cur.first + r); }, cur.n,
-            (g0 + ph * NG) * 128, min(g1 * 128, p.H), sh.buf[wave], sh.inv[wave]);
+            (g0 + ph * NG) * 128, min(g1 * 128, p.H), sh.own[wave].buf, sh.inv[wave]);
       held = cur.j;
       if (nph > 1 || next.j != cur.j) fetch(np, nph_i);
       const float4v back = *reinterpret_cast<const float4v*>(&sh.inv[wave][4 * q]);
 #pragma unroll
       for (int st = 0; st < NSH; ++st) {
         float4v acc = {0.0f, 0.0f, 0.0f, 0.0f};
-        uint32_t sc[NG];
-        dc_scales<NG, WHOLE>(w[st & 1], sc);
+        // two stages ahead, into the registers put last; the next stage's
+        // slot is filled half way through this one
+        if (st + 2 < NSH) load(cur, ph, st + 2);
+        else load(np, nph_i, st + 2 - NSH);
+        __builtin_amdgcn_sched_barrier(0);
+        dc_wave_sync();
+        DcCols<NG> cols;
+        cols.take(slot + (st & 1) * kDcSlot);
 #pragma unroll
         for (int i = 0; i < NG; ++i) {
-          dc_mul<PIECES, NG>(acc, fr, w[st & 1].code[i], sc[i], i);
-          // two stages ahead, into the registers just used
-          if (st + 2 < NSH) load(cur, ph, st + 2, i);
-          else load(np, nph_i, st + 2 - NSH, i);
-          __builtin_amdgcn_sched_barrier(0);
+          if (i == NG / 2) {
+            __builtin_amdgcn_sched_barrier(0);
+            walk.put(w[(st + 1) & 1], slot + ((st + 1) & 1) * kDcSlot);
+            __builtin_amdgcn_sched_barrier(0);
+          }
+          dc_mul<PIECES, NG>(acc, fr, cols.code[i], cols.scale[i], i);
         }
         tot[st] += acc * back;
       }
     }
 #pragma unroll
-    for (int st = 0; st < NSH; ++st) sh.red[wave][st][lane] = tot[st];
+    for (int st = 0; st < NSH; ++st) sh.own[wave].red[st][lane] = tot[st];
     __syncthreads();
     for (int it = threadIdx.x; it < SPU * 64; it += kDcThreads) {
       const int s = it >> 6, ln = it & 63, w0 = (s / SPW) * KS, st = 2 * (s % SPW);
       const int slab = cur.blk * SPU + s;
       if (slab >= nslab) continue;
-      float4v g = sh.red[w0][st][ln], up = sh.red[w0][st + 1][ln];
+      float4v g = sh.own[w0].red[st][ln], up = sh.own[w0].red[st + 1][ln];
       for (int i = 1; i < KS; ++i) {
-        g += sh.red[w0 + i][st][ln];
-        up += sh.red[w0 + i][st + 1][ln];
+        g += sh.own[w0 + i].red[st][ln];
+        up += sh.own[w0 + i].red[st + 1][ln];
       }
       // fp16 pieces scaled by the row's largest of these 16 columns, at the
       // place where k_dc_down's lane quarter and step find them
@@ -739,13 +788,20 @@ __global__ __launch_bounds__(kDcThreads, 2) void k_dc_gate_up(DecodeParams p) {
 // LDS accumulator of each wave, and nothing is synchronized until the end.
 // Where the column blocks alone do not fill the chip the tiles are split into
 // parts, and the last workgroup of a block adds the parts in their order.
+constexpr int kDcDownRows = 4;  // rows staged at a time
 struct DcDownShared {
+  __attribute__((aligned(16))) uint8_t slot[kDcWaves][kDcSlot];
+  uint8_t buf[kDcWaves][kDcDownRows * kDcRow];
   DcTables tb;
-  DcBuild bd;
   float wt[kDcMaxPairs];  // of a row
-  float acc[kDcWaves][kDcAcc];  // [token][NS * 16]
+  union {
+    DcBuild bd;
+    float acc[kDcWaves][kDcAcc];  // [token][NS * 16]
+  };
   int last;
 };
+static_assert(2 * sizeof(DcDownShared) <= 160 * 1024 && 2 * sizeof(DcGateUpShared) <= 160 * 1024,
+              "two workgroups on a CU");
 
 template <int PIECES, bool WHOLE, int NS, bool BF16>
 __global__ __launch_bounds__(kDcThreads, 2) void k_dc_down(DecodeParams p) {
@@ -755,7 +811,7 @@ __global__ __launch_bounds__(kDcThreads, 2) void k_dc_down(DecodeParams p) {
   const int lane = threadIdx.x & 63, c = lane & 15, q = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int KS = dc_k_shares(p.I, NG), ks = wave % KS, cs = wave / KS, CS = kDcWaves / KS;
-  const DcWalk walk(p.I);
+  const DcWalk<NG, WHOLE> walk(p.I);
   const int nslab = p.H >> 4, SPU = NS * CS, nblk = p.blocks;
   const int g0 = walk.ng * ks / KS, g1 = walk.ng * (ks + 1) / KS;
   const int nph = (g1 - g0 + NG - 1) / NG, ntile = sh.tb.ntile;
@@ -779,38 +835,74 @@ __global__ __launch_bounds__(kDcThreads, 2) void k_dc_down(DecodeParams p) {
       o.row = (int64_t)(tile >> 16) * p.H;
       return o;
     };
-    DcSlab<NG, WHOLE> w[2];
-    auto load = [&](const Pos& o, int ph, int st, int i) {
-      walk.load<NG, WHOLE>(w[st & 1], i, p.d_codes, p.d_scales,
-                    o.row + min(blk * SPU + cs * NS + st, nslab - 1) * 16,
-                    min(g0 + ph * NG + i, g1 - 1), g0 + ph * NG);
+    DcSlab<NG> w[2];
+    auto load = [&](const Pos& o, int ph, int st) {
+      walk.load(w[st & 1], p.d_codes, p.d_scales, o.row + min(blk * SPU + cs * NS + st, nslab - 1) * 16,
+                g0 + ph * NG);
     };
-    // Rows of the tile: lane (c, q) takes row c (rows past the tile are copies
-    // of its last one, whose sums nobody reads), quarter q also the exponent
-    // bytes of group q, as the block scales of W.
-    struct Rows {
-      DcFrags<PIECES> fr;
-      DcSlab<NG, true> exps;
+    uint8_t* slot = sh.slot[wave];
+    // Rows of the tile: a row's K range is 64 lanes of 16 bytes, eight rows in
+    // flight ahead; through LDS, four at a time, lane (c, q) takes row c (rows
+    // past the tile are copies of its last one, whose sums nobody reads) and
+    // quarter q also the exponent bytes of group q, as the block scales of W.
+    struct Ahead {
+      word4 v[2 * kDcDownRows];
+      uint32_t exps[NG / 2];
     };
-    auto fetch = [&](Rows& rw, const Pos& o, int ph) {
-      const int pair = sh.tb.pair_of(o.first + min(c, o.n - 1)), gf = g0 + ph * NG;
-      const uint16_t* row = p.h + (int64_t)pair * PIECES * Ip + q * 8;
+    constexpr int kLanes = 64 / PIECES;  // of one piece of a row
+    auto fetch_row = [&](const Pos& o, int r, int gf) -> word4 {
+      const int pair = sh.tb.pair_of(o.first + min(r, o.n - 1));
+      const int k = min(gf * 128 + (lane % kLanes) * 8, Ip - 8);
+      return *reinterpret_cast<const word4*>(p.h + ((int64_t)pair * PIECES + lane / kLanes) * Ip + k);
+    };
+    auto fetch = [&](Ahead& nx, const Pos& o, int ph) {
+      const int gf = g0 + ph * NG;
+#pragma unroll
+      for (int r = 0; r < 2 * kDcDownRows; ++r) nx.v[r] = fetch_row(o, r, gf);
+      const int pair = sh.tb.pair_of(o.first + min(c, o.n - 1));
       const uint8_t* ex = p.hexp + (int64_t)pair * (Ip >> 4);
       if constexpr (NG == 4) {
         const uint2 v = *reinterpret_cast<const uint2*>(ex + min(gf + q, g1 - 1) * 8);
-        rw.exps.scale[0] = v.x;
-        rw.exps.scale[1] = v.y;
+        nx.exps[0] = v.x;
+        nx.exps[1] = v.y;
       } else {
-        rw.exps.scale[0] = *reinterpret_cast<const uint32_t*>(ex + min(gf + (q >> 1), g1 - 1) * 8 + (q & 1) * 4);
+        nx.exps[0] = *reinterpret_cast<const uint32_t*>(ex + min(gf + (q >> 1), g1 - 1) * 8 + (q & 1) * 4);
       }
+    };
+    struct Rows {
+      DcFrags<PIECES> fr;
+      uint32_t exps[NG / 2];
+    };
+    auto rows4 = [&](Rows& rw, const word4* v, int p0, int n) {
+      uint8_t* buf = sh.buf[wave];
 #pragma unroll
-      for (int g = 0; g < NG; ++g)
+      for (int r = 0; r < kDcDownRows; ++r)
+        *reinterpret_cast<word4*>(buf + r * kDcRow + lane * 16) = v[r];
+      dc_wave_sync();
+      const int row = min(c, n - 1) - p0;
+      if (row >= 0 && row < kDcDownRows) {
 #pragma unroll
         for (int pc = 0; pc < PIECES; ++pc)
 #pragma unroll
-          for (int st = 0; st < 4; ++st)
-            rw.fr.a[pc][g][st] = *reinterpret_cast<const half8*>(
-                row + pc * Ip + min(gf + g, g1 - 1) * 128 + st * 32);
+          for (int g = 0; g < NG; ++g)
+#pragma unroll
+            for (int st = 0; st < 4; ++st)
+              rw.fr.a[pc][g][st] = *reinterpret_cast<const half8*>(
+                  buf + row * kDcRow + pc * NG * 256 + g * 256 + st * 64 + q * 16);
+      }
+      dc_wave_sync();
+    };
+    auto fill = [&](Rows& rw, const Ahead& nx, const Pos& o, int ph) {
+      rows4(rw, nx.v, 0, o.n);
+      if (o.n > kDcDownRows) rows4(rw, nx.v + kDcDownRows, kDcDownRows, o.n);
+      for (int p0 = 2 * kDcDownRows; p0 < o.n; p0 += kDcDownRows) {
+        word4 v[kDcDownRows];
+#pragma unroll
+        for (int r = 0; r < kDcDownRows; ++r) v[r] = fetch_row(o, p0 + r, g0 + ph * NG);
+        rows4(rw, v, p0, o.n);
+      }
+#pragma unroll
+      for (int i = 0; i < NG / 2; ++i) rw.exps[i] = nx.exps[i];
     };
     auto scale_group = [&](Rows& rw, int g, uint32_t f0, uint32_t f1) {
       const half2v lo = __builtin_bit_cast(half2v, f0 | (f0 << 16));
@@ -827,7 +919,7 @@ __global__ __launch_bounds__(kDcThreads, 2) void k_dc_down(DecodeParams p) {
     // scale of the lane's four result rows.
     auto settle = [&](Rows& rw, int left) -> float4v {
       uint32_t b[NG];
-      dc_scales<NG, true>(rw.exps, b);
+      dc_by_quarter<NG>(rw.exps, b);
       uint32_t top = 0;
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
@@ -866,59 +958,61 @@ __global__ __launch_bounds__(kDcThreads, 2) void k_dc_down(DecodeParams p) {
       return back;
     };
 
-    Rows ra, rb;
-    Pos cur = {0, 0, 0};
-    int j = j0, ph = 0;
-    // one K range of one tile: rows in `rw`, the next ones go to `nx`
-    auto step = [&](Rows& rw, Rows& nx) -> bool {
-      const bool inside = ph + 1 < nph, more = inside || j + 1 < j1;
-      const int nph_i = inside ? ph + 1 : 0;
-      Pos np = cur;
-      if (!inside && more) np = pos(j + 1);
-      fetch(nx, np, nph_i);
-      const float4v back = settle(rw, g1 - g0 - ph * NG);
-      int tok[4];
-      float wt[4];
+    Rows rw;
+    Ahead nx;
+    if (j0 < j1) {
+      Pos cur = pos(j0);
+      fetch(nx, cur, 0);  // before W: loads return in order
+      load(cur, 0, 0);
+      load(cur, 0, 1);
+      dc_wave_sync();
+      walk.put(w[0], slot);
+      for (int j = j0, ph = 0; j < j1;) {
+        const bool inside = ph + 1 < nph;
+        const int nph_i = inside ? ph + 1 : 0;
+        Pos np = cur;
+        if (!inside && j + 1 < j1) np = pos(j + 1);
+        fill(rw, nx, cur, ph);
+        fetch(nx, np, nph_i);
+        const float4v back = settle(rw, g1 - g0 - ph * NG);
+        int tok[4];
+        float wt[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = 4 * q + i;
-        tok[i] = r < cur.n ? sh.tb.token(cur.first + r) : -1;
-        wt[i] = r < cur.n ? sh.wt[cur.first + r] * back[i] : 0.0f;
-      }
-#pragma unroll
-      for (int st = 0; st < NS; ++st) {
-        float4v acc = {0.0f, 0.0f, 0.0f, 0.0f};
-        uint32_t sc[NG];
-        dc_scales<NG, WHOLE>(w[st & 1], sc);
-#pragma unroll
-        for (int i = 0; i < NG; ++i) {
-          dc_mul<PIECES, NG>(acc, rw.fr, w[st & 1].code[i], sc[i], i);
-          if (st + 2 < NS) load(cur, ph, st + 2, i);
-          else load(np, nph_i, st + 2 - NS, i);
-          __builtin_amdgcn_sched_barrier(0);
+        for (int i = 0; i < 4; ++i) {
+          const int r = 4 * q + i;
+          tok[i] = r < cur.n ? sh.tb.token(cur.first + r) : -1;
+          wt[i] = r < cur.n ? sh.wt[cur.first + r] * back[i] : 0.0f;
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (tok[i] >= 0) {
-            float* o = mine + tok[i] * (NS * 16) + st * 16 + c;
-            *o = __builtin_fmaf(acc[i], wt[i], *o);
+        for (int st = 0; st < NS; ++st) {
+          if (st + 2 < NS) load(cur, ph, st + 2);
+          else load(np, nph_i, st + 2 - NS);
+          __builtin_amdgcn_sched_barrier(0);
+          dc_wave_sync();
+          DcCols<NG> cols;
+          cols.take(slot);
+          __builtin_amdgcn_sched_barrier(0);
+          dc_wave_sync();
+          float4v acc = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+          for (int i = 0; i < NG; ++i) {
+            if (i == NG / 2) {
+              __builtin_amdgcn_sched_barrier(0);
+              walk.put(w[(st + 1) & 1], slot);
+              __builtin_amdgcn_sched_barrier(0);
+            }
+            dc_mul<PIECES, NG>(acc, rw.fr, cols.code[i], cols.scale[i], i);
           }
-      }
-      dc_wave_sync();
-      cur = np;
-      j = inside ? j : j + 1;
-      ph = nph_i;
-      return more;
-    };
-    if (j0 < j1) {
-      cur = pos(j0);
-      fetch(ra, cur, 0);  // before W: loads return in order
 #pragma unroll
-      for (int st = 0; st < 2; ++st)
-#pragma unroll
-        for (int i = 0; i < NG; ++i) load(cur, 0, st, i);
-      dc_wave_sync();
-      while (step(ra, rb) && step(rb, ra)) {
+          for (int i = 0; i < 4; ++i)
+            if (tok[i] >= 0) {
+              float* o = mine + tok[i] * (NS * 16) + st * 16 + c;
+              *o = __builtin_fmaf(acc[i], wt[i], *o);
+            }
+        }
+        cur = np;
+        j = inside ? j : j + 1;
+        ph = nph_i;
       }
     }
     __syncthreads();
@@ -946,9 +1040,10 @@ __global__ __launch_bounds__(kDcThreads, 2) void k_dc_down(DecodeParams p) {
         if (col < p.H) put(t, col, v);
       }
     } else {
-      // agent-scope stores and loads go past this XCD's cache, so no cache has
-      // to be written back or invalidated: each wave waits for its own stores
-      // to complete before the workgroup counts itself
+      // agent-scope stores go past this XCD's cache, so nothing has to be
+      // written back: each wave waits for its own to complete before the
+      // workgroup counts itself; the last one drops what its cache holds of
+      // the parts
       for (int i = threadIdx.x; i < p.T * cols; i += kDcThreads) {
         int t, col;
         const float v = total(i, t, col);
@@ -963,18 +1058,19 @@ __global__ __launch_bounds__(kDcThreads, 2) void k_dc_down(DecodeParams p) {
                                          __HIP_MEMORY_SCOPE_AGENT) == parts - 1;
       __syncthreads();
       if (sh.last) {
-        for (int i = threadIdx.x; i < p.T * cols; i += kDcThreads) {
-          const int t = i / cols, col = blk * cols + i - t * cols;
-          if (col >= p.H) continue;
-          float v[kDcMaxParts], s = 0.0f;
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
+        const int quads = min(cols, p.H - blk * cols) >> 2;
+        for (int i = threadIdx.x; i < p.T * quads; i += kDcThreads) {
+          const int t = i / quads, col = blk * cols + (i - t * quads) * 4;
+          float4v v[kDcMaxParts], s = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
           for (int n = 0; n < kDcMaxParts; ++n)
-            v[n] = n < parts ? __hip_atomic_load(p.part + ((int64_t)n * p.T + t) * p.H + col,
-                                                 __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)
-                             : 0.0f;
+            v[n] = *reinterpret_cast<const float4v*>(
+                p.part + ((int64_t)min(n, parts - 1) * p.T + t) * p.H + col);
 #pragma unroll
-          for (int n = 0; n < kDcMaxParts; ++n) s += v[n];
-          put(t, col, s);
+          for (int n = 0; n < kDcMaxParts; ++n) s += n < parts ? v[n] : float4v{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) put(t, col + e, s[e]);
         }
       }
     }
