@@ -70,6 +70,7 @@ struct DecodeParams {
   float* part;  // [parts, T, H]
   int32_t* count;  // per column block of k_dc_down
   int blocks;      // column blocks
+  int ks_up, ks_down;  // waves that share K (the others share the columns)
 };
 
 // What the lanes of a wave wrote to LDS before it, all of them read after it.
@@ -586,21 +587,6 @@ __device__ __forceinline__ float dc_silu_mul(float g, float u) {
   return g / (1.0f + __expf(-g)) * u;
 }
 
-// K shares of the four waves (the rest of them share the columns): the most
-// shares among those that pad K the least to whole ranges of NG groups.
-__host__ __device__ inline int dc_k_shares(int K, int NG) {
-  const int ng = (K + 127) / 128;
-  int best = 1, least = (ng + NG - 1) / NG * NG;
-  for (int ks = 2; ks <= kDcWaves; ks *= 2) {
-    const int padded = ((ng + ks - 1) / ks + NG - 1) / NG * NG * ks;
-    if (ng >= ks && padded <= least) {
-      best = ks;
-      least = padded;
-    }
-  }
-  return best;
-}
-
 constexpr int kDcSlot = DcSlot<4>::kBytes;
 static_assert(DcSlot<2>::kBytes <= kDcSlot, "a slot holds a slab of either shape");
 
@@ -610,7 +596,7 @@ struct DcGateUpShared {
   // a wave's rows while it fills its fragments, and its sums at the unit's end
   union Own {
     uint8_t buf[kDcStageRows * kDcRow];
-    float4v red[8][64];
+    float4v red[4][64];
   };
   union {
     DcBuild bd;
@@ -631,8 +617,10 @@ __device__ __forceinline__ void dc_gate_up(const DecodeParams& p, DcGateUpShared
   const int ks = wave % KS, cs = wave / KS, CS = kDcWaves / KS;
   const DcWalk<NG, WHOLE> walk(p.H);
   const int nslab = p.I >> 4, SPU = SPW * CS, nblk = (nslab + SPU - 1) / SPU;
-  const int g0 = walk.ng * ks / KS, g1 = walk.ng * (ks + 1) / KS;
-  const int nph = (g1 - g0 + NG - 1) / NG;
+  // K range ph of the wave starts at group (ph KS + ks) NG: the shares lie
+  // side by side, so that the waves read neighbouring runs of a row together
+  const int nph = (walk.ng + NG * KS - 1) / (NG * KS);
+  auto first_group = [&](int ph) { return min((ph * KS + ks) * NG, walk.ng); };
   const int units = sh.tb.ntile * nblk;
   const int Ip = dc_pad(p.I);
   const int u0 = (int)((int64_t)units * blockIdx.x / gridDim.x);
@@ -659,14 +647,14 @@ __device__ __forceinline__ void dc_gate_up(const DecodeParams& p, DcGateUpShared
   DcSlab<NG> w[2];
   auto load = [&](const Pos& o, int ph, int st) {
     walk.load(w[st & 1], p.gu_codes, p.gu_scales,
-              o.row + ((st & 1) ? p.I : 0) + min(o.slab + (st >> 1), nslab - 1) * 16, g0 + ph * NG);
+              o.row + ((st & 1) ? p.I : 0) + min(o.slab + (st >> 1), nslab - 1) * 16, first_group(ph));
   };
   uint8_t* slot = sh.slot[wave][0];
   auto row_off = [&](int row) { return (int64_t)sh.tb.token(row) * p.ldx; };
   DcRaw<F32, PIECES> raw;
   auto fetch = [&](const Pos& o, int ph) {
     dc_fetch_rows<F32, PIECES>(raw, p.x, row_off(o.first + min(q, o.n - 1)),
-                               (g0 + ph * NG) * 128, min(g1 * 128, p.H));
+                               first_group(ph) * 128, p.H);
   };
   DcFrags<PIECES> fr;
   Pos cur = pos(u0);
@@ -688,7 +676,7 @@ __device__ __forceinline__ void dc_gate_up(const DecodeParams& p, DcGateUpShared
       if (nph > 1 || held != cur.j)
         dc_fill<F32, PIECES>(
             fr, raw, p.x, [&](int r) { return row_off(cur.first + r); }, cur.n,
-            (g0 + ph * NG) * 128, min(g1 * 128, p.H), sh.own[wave].buf, sh.inv[wave]);
+            first_group(ph) * 128, p.H, sh.own[wave].buf, sh.inv[wave]);
       held = cur.j;
       if (nph > 1 || next.j != cur.j) fetch(np, nph_i);
       const float4v back = *reinterpret_cast<const float4v*>(&sh.inv[wave][4 * q]);
@@ -775,11 +763,14 @@ __global__ __launch_bounds__(kDcThreads, 2) void k_dc_gate_up(DecodeParams p) {
   } else {
     dc_build(p, p.ids, p.wts, sh.tb, sh.bd);
   }
-  const int KS = dc_k_shares(p.H, DcShape<PIECES>::NG), CS = kDcWaves / KS, nslab = p.I >> 4;
-  const int64_t grid = gridDim.x;
-  if ((int64_t)sh.tb.ntile * (nslab / (4 * CS)) >= 2 * grid) dc_gate_up<F32, PIECES, WHOLE, 8>(p, sh, KS);
-  else if ((int64_t)sh.tb.ntile * (nslab / (2 * CS)) >= grid) dc_gate_up<F32, PIECES, WHOLE, 4>(p, sh, KS);
-  else dc_gate_up<F32, PIECES, WHOLE, 2>(p, sh, KS);
+  const int KS = p.ks_up, CS = kDcWaves / KS, nslab = p.I >> 4;
+  // two gate and two up slabs a unit where that still gives every workgroup
+  // one (four of each read the rows in runs too far apart: 344 against 321 us
+  // for 16 tokens of the 256-expert layer)
+  if ((int64_t)sh.tb.ntile * (nslab / (2 * CS)) >= gridDim.x)
+    dc_gate_up<F32, PIECES, WHOLE, 4>(p, sh, KS);
+  else
+    dc_gate_up<F32, PIECES, WHOLE, 2>(p, sh, KS);
 }
 
 // ------------------------------------------------------------------- down
@@ -810,11 +801,11 @@ __global__ __launch_bounds__(kDcThreads, 2) void k_dc_down(DecodeParams p) {
   dc_build(p, p.ids, p.wts, sh.tb, sh.bd, sh.wt, p.d_ts);
   const int lane = threadIdx.x & 63, c = lane & 15, q = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int KS = dc_k_shares(p.I, NG), ks = wave % KS, cs = wave / KS, CS = kDcWaves / KS;
+  const int KS = p.ks_down, ks = wave % KS, cs = wave / KS, CS = kDcWaves / KS;
   const DcWalk<NG, WHOLE> walk(p.I);
   const int nslab = p.H >> 4, SPU = NS * CS, nblk = p.blocks;
-  const int g0 = walk.ng * ks / KS, g1 = walk.ng * (ks + 1) / KS;
-  const int nph = (g1 - g0 + NG - 1) / NG, ntile = sh.tb.ntile;
+  const int nph = (walk.ng + NG * KS - 1) / (NG * KS), ntile = sh.tb.ntile, g1 = walk.ng;
+  auto first_group = [&](int ph) { return min((ph * KS + ks) * NG, walk.ng); };
   const int parts = max(1, min(min(ntile, kDcMaxParts), (int)gridDim.x / nblk));
   float* mine = sh.acc[wave];
   const int Ip = dc_pad(p.I);
@@ -838,7 +829,7 @@ __global__ __launch_bounds__(kDcThreads, 2) void k_dc_down(DecodeParams p) {
     DcSlab<NG> w[2];
     auto load = [&](const Pos& o, int ph, int st) {
       walk.load(w[st & 1], p.d_codes, p.d_scales, o.row + min(blk * SPU + cs * NS + st, nslab - 1) * 16,
-                g0 + ph * NG);
+                first_group(ph));
     };
     uint8_t* slot = sh.slot[wave];
     // Rows of the tile: a row's K range is 64 lanes of 16 bytes, eight rows in
@@ -856,7 +847,7 @@ __global__ __launch_bounds__(kDcThreads, 2) void k_dc_down(DecodeParams p) {
       return *reinterpret_cast<const word4*>(p.h + ((int64_t)pair * PIECES + lane / kLanes) * Ip + k);
     };
     auto fetch = [&](Ahead& nx, const Pos& o, int ph) {
-      const int gf = g0 + ph * NG;
+      const int gf = first_group(ph);
 #pragma unroll
       for (int r = 0; r < 2 * kDcDownRows; ++r) nx.v[r] = fetch_row(o, r, gf);
       const int pair = sh.tb.pair_of(o.first + min(c, o.n - 1));
@@ -898,7 +889,7 @@ __global__ __launch_bounds__(kDcThreads, 2) void k_dc_down(DecodeParams p) {
       for (int p0 = 2 * kDcDownRows; p0 < o.n; p0 += kDcDownRows) {
         word4 v[kDcDownRows];
 #pragma unroll
-        for (int r = 0; r < kDcDownRows; ++r) v[r] = fetch_row(o, p0 + r, g0 + ph * NG);
+        for (int r = 0; r < kDcDownRows; ++r) v[r] = fetch_row(o, p0 + r, first_group(ph));
         rows4(rw, v, p0, o.n);
       }
 #pragma unroll
@@ -974,7 +965,7 @@ __global__ __launch_bounds__(kDcThreads, 2) void k_dc_down(DecodeParams p) {
         if (!inside && j + 1 < j1) np = pos(j + 1);
         fill(rw, nx, cur, ph);
         fetch(nx, np, nph_i);
-        const float4v back = settle(rw, g1 - g0 - ph * NG);
+        const float4v back = settle(rw, g1 - first_group(ph));
         int tok[4];
         float wt[4];
 #pragma unroll
@@ -1080,12 +1071,62 @@ __global__ __launch_bounds__(kDcThreads, 2) void k_dc_down(DecodeParams p) {
 
 constexpr int kDcGrid = 512;  // two workgroups on each of 256 CUs
 
-// Columns of k_dc_down's blocks, in 16-column slabs per wave.
-inline int dc_down_slabs(int64_t T) { return T <= 32 ? 4 : 2; }
-inline int64_t dc_down_blocks(int64_t T, int64_t H, int64_t I, bool f32) {
-  const int ng = f32 ? DcShape<2>::NG : DcShape<1>::NG;
-  const int64_t spu = dc_down_slabs(T) * (kDcWaves / dc_k_shares((int)I, ng));
-  return ((H >> 4) + spu - 1) / spu;
+// How the four waves of a workgroup divide its work: KS of them share K, and
+// the 4 / KS groups take ns slabs each.  The fewer K ranges are padded the
+// better, and larger blocks read the rows of activations less often; but what
+// costs most is workgroups without work, so the choice is the first that
+// gives at least 7 of 8 workgroups some, in that order, or the one that keeps
+// most busy.  tiles: an upper bound of the row tiles, which only the device
+// knows.
+struct DcSplit {
+  int ks, ns, blocks, parts;
+};
+inline DcSplit dc_split(int K, int NG, int nslab, int ns_most, int ns_least, int64_t tiles,
+                        int max_parts) {
+  const int ng = (K + 127) / 128;
+  int64_t padded[3];
+  int order[3] = {0, 1, 2};  // KS = 4, 2, 1
+  for (int i = 0; i < 3; ++i) {
+    const int ks = kDcWaves >> i;
+    padded[i] = (int64_t)((ng + NG * ks - 1) / (NG * ks)) * ks;
+    for (int j = i; j > 0 && padded[order[j]] < padded[order[j - 1]]; --j) {
+      const int t = order[j];
+      order[j] = order[j - 1];
+      order[j - 1] = t;
+    }
+  }
+  DcSplit best{1, ns_least, 1, 1};
+  int64_t most = -1;
+  for (int i = 0; i < 3; ++i)
+    for (int ns = ns_most; ns >= ns_least; ns /= 2) {
+      DcSplit o{kDcWaves >> order[i], ns, 0, 0};
+      const int spu = ns * (kDcWaves / o.ks);
+      o.blocks = (nslab + spu - 1) / spu;
+      int64_t parts = max_parts < tiles ? max_parts : tiles;
+      if (max_parts < kDcMaxTiles && parts > kDcGrid / o.blocks) parts = kDcGrid / o.blocks;
+      o.parts = (int)(parts < 1 ? 1 : parts);
+      const int64_t work = (int64_t)o.blocks * o.parts;
+      if (work >= kDcGrid * 7 / 8) return o;
+      if (work > most) {
+        most = work;
+        best = o;
+      }
+    }
+  return best;
+}
+inline int64_t dc_tiles(const nvfp4_moe_decode_args_t* a) {
+  const int64_t P = a->T * a->k, few = a->E + P / 16;
+  return P < few ? P : few;
+}
+inline int dc_groups(const nvfp4_moe_decode_args_t* a) {
+  return a->x_dtype == NVFP4_IN_F32 ? DcShape<2>::NG : DcShape<1>::NG;
+}
+inline DcSplit dc_split_up(const nvfp4_moe_decode_args_t* a) {
+  return dc_split((int)a->H, dc_groups(a), (int)(a->I >> 4), 1, 1, dc_tiles(a), kDcMaxTiles);
+}
+inline DcSplit dc_split_down(const nvfp4_moe_decode_args_t* a) {
+  return dc_split((int)a->I, dc_groups(a), (int)(a->H >> 4), a->T <= 32 ? 4 : 2, 2, dc_tiles(a),
+                  kDcMaxParts);
 }
 
 struct DcLayout {
@@ -1093,8 +1134,8 @@ struct DcLayout {
 };
 inline DcLayout dc_layout(const nvfp4_moe_decode_args_t* a) {
   const size_t P = (size_t)(a->T * a->k);
-  const int64_t nb = dc_down_blocks(a->T, a->H, a->I, a->x_dtype == NVFP4_IN_F32);
-  const int64_t fill = kDcGrid / nb, parts = fill < 1 ? 1 : fill > kDcMaxParts ? kDcMaxParts : fill;
+  const DcSplit d = dc_split_down(a);
+  const int64_t nb = d.blocks, parts = d.parts;
   DcLayout l;
   l.ids = 0;
   l.wts = l.ids + nv_round256(P * 4);
@@ -1135,11 +1176,11 @@ void dc_launch_gate_up(const DecodeParams& p, hipStream_t s) {
 }
 
 template <bool F32>
-void dc_launch(const DecodeParams& p, hipStream_t s) {
+void dc_launch(const DecodeParams& p, int ns, hipStream_t s) {
   if (p.H % 128 == 0) dc_launch_gate_up<F32, true>(p, s);
   else dc_launch_gate_up<F32, false>(p, s);
   const bool whole = p.I % 128 == 0;
-  if (dc_down_slabs(p.T) == 4) {
+  if (ns == 4) {
     if (whole) dc_launch_down<F32, true, 4>(p, s);
     else dc_launch_down<F32, false, 4>(p, s);
   } else {
@@ -1178,6 +1219,7 @@ int nvfp4_moe_decode(const nvfp4_moe_decode_args_t* a, void* ws, size_t ws_bytes
   NV_RETURN_IF(!ws || ws_bytes < l.bytes || !nv_aligned16(ws), NVFP4_ERR_WORKSPACE);
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   uint8_t* w = reinterpret_cast<uint8_t*>(ws);
+  const DcSplit down = dc_split_down(a);
   const DecodeParams p{(int)a->T, (int)a->E, (int)a->k, (int)a->H, (int)a->I, a->x, a->ldx,
                        a->logits, a->ld_logits, a->gu_codes, a->gu_scales, a->gu_tscale,
                        a->d_codes, a->d_scales, a->d_tscale, a->out, a->ldo,
@@ -1186,9 +1228,9 @@ int nvfp4_moe_decode(const nvfp4_moe_decode_args_t* a, void* ws, size_t ws_bytes
                        reinterpret_cast<uint16_t*>(w + l.h), w + l.hexp,
                        reinterpret_cast<float*>(w + l.part),
                        reinterpret_cast<int32_t*>(w + l.count),
-                       (int)dc_down_blocks(a->T, a->H, a->I, a->x_dtype == NVFP4_IN_F32)};
-  if (a->x_dtype == NVFP4_IN_BF16) dc_launch<false>(p, s);
-  else dc_launch<true>(p, s);
+                       down.blocks, dc_split_up(a).ks, down.ks};
+  if (a->x_dtype == NVFP4_IN_BF16) dc_launch<false>(p, down.ns, s);
+  else dc_launch<true>(p, down.ns, s);
   return nv_launch_status();
 }
 
