@@ -103,6 +103,15 @@ __device__ __forceinline__ uint32_t dc_wave_max(uint32_t v) {
   return max(max(a, b), max(c, d));
 }
 
+// Maximum over each row of 16 lanes.
+__device__ __forceinline__ float dc_row_max(float v) {
+  auto step = [](float a, int b) { return __builtin_fmaxf(a, __builtin_bit_cast(float, b)); };
+  v = step(v, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), 0xB1, 0xF, 0xF, false));
+  v = step(v, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), 0x4E, 0xF, 0xF, false));
+  v = step(v, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), 0x141, 0xF, 0xF, false));
+  return step(v, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), 0x140, 0xF, 0xF, false));
+}
+
 // Top-k of token t by one wave, PER logits per lane (E <= 64 PER).  The ids
 // and weights go to sid / swt, and to the workspace and the caller's arrays if
 // `store`.
@@ -384,8 +393,7 @@ __device__ __forceinline__ void dc_stage_rows(DcRaw<F32, PIECES>& raw, int k0, i
   for (int j = 0; j < NL; ++j)
 #pragma unroll
     for (int i = 0; i < 8; ++i) amax = __builtin_fmaxf(amax, __builtin_fabsf(get(j, i)));
-#pragma unroll
-  for (int o = 8; o > 0; o >>= 1) amax = __builtin_fmaxf(amax, __shfl_xor(amax, o, 64));
+  amax = dc_row_max(amax);
   float back;
   const float s = dc_row_scale(amax, &back);
 #pragma unroll
@@ -610,7 +618,8 @@ struct DcGateUpShared {
 // Units of (tile, column block): a wave takes NSH / 2 gate slabs and their up
 // slabs over its share of K (ks of KS) and column share (cs of CS).
 template <bool F32, int PIECES, bool WHOLE, int NSH>
-__device__ __forceinline__ void dc_gate_up(const DecodeParams& p, DcGateUpShared& sh, int KS) {
+__device__ __forceinline__ void dc_gate_up(const DecodeParams& p, DcGateUpShared& sh, int KS,
+                                           DcRaw<F32, PIECES>& raw) {
   constexpr int NG = DcShape<PIECES>::NG, SPW = NSH / 2;
   const int lane = threadIdx.x & 63, q = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -651,14 +660,13 @@ __device__ __forceinline__ void dc_gate_up(const DecodeParams& p, DcGateUpShared
   };
   uint8_t* slot = sh.slot[wave][0];
   auto row_off = [&](int row) { return (int64_t)sh.tb.token(row) * p.ldx; };
-  DcRaw<F32, PIECES> raw;
   auto fetch = [&](const Pos& o, int ph) {
     dc_fetch_rows<F32, PIECES>(raw, p.x, row_off(o.first + min(q, o.n - 1)),
                                first_group(ph) * 128, p.H);
   };
   DcFrags<PIECES> fr;
   Pos cur = pos(u0);
-  fetch(cur, 0);  // before W: loads return in order
+  if (p.T > 1) fetch(cur, 0);  // before W: loads return in order
   load(cur, 0, 0);
   load(cur, 0, 1);
   walk.put(w[0], slot);
@@ -723,9 +731,7 @@ __device__ __forceinline__ void dc_gate_up(const DecodeParams& p, DcGateUpShared
       for (int i = 0; i < 4; ++i) {
         const int r = 4 * (ln >> 4) + i;
         const float h = dc_silu_mul(ts * g[i], ts * up[i]);
-        float amax = __builtin_fabsf(h);
-#pragma unroll
-        for (int o = 8; o > 0; o >>= 1) amax = __builtin_fmaxf(amax, __shfl_xor(amax, o, 64));
+        const float amax = dc_row_max(__builtin_fabsf(h));
         if (r >= cur.n) continue;
         const int pair = sh.tb.pair_of(cur.first + r), e = dc_exponent(amax);
         const float v = h * __uint_as_float((uint32_t)(14 - e + 127) << 23);
@@ -753,6 +759,13 @@ __device__ __forceinline__ void dc_gate_up(const DecodeParams& p, DcGateUpShared
 template <bool F32, int PIECES, bool WHOLE, bool ROUTE>
 __global__ __launch_bounds__(kDcThreads, 2) void k_dc_gate_up(DecodeParams p) {
   __shared__ DcGateUpShared sh;
+  // one token: its row does not wait for the routing
+  DcRaw<F32, PIECES> raw;
+  if (p.T == 1) {
+    constexpr int NG = DcShape<PIECES>::NG;
+    const int ks = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) % p.ks_up;
+    dc_fetch_rows<F32, PIECES>(raw, p.x, 0, min(ks * NG, (p.H + 127) >> 7) * 128, p.H);
+  }
   if (blockIdx.x == 0)
     for (int i = threadIdx.x; i < p.blocks; i += kDcThreads) p.count[i] = 0;
   if constexpr (ROUTE) {
@@ -768,9 +781,9 @@ __global__ __launch_bounds__(kDcThreads, 2) void k_dc_gate_up(DecodeParams p) {
   // one (four of each read the rows in runs too far apart: 344 against 321 us
   // for 16 tokens of the 256-expert layer)
   if ((int64_t)sh.tb.ntile * (nslab / (2 * CS)) >= gridDim.x)
-    dc_gate_up<F32, PIECES, WHOLE, 4>(p, sh, KS);
+    dc_gate_up<F32, PIECES, WHOLE, 4>(p, sh, KS, raw);
   else
-    dc_gate_up<F32, PIECES, WHOLE, 2>(p, sh, KS);
+    dc_gate_up<F32, PIECES, WHOLE, 2>(p, sh, KS, raw);
 }
 
 // ------------------------------------------------------------------- down
@@ -1075,8 +1088,9 @@ constexpr int kDcGrid = 512;  // two workgroups on each of 256 CUs
 // the 4 / KS groups take ns slabs each.  The fewer K ranges are padded the
 // better, and larger blocks read the rows of activations less often; but what
 // costs most is workgroups without work, so the choice is the first that
-// gives at least 7 of 8 workgroups some, in that order, or the one that keeps
-// most busy.  tiles: an upper bound of the row tiles, which only the device
+// gives at least 7 of 8 workgroups some (32 a tile where there are few tiles:
+// one token of the 128-expert layer takes 12.1 us for its down product with
+// 64), in that order, or the one that keeps most busy.  tiles: an upper bound of the row tiles, which only the device
 // knows.
 struct DcSplit {
   int ks, ns, blocks, parts;
@@ -1096,6 +1110,7 @@ inline DcSplit dc_split(int K, int NG, int nslab, int ns_most, int ns_least, int
     }
   }
   DcSplit best{1, ns_least, 1, 1};
+  const int64_t enough = tiles * 32 < kDcGrid * 7 / 8 ? tiles * 32 : kDcGrid * 7 / 8;
   int64_t most = -1;
   for (int i = 0; i < 3; ++i)
     for (int ns = ns_most; ns >= ns_least; ns /= 2) {
@@ -1106,7 +1121,7 @@ inline DcSplit dc_split(int K, int NG, int nslab, int ns_most, int ns_least, int
       if (max_parts < kDcMaxTiles && parts > kDcGrid / o.blocks) parts = kDcGrid / o.blocks;
       o.parts = (int)(parts < 1 ? 1 : parts);
       const int64_t work = (int64_t)o.blocks * o.parts;
-      if (work >= kDcGrid * 7 / 8) return o;
+      if (work >= enough) return o;
       if (work > most) {
         most = work;
         best = o;
