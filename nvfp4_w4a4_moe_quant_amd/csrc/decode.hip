@@ -41,6 +41,7 @@ constexpr int kDcMaxPairs = kDcMaxT * kDcMaxK;
 constexpr int kDcMaxTiles = kDcMaxPairs;  // 16-row tiles: at most one per pair
 constexpr int kDcThreads = 256;
 constexpr int kDcWaves = kDcThreads / 64;
+constexpr int kDcGrid = 512;     // two workgroups on each of 256 CUs
 constexpr int kDcInlineT = 8;    // tokens up to which the gate/up kernel routes
 constexpr int kDcInlineE = 256;
 constexpr int kDcRow = 1024 + 16;  // bytes of a staged row: 512 k x 1 piece or 256 k x 2, padded
@@ -632,8 +633,8 @@ __device__ __forceinline__ void dc_gate_up(const DecodeParams& p, DcGateUpShared
   auto first_group = [&](int ph) { return min((ph * KS + ks) * NG, walk.ng); };
   const int units = sh.tb.ntile * nblk;
   const int Ip = dc_pad(p.I);
-  const int u0 = (int)((int64_t)units * blockIdx.x / gridDim.x);
-  const int u1 = (int)((int64_t)units * (blockIdx.x + 1) / gridDim.x);
+  const int u0 = (int)((int64_t)units * blockIdx.x / kDcGrid);
+  const int u1 = (int)((int64_t)units * (blockIdx.x + 1) / kDcGrid);
   if (u0 >= u1) return;
 
   // where a unit's columns lie: its expert's first W row and the wave's slab
@@ -714,40 +715,38 @@ __device__ __forceinline__ void dc_gate_up(const DecodeParams& p, DcGateUpShared
 #pragma unroll
     for (int st = 0; st < NSH; ++st) sh.own[wave].red[st][lane] = tot[st];
     __syncthreads();
-    for (int it = threadIdx.x; it < SPU * 64; it += kDcThreads) {
-      const int s = it >> 6, ln = it & 63, w0 = (s / SPW) * KS, st = 2 * (s % SPW);
+    // a wave takes rows i, 4 + i, 8 + i and 12 + i of a slab
+    for (int it = wave; it < SPU * 4; it += kDcWaves) {
+      const int s = it >> 2, i = it & 3, w0 = (s / SPW) * KS, st = 2 * (s % SPW);
       const int slab = cur.blk * SPU + s;
-      if (slab >= nslab) continue;
-      float4v g = sh.own[w0].red[st][ln], up = sh.own[w0].red[st + 1][ln];
-      for (int i = 1; i < KS; ++i) {
-        g += sh.own[w0 + i].red[st][ln];
-        up += sh.own[w0 + i].red[st + 1][ln];
+      if (slab >= nslab || i >= cur.n) continue;
+      float g = 0.0f, up = 0.0f;
+      for (int v = 0; v < KS; ++v) {
+        g += sh.own[w0 + v].red[st][lane][i];
+        up += sh.own[w0 + v].red[st + 1][lane][i];
       }
       // fp16 pieces scaled by the row's largest of these 16 columns, at the
       // place where k_dc_down's lane quarter and step find them
-      const int k = slab * 16 + (ln & 15);
-      const int at = (k & ~127) + ((k >> 3) & 3) * 32 + ((k >> 5) & 3) * 8 + (k & 7);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = 4 * (ln >> 4) + i;
-        const float h = dc_silu_mul(ts * g[i], ts * up[i]);
-        const float amax = dc_row_max(__builtin_fabsf(h));
-        if (r >= cur.n) continue;
-        const int pair = sh.tb.pair_of(cur.first + r), e = dc_exponent(amax);
-        const float v = h * __uint_as_float((uint32_t)(14 - e + 127) << 23);
-        const _Float16 hi = (_Float16)v;
-        uint16_t* out = p.h + (int64_t)pair * PIECES * Ip + at;
-        out[0] = __builtin_bit_cast(uint16_t, hi);
-        if constexpr (PIECES == 2) out[Ip] = __builtin_bit_cast(uint16_t, (_Float16)(v - (float)hi));
-        if ((ln & 15) == 0) p.hexp[(int64_t)pair * (Ip >> 4) + slab] = (uint8_t)(e + 128);
-        if (slab == nslab - 1) {  // zeros behind I, for the lanes that read them
-          for (int z = p.I + (ln & 15); z < Ip; z += 16) {
-            const int zat = (z & ~127) + ((z >> 3) & 3) * 32 + ((z >> 5) & 3) * 8 + (z & 7);
-            uint16_t* zo = p.h + (int64_t)pair * PIECES * Ip + zat;
-            zo[0] = 0;
-            if constexpr (PIECES == 2) zo[Ip] = 0;
-            if ((ln & 15) == 0) p.hexp[(int64_t)pair * (Ip >> 4) + (z >> 4)] = 0;
-          }
+      auto place = [](int k) { return (k & ~127) + ((k >> 3) & 3) * 32 + ((k >> 5) & 3) * 8 + (k & 7); };
+      const float h = dc_silu_mul(ts * g, ts * up);
+      const float amax = dc_row_max(__builtin_fabsf(h));
+      const int r = 4 * q + i, c = lane & 15;
+      if (r >= cur.n) continue;
+      const int64_t pair = sh.tb.pair_of(cur.first + r);
+      const int e = dc_exponent(amax);
+      const float v = h * __uint_as_float((uint32_t)(14 - e + 127) << 23);
+      const _Float16 hi = (_Float16)v;
+      uint16_t* out = p.h + pair * PIECES * Ip;
+      uint8_t* ex = p.hexp + pair * (Ip >> 4);
+      const int at = place(slab * 16 + c);
+      out[at] = __builtin_bit_cast(uint16_t, hi);
+      if constexpr (PIECES == 2) out[Ip + at] = __builtin_bit_cast(uint16_t, (_Float16)(v - (float)hi));
+      if (c == 0) ex[slab] = (uint8_t)(e + 128);
+      if (slab == nslab - 1) {  // zeros behind I, for the lanes that read them
+        for (int z = p.I + c; z < Ip; z += 16) {
+          out[place(z)] = 0;
+          if constexpr (PIECES == 2) out[Ip + place(z)] = 0;
+          if (c == 0) ex[z >> 4] = 0;
         }
       }
     }
@@ -780,7 +779,7 @@ __global__ __launch_bounds__(kDcThreads, 2) void k_dc_gate_up(DecodeParams p) {
   // two gate and two up slabs a unit where that still gives every workgroup
   // one (four of each read the rows in runs too far apart: 344 against 321 us
   // for 16 tokens of the 256-expert layer)
-  if ((int64_t)sh.tb.ntile * (nslab / (2 * CS)) >= gridDim.x)
+  if ((int64_t)sh.tb.ntile * (nslab / (2 * CS)) >= kDcGrid)
     dc_gate_up<F32, PIECES, WHOLE, 4>(p, sh, KS, raw);
   else
     dc_gate_up<F32, PIECES, WHOLE, 2>(p, sh, KS, raw);
@@ -800,7 +799,7 @@ struct DcDownShared {
   float wt[kDcMaxPairs];  // of a row
   union {
     DcBuild bd;
-    float acc[kDcWaves][kDcAcc];  // [token][NS * 16]
+    __attribute__((aligned(16))) float acc[kDcWaves][kDcAcc];  // [token][NS * 16]
   };
   int last;
 };
@@ -819,13 +818,13 @@ __global__ __launch_bounds__(kDcThreads, 2) void k_dc_down(DecodeParams p) {
   const int nslab = p.H >> 4, SPU = NS * CS, nblk = p.blocks;
   const int nph = (walk.ng + NG * KS - 1) / (NG * KS), ntile = sh.tb.ntile, g1 = walk.ng;
   auto first_group = [&](int ph) { return min((ph * KS + ks) * NG, walk.ng); };
-  const int parts = max(1, min(min(ntile, kDcMaxParts), (int)gridDim.x / nblk));
+  const int parts = max(1, min(min(ntile, kDcMaxParts), kDcGrid / nblk));
   float* mine = sh.acc[wave];
   const int Ip = dc_pad(p.I);
 
-  for (int id = blockIdx.x; id < nblk * parts; id += gridDim.x) {
+  for (int id = blockIdx.x; id < nblk * parts; id += kDcGrid) {
     const int part = id / nblk, blk = id - part * nblk;
-    const int j0 = (int)((int64_t)ntile * part / parts), j1 = (int)((int64_t)ntile * (part + 1) / parts);
+    const int j0 = ntile * part / parts, j1 = ntile * (part + 1) / parts;
     for (int i = lane; i < p.T * NS * 16; i += 64) mine[i] = 0.0f;
     struct Pos {
       int first, n;
@@ -1021,39 +1020,39 @@ __global__ __launch_bounds__(kDcThreads, 2) void k_dc_down(DecodeParams p) {
     }
     __syncthreads();
     // the K shares of each column, in order
-    const int cols = SPU * 16;
-    auto total = [&](int i, int& t, int& col) -> float {
-      t = i / cols;
-      const int b = i - t * cols, w0 = (b / (NS * 16)) * KS;
-      col = blk * cols + b;
-      float s = 0.0f;
-      for (int v = 0; v < KS; ++v)
-        s += sh.acc[w0 + v][t * (NS * 16) + b % (NS * 16)];
+    const int cols = SPU * 16, quads = min(cols, p.H - blk * cols) >> 2;
+    auto total = [&](int t, int b) -> float4v {  // columns b .. b + 3 of the block
+      const int w0 = (b / (NS * 16)) * KS, at = t * (NS * 16) + b % (NS * 16);
+      float4v s = {0.0f, 0.0f, 0.0f, 0.0f};
+      for (int v = 0; v < KS; ++v) s += *reinterpret_cast<const float4v*>(&sh.acc[w0 + v][at]);
       return s;
     };
-    auto put = [&](int t, int col, float v) {
-      if constexpr (BF16)
-        reinterpret_cast<__bf16*>(p.out)[t * p.ldo + col] = (__bf16)v;
-      else
-        reinterpret_cast<float*>(p.out)[t * p.ldo + col] = v;
+    auto put = [&](int t, int col, const float4v& v) {
+      if constexpr (BF16) {
+        typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+        const bf16x4 o = {(__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]};
+        *reinterpret_cast<bf16x4*>(reinterpret_cast<__bf16*>(p.out) + t * p.ldo + col) = o;
+      } else {
+        *reinterpret_cast<float4v*>(reinterpret_cast<float*>(p.out) + t * p.ldo + col) = v;
+      }
     };
     if (parts == 1) {
-      for (int i = threadIdx.x; i < p.T * cols; i += kDcThreads) {
-        int t, col;
-        const float v = total(i, t, col);
-        if (col < p.H) put(t, col, v);
+      for (int i = threadIdx.x; i < p.T * quads; i += kDcThreads) {
+        const int t = i / quads, b = (i - t * quads) * 4;
+        put(t, blk * cols + b, total(t, b));
       }
     } else {
       // agent-scope stores go past this XCD's cache, so nothing has to be
       // written back: each wave waits for its own to complete before the
       // workgroup counts itself; the last one drops what its cache holds of
       // the parts
-      for (int i = threadIdx.x; i < p.T * cols; i += kDcThreads) {
-        int t, col;
-        const float v = total(i, t, col);
-        if (col < p.H)
-          __hip_atomic_store(p.part + ((int64_t)part * p.T + t) * p.H + col, v, __ATOMIC_RELAXED,
-                             __HIP_MEMORY_SCOPE_AGENT);
+      for (int i = threadIdx.x; i < p.T * quads; i += kDcThreads) {
+        const int t = i / quads, b = (i - t * quads) * 4;
+        const float4v v = total(t, b);
+        float* at = p.part + ((int64_t)part * p.T + t) * p.H + blk * cols + b;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          __hip_atomic_store(at + e, v[e], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       }
       asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
       __syncthreads();
@@ -1063,7 +1062,6 @@ __global__ __launch_bounds__(kDcThreads, 2) void k_dc_down(DecodeParams p) {
       __syncthreads();
       if (sh.last) {
         __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
-        const int quads = min(cols, p.H - blk * cols) >> 2;
         for (int i = threadIdx.x; i < p.T * quads; i += kDcThreads) {
           const int t = i / quads, col = blk * cols + (i - t * quads) * 4;
           float4v v[kDcMaxParts], s = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -1073,8 +1071,7 @@ __global__ __launch_bounds__(kDcThreads, 2) void k_dc_down(DecodeParams p) {
                 p.part + ((int64_t)min(n, parts - 1) * p.T + t) * p.H + col);
 #pragma unroll
           for (int n = 0; n < kDcMaxParts; ++n) s += n < parts ? v[n] : float4v{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) put(t, col + e, s[e]);
+          put(t, col, s);
         }
       }
     }
@@ -1082,7 +1079,6 @@ __global__ __launch_bounds__(kDcThreads, 2) void k_dc_down(DecodeParams p) {
   }
 }
 
-constexpr int kDcGrid = 512;  // two workgroups on each of 256 CUs
 
 // How the four waves of a workgroup divide its work: KS of them share K, and
 // the 4 / KS groups take ns slabs each.  The fewer K ranges are padded the
