@@ -440,6 +440,27 @@ def moe_extras(w, dev, x, lg, wgu, wd, nsx, nsh, timed, step, ms_step, nev):
                                speedup=round(eager_us / graph_us, 3),
                                graph_with_input_copies_us=round(graph_cp_us, 1))
     out["decode_gemms"] = decode_moe_gemms(w, P, L, xd, lgd, args)
+    # the same layer with unquantized activations in two or three launches
+    out["decode_layer"] = {}
+    for Tn in (1, Td):
+        xn, lgn = x[:Tn].contiguous(), lg[:Tn].contiguous()
+        gn = P.GraphedMoEDecode(wgu, wd, w.topk, T=Tn, E=w.E, x_dtype=x.dtype, device=dev, x=xn,
+                                logits=lgn)
+        nexp = int(torch.unique(gn().topk_ids).numel())
+        us = []
+        for _ in range(6):
+            torch.cuda.synchronize()
+            t0 = time.perf_counter()
+            for _ in range(10):
+                gn()
+            torch.cuda.synchronize()
+            us.append((time.perf_counter() - t0) / 10 * 1e6)
+        us = float(np.median(us))
+        nbytes = nexp * 3 * w.H * w.I * 9 // 16
+        out["decode_layer"][f"tokens_{Tn}"] = dict(
+            graph_us_per_call=round(us, 1), experts=nexp, weight_bytes=nbytes,
+            gbs=round(nbytes / us / 1e3, 1),
+            frac_hbm=round(nbytes / us / 1e3 / PEAK_HBM_GBS, 4))
     # a larger decode batch: 256 tokens, 8 routed rows per expert on average
     Tb = 256
     xb, lgb = x[:Tb].contiguous(), lg[:Tb].contiguous()

@@ -14,6 +14,10 @@ blog post's section "Two fixes, on two different sides"):
     moe_combine(Y, row_of, routing weights) -> token-order output (moe_block)
 GraphedMoEBlock captures the whole block once as a HIP graph for fixed
 shapes (decode), so a step replays every kernel with no host work per launch.
+For up to 64 tokens moe_decode computes the whole layer in two or three
+launches with unquantized activations, on the same weights; token_logprobs
+gives the log-probabilities and entropies of the tokens that both sides of
+the rollout-trainer gap are measured by, with their gradient.
 Weights are quantized once, per expert and projection, by the same
 nvfp4_quantize (every engine quantizes the synchronized weights the same way:
 blog post, section "The failure mode").
@@ -195,6 +199,43 @@ class GraphedMoEBlock:
         return self.out
 
 
+class GraphedMoEDecode:
+    """moe_decode captured once as a HIP graph for a fixed number of tokens (at
+    most 64): a call replays the layer on the static inputs, its own or the
+    caller's x [T, H] and logits [T, E] when given, after copying inputs that
+    live elsewhere.  A batch of fewer tokens fills the remaining logits rows
+    with -inf: such rows cost nothing and give 0.  The returned MoEDecodeOut is
+    the graph's own, overwritten by the next call."""
+
+    def __init__(self, wgu: QuantWeights, wd: QuantWeights, topk: int, T: int, E: int,
+                 x_dtype: torch.dtype, device, warmup: int = 2,
+                 x: Optional[torch.Tensor] = None, logits: Optional[torch.Tensor] = None):
+        self.x = x if x is not None else torch.zeros((T, wgu.K), dtype=x_dtype, device=device)
+        self.logits = (logits if logits is not None
+                       else torch.zeros((T, E), dtype=torch.float32, device=device))
+        if self.x.shape != (T, wgu.K) or self.x.dtype != x_dtype or self.logits.shape != (T, E):
+            raise ValueError("x [T, H] of x_dtype and logits [T, E]")
+        args = (wgu, wd, topk)
+        side = torch.cuda.Stream(device)
+        side.wait_stream(torch.cuda.current_stream(device))
+        with torch.cuda.stream(side):
+            for _ in range(warmup):
+                moe_decode(self.x, self.logits, *args)
+        torch.cuda.current_stream(device).wait_stream(side)
+        self.graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(self.graph):
+            self.out = moe_decode(self.x, self.logits, *args)
+
+    def __call__(self, x: Optional[torch.Tensor] = None,
+                 logits: Optional[torch.Tensor] = None) -> L.MoEDecodeOut:
+        if x is not None and x.data_ptr() != self.x.data_ptr():
+            self.x.copy_(x)
+        if logits is not None and logits.data_ptr() != self.logits.data_ptr():
+            self.logits.copy_(logits)
+        self.graph.replay()
+        return self.out
+
+
 class GraphedDense:
     """dense_forward captured once as a HIP graph for fixed [rows, K] (the
     decode shape): a call copies x into the static input and replays every
@@ -264,5 +305,13 @@ def token_logprobs(logits: torch.Tensor, targets: torch.Tensor,
                    ) -> Tuple[torch.Tensor, torch.Tensor]:
     """(log-probabilities of targets, entropies) of logits [T, V], with the
     gradient of the logits (the trainer's side of the rollout-trainer
-    log-prob gap).  Targets and temperatures get no gradient."""
+    log-prob gap).  Targets and temperatures get no gradient, and there is no
+    second derivative.  Leaf logits that require a gradient are refused under
+    graph capture, where another living graph of the same leaf ends the
+    process: capture the two library calls instead."""
+    if inv_temperature is not None and inv_temperature.requires_grad:
+        raise ValueError("inv_temperature gets no gradient")
+    if logits.requires_grad and logits.is_leaf and torch.cuda.is_current_stream_capturing():
+        raise RuntimeError("leaf logits under capture: use the library's token_logprobs and "
+                           "token_logprobs_backward")
     return _TokenLogprobs.apply(logits, targets, inv_temperature)
