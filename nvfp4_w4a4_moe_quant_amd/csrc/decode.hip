@@ -42,7 +42,10 @@ constexpr int kDcMaxTiles = kDcMaxPairs;  // 16-row tiles: at most one per pair
 constexpr int kDcThreads = 256;
 constexpr int kDcWaves = kDcThreads / 64;
 constexpr int kDcGrid = 512;     // two workgroups on each of 256 CUs
-constexpr int kDcInlineT = 8;    // tokens up to which the gate/up kernel routes
+// The gate/up kernel routes by itself for few tokens (every workgroup does
+// it all): 1 token of the 128-expert layer 21.4 against 22.2 us with a launch
+// before it, 4 tokens 38.9 / 39.9, 8 tokens 53.3 / 51.9.
+constexpr int kDcInlineT = 4;
 constexpr int kDcInlineE = 256;
 constexpr int kDcRow = 1024 + 16;  // bytes of a staged row: 512 k x 1 piece or 256 k x 2, padded
 constexpr int kDcStageRows = 8;
@@ -755,7 +758,7 @@ __device__ __forceinline__ void dc_gate_up(const DecodeParams& p, DcGateUpShared
   }
 }
 
-template <bool F32, int PIECES, bool WHOLE, bool ROUTE>
+template <bool F32, int PIECES, bool WHOLE, bool ROUTE, int NSH>
 __global__ __launch_bounds__(kDcThreads, 2) void k_dc_gate_up(DecodeParams p) {
   __shared__ DcGateUpShared sh;
   // one token: its row does not wait for the routing
@@ -775,14 +778,7 @@ __global__ __launch_bounds__(kDcThreads, 2) void k_dc_gate_up(DecodeParams p) {
   } else {
     dc_build(p, p.ids, p.wts, sh.tb, sh.bd);
   }
-  const int KS = p.ks_up, CS = kDcWaves / KS, nslab = p.I >> 4;
-  // two gate and two up slabs a unit where that still gives every workgroup
-  // one (four of each read the rows in runs too far apart: 344 against 321 us
-  // for 16 tokens of the 256-expert layer)
-  if ((int64_t)sh.tb.ntile * (nslab / (2 * CS)) >= kDcGrid)
-    dc_gate_up<F32, PIECES, WHOLE, 4>(p, sh, KS, raw);
-  else
-    dc_gate_up<F32, PIECES, WHOLE, 2>(p, sh, KS, raw);
+  dc_gate_up<F32, PIECES, WHOLE, NSH>(p, sh, p.ks_up, raw);
 }
 
 // ------------------------------------------------------------------- down
@@ -1132,8 +1128,15 @@ inline int64_t dc_tiles(const nvfp4_moe_decode_args_t* a) {
 inline int dc_groups(const nvfp4_moe_decode_args_t* a) {
   return a->x_dtype == NVFP4_IN_F32 ? DcShape<2>::NG : DcShape<1>::NG;
 }
+// ns: gate slabs of a wave's unit, with as many up slabs.  Two halve the
+// reductions, if every workgroup has a unit then (four would read the rows of a
+// long K in runs too far apart: 344 against 321 us for 16 tokens of the
+// 256-expert layer).
 inline DcSplit dc_split_up(const nvfp4_moe_decode_args_t* a) {
-  return dc_split((int)a->H, dc_groups(a), (int)(a->I >> 4), 1, 1, dc_tiles(a), kDcMaxTiles);
+  const int nslab = (int)(a->I >> 4);
+  DcSplit s = dc_split((int)a->H, dc_groups(a), nslab, 1, 1, dc_tiles(a), kDcMaxTiles);
+  if (dc_tiles(a) * (nslab / (2 * (kDcWaves / s.ks))) >= kDcGrid) s.ns = 2;
+  return s;
 }
 inline DcSplit dc_split_down(const nvfp4_moe_decode_args_t* a) {
   return dc_split((int)a->I, dc_groups(a), (int)(a->H >> 4), a->T <= 32 ? 4 : 2, 2, dc_tiles(a),
@@ -1171,11 +1174,11 @@ void dc_launch_down(const DecodeParams& p, hipStream_t s) {
                      s, p);
 }
 
-template <bool F32, bool WHOLE>
+template <bool F32, bool WHOLE, int NSH>
 void dc_launch_gate_up(const DecodeParams& p, hipStream_t s) {
   const dim3 grid(kDcGrid), wg(kDcThreads);
   if (p.T <= kDcInlineT && p.E <= kDcInlineE) {
-    hipLaunchKernelGGL((k_dc_gate_up<F32, F32 ? 2 : 1, WHOLE, true>), grid, wg, 0, s, p);
+    hipLaunchKernelGGL((k_dc_gate_up<F32, F32 ? 2 : 1, WHOLE, true, NSH>), grid, wg, 0, s, p);
     return;
   }
   const dim3 gt((unsigned)p.T);
@@ -1183,13 +1186,19 @@ void dc_launch_gate_up(const DecodeParams& p, hipStream_t s) {
   else if (p.E <= 128) hipLaunchKernelGGL(k_dc_route<2>, gt, dim3(64), 0, s, p);
   else if (p.E <= 256) hipLaunchKernelGGL(k_dc_route<4>, gt, dim3(64), 0, s, p);
   else hipLaunchKernelGGL(k_dc_route<16>, gt, dim3(64), 0, s, p);
-  hipLaunchKernelGGL((k_dc_gate_up<F32, F32 ? 2 : 1, WHOLE, false>), grid, wg, 0, s, p);
+  hipLaunchKernelGGL((k_dc_gate_up<F32, F32 ? 2 : 1, WHOLE, false, NSH>), grid, wg, 0, s, p);
 }
 
 template <bool F32>
-void dc_launch(const DecodeParams& p, int ns, hipStream_t s) {
-  if (p.H % 128 == 0) dc_launch_gate_up<F32, true>(p, s);
-  else dc_launch_gate_up<F32, false>(p, s);
+void dc_launch(const DecodeParams& p, int ns_up, int ns, hipStream_t s) {
+  const bool whole_h = p.H % 128 == 0;
+  if (ns_up == 2) {
+    if (whole_h) dc_launch_gate_up<F32, true, 4>(p, s);
+    else dc_launch_gate_up<F32, false, 4>(p, s);
+  } else {
+    if (whole_h) dc_launch_gate_up<F32, true, 2>(p, s);
+    else dc_launch_gate_up<F32, false, 2>(p, s);
+  }
   const bool whole = p.I % 128 == 0;
   if (ns == 4) {
     if (whole) dc_launch_down<F32, true, 4>(p, s);
@@ -1230,7 +1239,7 @@ int nvfp4_moe_decode(const nvfp4_moe_decode_args_t* a, void* ws, size_t ws_bytes
   NV_RETURN_IF(!ws || ws_bytes < l.bytes || !nv_aligned16(ws), NVFP4_ERR_WORKSPACE);
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   uint8_t* w = reinterpret_cast<uint8_t*>(ws);
-  const DcSplit down = dc_split_down(a);
+  const DcSplit up = dc_split_up(a), down = dc_split_down(a);
   const DecodeParams p{(int)a->T, (int)a->E, (int)a->k, (int)a->H, (int)a->I, a->x, a->ldx,
                        a->logits, a->ld_logits, a->gu_codes, a->gu_scales, a->gu_tscale,
                        a->d_codes, a->d_scales, a->d_tscale, a->out, a->ldo,
@@ -1239,9 +1248,9 @@ int nvfp4_moe_decode(const nvfp4_moe_decode_args_t* a, void* ws, size_t ws_bytes
                        reinterpret_cast<uint16_t*>(w + l.h), w + l.hexp,
                        reinterpret_cast<float*>(w + l.part),
                        reinterpret_cast<int32_t*>(w + l.count),
-                       down.blocks, dc_split_up(a).ks, down.ks};
-  if (a->x_dtype == NVFP4_IN_BF16) dc_launch<false>(p, down.ns, s);
-  else dc_launch<true>(p, down.ns, s);
+                       down.blocks, up.ks, down.ks};
+  if (a->x_dtype == NVFP4_IN_BF16) dc_launch<false>(p, up.ns, down.ns, s);
+  else dc_launch<true>(p, up.ns, down.ns, s);
   return nv_launch_status();
 }
 
