@@ -53,6 +53,7 @@ constexpr int kDcAcc = 2048;       // output sums of a wave of k_dc_down
 constexpr int kDcMaxParts = 16;
 __host__ __device__ inline int dc_pad(int I) { return (I + 127) & ~127; }
 
+struct DcRows;
 struct DecodeParams {
   int T, E, k, H, I;
   const void* x;
@@ -73,6 +74,7 @@ struct DecodeParams {
   uint8_t* hexp;
   float* part;  // [parts, T, H]
   int32_t* count;  // per column block of k_dc_down
+  DcRows* rows;  // the row tables for k_dc_down
   int blocks;      // column blocks
   int ks_up, ks_down;  // waves that share K (the others share the columns)
 };
@@ -190,7 +192,7 @@ __global__ __launch_bounds__(64) void k_dc_route(DecodeParams p) {
 }
 
 // --------------------------------------------------------- rows by expert
-// Every workgroup builds the same tables in LDS: the pairs with a weight, in
+// Every workgroup of the gate/up kernel builds the same tables in LDS: the pairs with a weight, in
 // (expert, token) order, cut into tiles of at most 16 rows of one expert.
 struct DcTables {
   uint32_t tile[kDcMaxTiles];   // expert << 16 | first row
@@ -199,17 +201,22 @@ struct DcTables {
   __device__ __forceinline__ int token(int row) const { return pair[row] & 63; }
   __device__ __forceinline__ int pair_of(int row) const { return pair[row] >> 6; }
 };
+// The same for k_dc_down, from the gate/up kernel's first workgroup.
+struct DcRows {
+  DcTables tb;
+  float wt[kDcMaxPairs];  // of a row: its weight times its expert's tensor scale
+};
 struct DcBuild {  // while building
   unsigned long long mask[kDcMaxE];  // tokens of an expert
   uint16_t base[kDcMaxE];            // its first row
   int wave_rows[kDcWaves], wave_tiles[kDcWaves];
 };
 
-// ids and weights: LDS or the workspace.  row_wt (nullable): each row's weight
-// times its expert's tensor scale ts.
+// ids and weights: LDS or the workspace.
 __device__ __forceinline__ void dc_build(const DecodeParams& p, const int32_t* ids,
-                                         const float* wts, DcTables& tb, DcBuild& bd,
-                                         float* row_wt = nullptr, const float* ts = nullptr) {
+                                         const float* wts, DcTables& tb, DcBuild& bd) {
+  const bool publish = blockIdx.x == 0;
+  DcRows* pub = p.rows;
   const int tid = threadIdx.x, P = p.T * p.k;
   if (p.T == 1) {  // a row and a tile for each slot, in slot order
     if (tid < 64) {
@@ -219,9 +226,16 @@ __device__ __forceinline__ void dc_build(const DecodeParams& p, const int32_t* i
         const int row = __popcll(bal & ((1ull << tid) - 1)), e = ids[tid];
         tb.tile[row] = ((uint32_t)e << 16) | (uint32_t)row;
         tb.pair[row] = (uint16_t)(tid << 6);
-        if (row_wt) row_wt[row] = wts[tid] * ts[e];
+        if (publish) {
+          pub->tb.tile[row] = tb.tile[row];
+          pub->tb.pair[row] = tb.pair[row];
+          pub->wt[row] = wts[tid] * p.d_ts[e];
+        }
       }
-      if (tid == 0) tb.ntile = tb.nrow = __popcll(bal);
+      if (tid == 0) {
+        tb.ntile = tb.nrow = __popcll(bal);
+        if (publish) pub->tb.ntile = pub->tb.nrow = __popcll(bal);
+      }
     }
     __syncthreads();
     return;
@@ -273,12 +287,20 @@ __device__ __forceinline__ void dc_build(const DecodeParams& p, const int32_t* i
   for (int j = 0; j < kPer; ++j) {
     const int e = tid * kPer + j;
     if (e < p.E) bd.base[e] = (uint16_t)r;
-    for (int i = 0; i < rows[j]; i += 16) tb.tile[t++] = ((uint32_t)e << 16) | (uint32_t)(r + i);
+    for (int i = 0; i < rows[j]; i += 16) {
+      const uint32_t tile = ((uint32_t)e << 16) | (uint32_t)(r + i);
+      if (publish) pub->tb.tile[t] = tile;
+      tb.tile[t++] = tile;
+    }
     r += rows[j];
   }
   if (tid == kDcThreads - 1) {
     tb.ntile = t;
     tb.nrow = r;
+    if (publish) {
+      pub->tb.ntile = t;
+      pub->tb.nrow = r;
+    }
   }
   __syncthreads();
 #pragma unroll
@@ -288,7 +310,10 @@ __device__ __forceinline__ void dc_build(const DecodeParams& p, const int32_t* i
       const unsigned long long before = (1ull << (i / p.k)) - 1;
       const int row = bd.base[e] + __popcll(bd.mask[e] & before);
       tb.pair[row] = (uint16_t)((i << 6) | (i / p.k));
-      if (row_wt) row_wt[row] = wts[i] * ts[e];
+      if (publish) {
+        pub->tb.pair[row] = tb.pair[row];
+        pub->wt[row] = wts[i] * p.d_ts[e];
+      }
     }
   }
   __syncthreads();
@@ -793,10 +818,7 @@ struct DcDownShared {
   uint8_t buf[kDcWaves][kDcDownRows * kDcRow];
   DcTables tb;
   float wt[kDcMaxPairs];  // of a row
-  union {
-    DcBuild bd;
-    __attribute__((aligned(16))) float acc[kDcWaves][kDcAcc];  // [token][NS * 16]
-  };
+  __attribute__((aligned(16))) float acc[kDcWaves][kDcAcc];  // [token][NS * 16]
   int last;
 };
 static_assert(2 * sizeof(DcDownShared) <= 160 * 1024 && 2 * sizeof(DcGateUpShared) <= 160 * 1024,
@@ -806,7 +828,16 @@ template <int PIECES, bool WHOLE, int NS, bool BF16>
 __global__ __launch_bounds__(kDcThreads, 2) void k_dc_down(DecodeParams p) {
   constexpr int NG = DcShape<PIECES>::NG;
   __shared__ DcDownShared sh;
-  dc_build(p, p.ids, p.wts, sh.tb, sh.bd, sh.wt, p.d_ts);
+  for (int i = threadIdx.x; i < p.T * p.k; i += kDcThreads) {  // no more rows or tiles than pairs
+    sh.tb.tile[i] = p.rows->tb.tile[i];
+    sh.tb.pair[i] = p.rows->tb.pair[i];
+    sh.wt[i] = p.rows->wt[i];
+  }
+  if (threadIdx.x == 0) {
+    sh.tb.ntile = p.rows->tb.ntile;
+    sh.tb.nrow = p.rows->tb.nrow;
+  }
+  __syncthreads();
   const int lane = threadIdx.x & 63, c = lane & 15, q = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int KS = p.ks_down, ks = wave % KS, cs = wave / KS, CS = kDcWaves / KS;
@@ -1144,7 +1175,7 @@ inline DcSplit dc_split_down(const nvfp4_moe_decode_args_t* a) {
 }
 
 struct DcLayout {
-  size_t ids, wts, count, h, hexp, part, bytes;
+  size_t ids, wts, count, rows, h, hexp, part, bytes;
 };
 inline DcLayout dc_layout(const nvfp4_moe_decode_args_t* a) {
   const size_t P = (size_t)(a->T * a->k);
@@ -1154,7 +1185,8 @@ inline DcLayout dc_layout(const nvfp4_moe_decode_args_t* a) {
   l.ids = 0;
   l.wts = l.ids + nv_round256(P * 4);
   l.count = l.wts + nv_round256(P * 4);
-  l.h = l.count + nv_round256((size_t)nb * 4);
+  l.rows = l.count + nv_round256((size_t)nb * 4);
+  l.h = l.rows + nv_round256(sizeof(DcRows));
   const size_t Ip = dc_pad((int)a->I);
   l.hexp = l.h + nv_round256(P * Ip * (a->x_dtype == NVFP4_IN_F32 ? 4 : 2));
   l.part = l.hexp + nv_round256(P * (Ip / 16));
@@ -1248,6 +1280,7 @@ int nvfp4_moe_decode(const nvfp4_moe_decode_args_t* a, void* ws, size_t ws_bytes
                        reinterpret_cast<uint16_t*>(w + l.h), w + l.hexp,
                        reinterpret_cast<float*>(w + l.part),
                        reinterpret_cast<int32_t*>(w + l.count),
+                       reinterpret_cast<DcRows*>(w + l.rows),
                        down.blocks, up.ks, down.ks};
   if (a->x_dtype == NVFP4_IN_BF16) dc_launch<false>(p, up.ns, down.ns, s);
   else dc_launch<true>(p, up.ns, down.ns, s);
