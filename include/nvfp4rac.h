@@ -402,7 +402,7 @@ int fp8_grouped_gemm(const fp8_gemm_args_t* args, void* stream);
  *                      lower expert index, in (logit desc, index asc) order;
  *   topk_weights[t, s] softmax(l) at that expert (not renormalized), 0 where
  *                      the logit is -inf;
- *   out[t, :] = sum over slots s with weight > 0, in slot order, of
+ *   out[t, :] = sum over slots s with weight > 0 of
  *      topk_weights[t, s] * s_d[e] * W_d[e] h,
  *      h = silu(g) * u,  [g; u] = s_gu[e] * W_gu[e] x[t, :]
  * with W the exact dequantized values g * s_b.  A slot of weight 0 costs
@@ -419,8 +419,10 @@ int fp8_grouped_gemm(const fp8_gemm_args_t* args, void* stream);
  * nullable.  Requires 0 <= T <= 64, 1 <= k <= min(E, 16), E <= 1024, H and I
  * multiples of 32 up to 65536, ldx and ldo multiples of 8, x, out, codes and
  * scales 16-byte aligned, ws 16-byte aligned.  Inputs and out may not
- * overlap.  Finite x is a precondition for the row it is in only.  The
- * result is deterministic.  With T == 0 nothing is enqueued.
+ * overlap.  Finite x is a precondition for the row it is in only; logits of
+ * +inf give their row NaN weights, and such slots are left out of the sum.
+ * The result is deterministic (sums in a fixed order).  With T == 0 nothing
+ * is enqueued.
  * ------------------------------------------------------------------------ */
 typedef struct {
   int64_t T, E, k, H, I;

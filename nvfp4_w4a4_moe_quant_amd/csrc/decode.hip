@@ -6,14 +6,22 @@
 // the activations are, so this path multiplies unquantized activations and
 // needs neither the quantizer nor the residual pass.
 //
-//   k_dc_route    one wave per token: top-k, softmax weights (only where the
+//   k_dc_route    one wave per token: top-k, softmax weights (where the
 //                 gate/up kernel does not route by itself)
-//   k_dc_gate_up  routing (few tokens), then h = silu(g) u of every routed
-//                 (token, slot) pair, FP32 in the workspace
+//   k_dc_gate_up  tables of the routed rows by expert, then h = silu(g) u of
+//                 every routed (token, slot) pair, to the workspace
 //   k_dc_down     the down product, weighted and summed over each token's
 //                 experts, to the output
 //
-// Both products stream W once, straight into registers in the layout of
+// Both products stream W once, 0.5625 bytes a weight, and that is what bounds
+// them: 16 tokens of a layer of 256 experts, H 7168, I 2048 (103 experts, 1.70
+// and 0.85 GB) take 321 and 157-178 us, 5.3 and 4.8-5.4 TB/s where a large
+// copy reaches 4.9 on this card; the same with the arithmetic taken out takes
+// as long.  One token (8 experts) takes 31 and 20 us: some 8 us of the first
+// and 5 us of the second pass before the stream runs (routing 3, first loads
+// 4), which is all of it in small layers (128 experts, H 2048, I 768: 11 and
+// 10 us, 16 tokens 67 us for 47 us of bytes).
+//
 // v_mfma_f32_16x16x32_f16 (16 tokens x 16 columns): lane (c, q) of a wave
 // takes column c and, of each group of 128 k, the 16 code bytes of k = 32 q ..
 // 32 q + 31 for four MFMA steps of 8 k -- the same permutation of k for both
@@ -21,9 +29,10 @@
 // row's values in one K range are scaled by a power of two to just below
 // 2^15, so that one piece holds a bf16 value exactly (down to 2^-29 of the
 // largest) and two hold 22 bits of an FP32 value; the FP32 sums of the range
-// are scaled back.  A wave stages the rows of its K range through a small LDS
-// buffer of its own and keeps the fragments in registers for every column of
-// its work; W loads run two column slabs ahead of their use.
+// are scaled back.  h goes from one product to the other in the same form
+// (rounded to 11 bits for bf16, an eighth of bf16's step; to 22 for FP32).  A
+// wave keeps the fragments of its rows in registers for every column of its
+// work; W loads run two column slabs ahead of their use.
 #include "common.h"
 
 namespace {
@@ -645,7 +654,11 @@ struct DcGateUpShared {
 };
 
 // Units of (tile, column block): a wave takes NSH / 2 gate slabs and their up
-// slabs over its share of K (ks of KS) and column share (cs of CS).
+// slabs over its share of K (ks of KS) and column share (cs of CS); the K
+// shares meet in LDS at the unit's end, where h is computed, scaled by its
+// largest value in 16 columns and stored where k_dc_down's lanes want it.
+// Consecutive units of a workgroup mostly have the same rows, which stay in
+// registers where K is one range.
 template <bool F32, int PIECES, bool WHOLE, int NSH>
 __device__ __forceinline__ void dc_gate_up(const DecodeParams& p, DcGateUpShared& sh, int KS,
                                            DcRaw<F32, PIECES>& raw) {
@@ -807,7 +820,7 @@ __global__ __launch_bounds__(kDcThreads, 2) void k_dc_gate_up(DecodeParams p) {
 }
 
 // ------------------------------------------------------------------- down
-// A workgroup owns a block of output columns and walks the tiles of its
+// A workgroup owns a block of output columns and walks the row tiles of its
 // part: W streams without a break, a tile's sums go to the tokens' rows of an
 // LDS accumulator of each wave, and nothing is synchronized until the end.
 // Where the column blocks alone do not fill the chip the tiles are split into

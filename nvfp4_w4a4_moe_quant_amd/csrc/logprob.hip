@@ -9,8 +9,16 @@
 //   entropy = ln 2 (log2 S - Q / S).
 // Base 2 saves the multiplication inside every exponential.  The difference
 // comes before the product, so that logits at the type's lowest value (a mask
-// that is a number) do not overflow.  Reported log-probabilities are
-// (l_j - m) inv_temperature - ln 2 log2 S.
+// that is a number) do not overflow, and the row's maximum gives exactly 1.
+// Reported log-probabilities are (l_j - m) inv_temperature - ln 2 log2 S.
+//
+// The forward pass is bound by reading the logits where there are rows enough:
+// 4096 x 131072 bf16 with 8 alternatives 195 us, 5.5 TB/s (a large copy reaches
+// 4.9 here); its arithmetic, of which a quarter-rate exponential per logit is
+// the largest part, takes about two thirds of that.  A single row is bound by
+// the arithmetic of the CU that it is on, and by latency: 1 x 32768 with 5
+// alternatives 8 us.  The backward pass reads and writes 2048 x 131072 in 165
+// us, 6.5 TB/s.
 #include "common.h"
 
 namespace {
