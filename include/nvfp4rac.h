@@ -480,7 +480,9 @@ int nvfp4_moe_decode(const nvfp4_moe_decode_args_t* args, void* ws, size_t ws_by
  *                                       - b p_j (log p_j + entropy[t]) )
  * with a = grad_logprobs[t] (0 where NULL, where y < 0, or where the whole
  * row is masked) and b = grad_entropy[t] (0 where NULL), rounded once to the
- * logits' dtype; 0 for masked tokens, NaN for a row with y >= V.  targets is
+ * logits' dtype; 0 for masked tokens, NaN for a row with y >= V.  A row with
+ * a = b = 0 (an ignored position without an entropy gradient) gets 0 and its
+ * logits are not read, whatever they are.  targets is
  * required with grad_logprobs, entropy with grad_entropy.  grad_logits has
  * row stride ldg >= V and may be the logits themselves (same ld).  No
  * workspace.

@@ -616,8 +616,10 @@ __global__ __launch_bounds__(NT) void k_logprob_bwd(
     const bool empty = L == -kInf;
     const int64_t y = targets ? targets[t] : -1;
     float a = (g_lp && y >= 0 && !empty) ? g_lp[t] : 0.0f;
-    if ((g_lp && y >= V) || L != L) a = __builtin_nanf("");
     const float b = (g_ent && !empty) ? g_ent[t] : 0.0f;
+    const bool wrong = g_lp && y >= V;
+    const bool none = a == 0.0f && b == 0.0f && !wrong;  // zeros; the logits are not read
+    if (wrong || (L != L && !none)) a = __builtin_nanf("");
     const float k0 = -it * (a + (g_ent && !empty ? b * entropy[t] : 0.0f)), k1 = -it * kLn2 * b;
     const float Lf = empty ? kInf : L;
     auto value = [&](float l) {
@@ -625,7 +627,7 @@ __global__ __launch_bounds__(NT) void k_logprob_bwd(
       return __builtin_amdgcn_exp2f(d) * __builtin_fmaf(k1, d, k0);
     };
     auto one = [&](int j) {
-      const float g = value(LE::load(row + j));
+      const float g = none ? 0.0f : value(LE::load(row + j));
       LE::store(out + j, j == y ? __builtin_fmaf(it, a, g) : g);
     };
     if constexpr (!VEC) {
@@ -638,6 +640,14 @@ __global__ __launch_bounds__(NT) void k_logprob_bwd(
       const uint4* vec = reinterpret_cast<const uint4*>(row + head);
       uint4* dst = reinterpret_cast<uint4*>(out + head);
       for (int i0 = blockIdx.x * (NT * kLpBwdU); i0 < nv; i0 += gridDim.x * (NT * kLpBwdU)) {
+        if (none) {
+#pragma unroll
+          for (int u = 0; u < kLpBwdU; ++u) {
+            const int i = i0 + u * NT + threadIdx.x;
+            if (i < nv) dst[i] = make_uint4(0, 0, 0, 0);
+          }
+          continue;
+        }
         uint4 x[kLpBwdU];
 #pragma unroll
         for (int u = 0; u < kLpBwdU; ++u) {

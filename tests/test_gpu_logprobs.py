@@ -115,6 +115,49 @@ def test_masks(dtype):
         check(z, y, it, 8)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_masks_of_the_lowest_value(dtype):
+    """Tokens masked with the type's lowest number instead of -inf, some rows
+    with fewer live tokens than alternatives."""
+    say(f"logprobs masked by the lowest value {dtype}")
+    for V in (700, 40001, 131072):
+        z, y, _ = _case(V + 1, 6, V, dtype)
+        low = torch.finfo(z.dtype).min
+        z[torch.rand(6, V, device=DEV, generator=torch.Generator(device=DEV).manual_seed(V)) < 0.6] = low
+        z[2, 3:] = low
+        z[3, 1:] = float("-inf")
+        z[4, y[4]] = low
+        check(z, y, None, 8)
+        check(z, y, np.array([1, .5, .25, 1, .75, 1], np.float32), 8)
+        r = L.token_logprobs(z, up(y))
+        g = L.token_logprobs_backward(z, up(y), r.norm, r.entropy, torch.ones(6, device=DEV),
+                                      torch.ones(6, device=DEV))
+        want, tol = R.log_probs_grad(R.log_probs(host(z.float()), y, None, 0), y, None, np.ones(6),
+                                     np.ones(6), dtype)
+        near(g.float(), want, tol, "gradient")
+
+
+def test_ignored_rows_are_not_read():
+    """Ignored positions without an entropy gradient get a gradient of 0 even
+    where their logits are NaN; the other rows are what they are alone."""
+    say("logprobs gradient of ignored rows")
+    for V in (77, 5000):
+        z, y, _ = _case(V, 5, V, "bf16")
+        y[1], y[3] = -100, -1
+        z[1], z[3, 5] = float("nan"), float("inf")
+        r = L.token_logprobs(z, up(y))
+        ga = torch.randn(5, device=DEV)
+        g = L.token_logprobs_backward(z, up(y), r.norm, None, ga)
+        assert (g[[1, 3]] == 0).all() and (r.logprobs[[1, 3]] == 0).all()
+        keep = [0, 2, 4]
+        alone = L.token_logprobs_backward(z[keep].contiguous(), up(y[keep]),
+                                          r.norm[keep].contiguous(), None, ga[keep])
+        assert torch.equal(g[keep], alone) and torch.isfinite(alone).all()
+        odd = torch.full((5, V + 1), 7.0, dtype=z.dtype, device=DEV)
+        L.token_logprobs_backward(z, up(y), r.norm, None, ga, out=odd[:, 1:])
+        assert torch.equal(odd[:, 1:], g) and (odd[:, 0] == 7).all()
+
+
 def test_invalid_targets_and_numbers():
     say("logprobs: targets outside the vocabulary, NaN and inf logits")
     z, y, _ = _case(3, 6, 5000, "f32")
