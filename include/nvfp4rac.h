@@ -421,8 +421,9 @@ int fp8_grouped_gemm(const fp8_gemm_args_t* args, void* stream);
  * scales 16-byte aligned, ws 16-byte aligned.  Inputs and out may not
  * overlap.  Finite x is a precondition for the row it is in only; logits of
  * +inf give their row NaN weights, and such slots are left out of the sum.
- * The result is deterministic (sums in a fixed order).  With T == 0 nothing
- * is enqueued.
+ * The result is deterministic (sums in a fixed order).  Calls that may
+ * overlap (on two streams, in two graphs) need workspaces and outputs of their
+ * own.  With T == 0 nothing is enqueued.
  * ------------------------------------------------------------------------ */
 typedef struct {
   int64_t T, E, k, H, I;
@@ -471,9 +472,10 @@ int nvfp4_moe_decode(const nvfp4_moe_decode_args_t* args, void* ws, size_t ws_by
  * alignment beyond the element's).  targets and logprobs are given together
  * or both NULL; entropy, norm and inv_temperature are nullable; top_ids and
  * top_logprobs are required if top_k > 0.  inv_temperature must be positive
- * and finite.  Requires 1 <= V < 2^31, 0 <= top_k <= min(V, 32), T < 2^31.
- * ws may be NULL where its size is 0.  Sums are FP32; the result is
- * deterministic.
+ * and finite.  Requires 1 <= V <= 2^30, 0 <= top_k <= min(V, 32), T < 2^24,
+ * arrays aligned to their elements.  ws may be NULL where its size is 0; calls
+ * that may overlap need workspaces of their own.  Sums are FP32; the result
+ * is deterministic.
  *
  * token_logprobs_backward -- the gradient of the logits:
  *   grad[t, j] = inv_temperature[t] * ( a ([j = y] - p_j)
@@ -482,10 +484,10 @@ int nvfp4_moe_decode(const nvfp4_moe_decode_args_t* args, void* ws, size_t ws_by
  * row is masked) and b = grad_entropy[t] (0 where NULL), rounded once to the
  * logits' dtype; 0 for masked tokens, NaN for a row with y >= V.  A row with
  * a = b = 0 (an ignored position without an entropy gradient) gets 0 and its
- * logits are not read, whatever they are.  targets is
- * required with grad_logprobs, entropy with grad_entropy.  grad_logits has
- * row stride ldg >= V and may be the logits themselves (same ld).  No
- * workspace.
+ * logits are not read, whatever they are.  targets is required with
+ * grad_logprobs, entropy with grad_entropy.  grad_logits has row stride ldg
+ * >= V and may be the logits themselves (same ld), but not overlap them in
+ * another way.  The forward call's limits hold.  No workspace.
  * ------------------------------------------------------------------------ */
 size_t token_logprobs_workspace_size(int64_t T, int64_t V, int64_t top_k);
 int token_logprobs(const void* logits, int dtype, int64_t T, int64_t V, int64_t ld,

@@ -24,6 +24,8 @@
 namespace {
 
 constexpr int kLpMaxTop = 32;
+constexpr int64_t kLpMaxV = 1 << 30;        // element indexes with room for a step behind the row
+constexpr int64_t kLpMaxT = (1 << 24) - 1;  // a launch has less than 2^32 threads
 constexpr int kLpCand = 128;   // candidates that are ranked at a time
 constexpr int kLpPieces = 512; // pieces of a row that wait for the ranking
 constexpr float kLpLowest = -3.402823466e38f;  // masked tokens (-inf) are below it
@@ -735,6 +737,12 @@ int lp_launch(const LpCall& a, hipStream_t s) {
   return nv_launch_status();
 }
 
+// Some array of 32-bit elements is not 4-byte aligned.
+template <typename... P>
+bool lp_misaligned(P... p) {
+  return ((reinterpret_cast<uintptr_t>(p) | ...) & 3) != 0;
+}
+
 struct LpGradCall {
   const void* logits;
   int64_t T;
@@ -772,7 +780,7 @@ int lp_launch_bwd(const LpGradCall& a, hipStream_t s) {
 extern "C" {
 
 size_t token_logprobs_workspace_size(int64_t T, int64_t V, int64_t top_k) {
-  if (T < 1 || T > INT32_MAX || V < 1 || V > INT32_MAX || top_k < 0 || top_k > kLpMaxTop) return 0;
+  if (T < 1 || T > kLpMaxT || V < 1 || V > kLpMaxV || top_k < 0 || top_k > kLpMaxTop) return 0;
   const int parts = lp_parts(T, V);
   return parts > 1 ? nv_round256((size_t)T * parts * lp_part_bytes((int)top_k)) : 0;
 }
@@ -782,7 +790,7 @@ int token_logprobs(const void* logits, int dtype, int64_t T, int64_t V, int64_t 
                    float* logprobs, float* entropy, float* norm, int32_t* top_ids,
                    float* top_logprobs, void* ws, size_t ws_bytes, void* stream) {
   NV_RETURN_IF(dtype != NVFP4_IN_F32 && dtype != NVFP4_IN_BF16, NVFP4_ERR_DTYPE);
-  NV_RETURN_IF(T < 0 || T > INT32_MAX || V < 1 || V > INT32_MAX || ld < V || top_k < 0 ||
+  NV_RETURN_IF(T < 0 || T > kLpMaxT || V < 1 || V > kLpMaxV || ld < V || top_k < 0 ||
                    top_k > kLpMaxTop || top_k > V,
                NVFP4_ERR_SHAPE);
   if (T == 0) return NVFP4_OK;
@@ -791,7 +799,7 @@ int token_logprobs(const void* logits, int dtype, int64_t T, int64_t V, int64_t 
                NVFP4_ERR_NULL);
   NV_RETURN_IF((reinterpret_cast<uintptr_t>(logits) & (dtype == NVFP4_IN_F32 ? 3 : 1)) ||
                    (reinterpret_cast<uintptr_t>(targets) & 7) ||
-                   (reinterpret_cast<uintptr_t>(inv_temperature) & 3),
+                   lp_misaligned(inv_temperature, logprobs, entropy, norm, top_ids, top_logprobs),
                NVFP4_ERR_ALIGN);
   const size_t need = token_logprobs_workspace_size(T, V, top_k);
   NV_RETURN_IF((need && !ws) || ws_bytes < need || (reinterpret_cast<uintptr_t>(ws) & 15),
@@ -809,7 +817,7 @@ int token_logprobs_backward(const void* logits, int dtype, int64_t T, int64_t V,
                             const float* grad_entropy, void* grad_logits, int64_t ldg,
                             void* stream) {
   NV_RETURN_IF(dtype != NVFP4_IN_F32 && dtype != NVFP4_IN_BF16, NVFP4_ERR_DTYPE);
-  NV_RETURN_IF(T < 0 || T > INT32_MAX || V < 1 || V > INT32_MAX || ld < V || ldg < V ||
+  NV_RETURN_IF(T < 0 || T > kLpMaxT || V < 1 || V > kLpMaxV || ld < V || ldg < V ||
                    (logits == grad_logits && ld != ldg),
                NVFP4_ERR_SHAPE);
   if (T == 0) return NVFP4_OK;
@@ -820,7 +828,7 @@ int token_logprobs_backward(const void* logits, int dtype, int64_t T, int64_t V,
   NV_RETURN_IF((reinterpret_cast<uintptr_t>(logits) & mask) ||
                    (reinterpret_cast<uintptr_t>(grad_logits) & mask) ||
                    (reinterpret_cast<uintptr_t>(targets) & 7) ||
-                   (reinterpret_cast<uintptr_t>(norm) & 7),
+                   lp_misaligned(inv_temperature, norm, entropy, grad_logprobs, grad_entropy),
                NVFP4_ERR_ALIGN);
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   const LpGradCall a{logits, T, (int)V, ld, targets, inv_temperature, norm, entropy,

@@ -216,15 +216,16 @@ class GraphedMoEDecode:
         if self.x.shape != (T, wgu.K) or self.x.dtype != x_dtype or self.logits.shape != (T, E):
             raise ValueError("x [T, H] of x_dtype and logits [T, E]")
         args = (wgu, wd, topk)
-        side = torch.cuda.Stream(device)
-        side.wait_stream(torch.cuda.current_stream(device))
-        with torch.cuda.stream(side):
-            for _ in range(warmup):
-                moe_decode(self.x, self.logits, *args)
-        torch.cuda.current_stream(device).wait_stream(side)
-        self.graph = torch.cuda.CUDAGraph()
-        with torch.cuda.graph(self.graph):
-            self.out = moe_decode(self.x, self.logits, *args)
+        with torch.cuda.device(device):
+            side = torch.cuda.Stream()
+            side.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(side):
+                for _ in range(warmup):
+                    moe_decode(self.x, self.logits, *args)
+            torch.cuda.current_stream().wait_stream(side)
+            self.graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(self.graph):
+                self.out = moe_decode(self.x, self.logits, *args)
 
     def __call__(self, x: Optional[torch.Tensor] = None,
                  logits: Optional[torch.Tensor] = None) -> L.MoEDecodeOut:

@@ -78,6 +78,24 @@ def test_logprobs_refusals(lib, want, kw):
     assert _fwd(lib, **kw) == want
 
 
+@pytest.mark.parametrize("want,kw", [
+    (ESHAPE, dict(T=2 ** 24)), (ESHAPE, dict(V=2 ** 30 + 1, ld=2 ** 31)),
+    (EALIGN, dict(ent=FAKE + 2)), (EALIGN, dict(norm=FAKE + 1)), (EALIGN, dict(ids=FAKE + 2)),
+    (EALIGN, dict(it=FAKE + 2)),
+])
+def test_logprobs_limits_and_alignment(lib, want, kw):
+    assert _fwd(lib, **kw) == want
+
+
+@pytest.mark.parametrize("want,kw", [
+    (ESHAPE, dict(T=2 ** 24)), (ESHAPE, dict(V=2 ** 30 + 1, ld=2 ** 31, ldg=2 ** 31)),
+    (EALIGN, dict(ga=FAKE + 2)), (EALIGN, dict(gb=FAKE + 1)), (EALIGN, dict(ent=FAKE + 2)),
+    (EALIGN, dict(norm=FAKE + 2)),
+])
+def test_logprobs_backward_limits_and_alignment(lib, want, kw):
+    assert _bwd(lib, **kw) == want
+
+
 def _bwd(lib, logits=FAKE, dtype=1, T=4, V=100, ld=100, y=FAKE, it=None, norm=FAKE, ent=FAKE,
          ga=FAKE, gb=FAKE, g=2 * FAKE, ldg=100):
     return lib.token_logprobs_backward(logits, dtype, T, V, ld, y, it, norm, ent, ga, gb, g, ldg,

@@ -287,6 +287,32 @@ def test_rows_beyond_32_bit_offsets():
     assert torch.equal(z[rows], want)
 
 
+def test_more_rows_than_a_grid_dimension():
+    """70001 short rows: past the 65535 of a grid's second dimension."""
+    say("logprobs: 70001 x 33")
+    T, V = 70001, 33
+    z, y, it = _case(12, T, V, "bf16")
+    r, ref = check(z, y, it, 2)
+    ga = np.random.default_rng(3).standard_normal(T).astype(np.float32)
+    g = L.token_logprobs_backward(z, up(y), r.norm, r.entropy, up(ga), up(ga[::-1]),
+                                  inv_temperature=up(it))
+    want, tol = R.log_probs_grad(ref, y, it, ga, ga[::-1], "bf16")
+    near(g.float(), want, tol, "gradient")
+
+
+def test_one_long_row():
+    """A row of 2^24 + 9 tokens in 64 parts, at an odd address."""
+    say("logprobs: 1 x 16777225")
+    V = 2 ** 24 + 9
+    z = torch.empty(V + 3, dtype=torch.bfloat16, device=DEV)
+    z.normal_(generator=torch.Generator(device=DEV).manual_seed(4))
+    z = z[3:].view(1, V)
+    z[0, V - 2] = 9.0
+    y = np.array([V - 1])
+    r, _ = check(z, y, None, 20)
+    assert int(r.top_ids[0, 0]) == V - 2
+
+
 def test_repeatable_on_streams_and_graphs():
     say("logprobs: streams and graphs")
     cases = [_case(40 + i, 9, 40000, "bf16") for i in range(3)]
