@@ -34,6 +34,8 @@
 // (rounded to 11 bits for bf16, an eighth of bf16's step; to 22 for FP32).  A
 // wave keeps the fragments of its rows in registers for every column of its
 // work; W loads run two column slabs ahead of their use.
+#include <cmath>
+
 #include "common.h"
 
 namespace {
@@ -1125,22 +1127,65 @@ __global__ __launch_bounds__(kDcThreads, 2) void k_dc_down(DecodeParams p) {
 }
 
 
-// How the four waves of a workgroup divide its work: KS of them share K, and
-// the 4 / KS groups take ns slabs each.  The fewer K ranges are padded the
-// better, and larger blocks read the rows of activations less often; but what
-// costs most is workgroups without work, so the choice is the first that
-// gives at least 7 of 8 workgroups some (32 a tile where there are few tiles:
-// one token of the 128-expert layer takes 12.1 us for its down product with
-// 64), in that order, or the one that keeps most busy.  tiles: an upper bound of the row tiles, which only the device
-// knows.
+// How the four waves of a workgroup divide its work: ks of them share K, and
+// the 4 / ks groups take ns slabs each; column blocks, and parts of the tiles.
 struct DcSplit {
   int ks, ns, blocks, parts;
 };
-inline DcSplit dc_split(int K, int NG, int nslab, int ns_most, int ns_least, int64_t tiles,
-                        int max_parts) {
-  const int ng = (K + 127) / 128;
+inline int64_t dc_tiles(const nvfp4_moe_decode_args_t* a) {
+  const int64_t P = a->T * a->k, few = a->E + P / 16;
+  return P < few ? P : few;
+}
+inline int dc_groups(const nvfp4_moe_decode_args_t* a) {
+  return a->x_dtype == NVFP4_IN_F32 ? DcShape<2>::NG : DcShape<1>::NG;
+}
+// Row tiles that the routing will likely give: an even choice's mean, and a
+// tenth more for its spread.
+inline double dc_likely_tiles(const nvfp4_moe_decode_args_t* a) {
+  const double P = (double)(a->T * a->k), E = (double)a->E;
+  if (a->T == 1) return P;
+  const double touched = E * (1.0 - std::pow(1.0 - (double)a->k / E, (double)a->T)) + P / 32;
+  return 1.1 * (touched < P ? touched : P);
+}
+// How the gate/up kernel divides a tile's work: KS waves of a workgroup share
+// K, and the 4 / KS groups take ns gate slabs (with as many up slabs) of a unit
+// each.  A workgroup takes one unit or, of u on average, u + 1/2 (units are
+// whole), and a unit costs its K ranges times its slabs and half a slab for the
+// rows.  Over 22 layers (7 to 256 experts, H 416 to 7168, I 96 to 14336, 1 to 64
+// tokens) the least such cost is within 3% of the fastest of the six choices,
+// 0.5% on average; the fewest padded K ranges alone cost up to 1.4 times as
+// much (49 tokens, 166 experts, H 5280, I 224: 173 against 127 us).  Larger
+// units than ns = 2 would read the rows of a long K in runs too far apart: 344
+// against 321 us for 16 tokens of the 256-expert layer.
+inline DcSplit dc_split_up(const nvfp4_moe_decode_args_t* a) {
+  const int nslab = (int)(a->I >> 4), ng = (int)((a->H + 127) / 128), NG = dc_groups(a);
+  DcSplit best{4, 1, 0, 0};
+  double least = 0.0;
+  for (int ks = kDcWaves; ks >= 1; ks /= 2)
+    for (int ns = 1; ns <= 2; ++ns) {
+      const int spu = ns * (kDcWaves / ks), ranges = (ng + NG * ks - 1) / (NG * ks);
+      const double u = dc_likely_tiles(a) * ((nslab + spu - 1) / spu) / kDcGrid;
+      const double cost = (u <= 1.0 ? 1.0 : u + 0.5) * ranges * (2 * ns + 0.5);
+      if (least == 0.0 || cost < least) {
+        least = cost;
+        best = DcSplit{ks, ns, 0, 0};
+      }
+    }
+  return best;
+}
+// The down kernel: the fewer K ranges are padded the better, and larger blocks
+// read the rows of activations less often; but what costs most is workgroups
+// without work, so the choice is the first that gives at least 7 of 8
+// workgroups some (32 a tile where there are few tiles: one token of the
+// 128-expert layer takes 12.1 us for its down product with 64), in that order,
+// or the one that keeps most busy: within 3% of the fastest choice over the
+// layers above, 10% for the smallest.  It counts on the most tiles there can
+// be, since the workspace holds the parts.
+inline DcSplit dc_split_down(const nvfp4_moe_decode_args_t* a) {
+  const int NG = dc_groups(a), ng = (int)((a->I + 127) / 128), nslab = (int)(a->H >> 4);
+  const int64_t tiles = dc_tiles(a);
   int64_t padded[3];
-  int order[3] = {0, 1, 2};  // KS = 4, 2, 1
+  int order[3] = {0, 1, 2};  // ks = 4, 2, 1
   for (int i = 0; i < 3; ++i) {
     const int ks = kDcWaves >> i;
     padded[i] = (int64_t)((ng + NG * ks - 1) / (NG * ks)) * ks;
@@ -1150,16 +1195,16 @@ inline DcSplit dc_split(int K, int NG, int nslab, int ns_most, int ns_least, int
       order[j - 1] = t;
     }
   }
-  DcSplit best{1, ns_least, 1, 1};
+  DcSplit best{1, 2, 1, 1};
   const int64_t enough = tiles * 32 < kDcGrid * 7 / 8 ? tiles * 32 : kDcGrid * 7 / 8;
   int64_t most = -1;
   for (int i = 0; i < 3; ++i)
-    for (int ns = ns_most; ns >= ns_least; ns /= 2) {
+    for (int ns = a->T <= 32 ? 4 : 2; ns >= 2; ns /= 2) {  // accumulators: T ns <= 128
       DcSplit o{kDcWaves >> order[i], ns, 0, 0};
       const int spu = ns * (kDcWaves / o.ks);
       o.blocks = (nslab + spu - 1) / spu;
-      int64_t parts = max_parts < tiles ? max_parts : tiles;
-      if (max_parts < kDcMaxTiles && parts > kDcGrid / o.blocks) parts = kDcGrid / o.blocks;
+      int64_t parts = kDcMaxParts < tiles ? kDcMaxParts : tiles;
+      if (parts > kDcGrid / o.blocks) parts = kDcGrid / o.blocks;
       o.parts = (int)(parts < 1 ? 1 : parts);
       const int64_t work = (int64_t)o.blocks * o.parts;
       if (work >= enough) return o;
@@ -1169,27 +1214,6 @@ inline DcSplit dc_split(int K, int NG, int nslab, int ns_most, int ns_least, int
       }
     }
   return best;
-}
-inline int64_t dc_tiles(const nvfp4_moe_decode_args_t* a) {
-  const int64_t P = a->T * a->k, few = a->E + P / 16;
-  return P < few ? P : few;
-}
-inline int dc_groups(const nvfp4_moe_decode_args_t* a) {
-  return a->x_dtype == NVFP4_IN_F32 ? DcShape<2>::NG : DcShape<1>::NG;
-}
-// ns: gate slabs of a wave's unit, with as many up slabs.  Two halve the
-// reductions, if every workgroup has a unit then (four would read the rows of a
-// long K in runs too far apart: 344 against 321 us for 16 tokens of the
-// 256-expert layer).
-inline DcSplit dc_split_up(const nvfp4_moe_decode_args_t* a) {
-  const int nslab = (int)(a->I >> 4);
-  DcSplit s = dc_split((int)a->H, dc_groups(a), nslab, 1, 1, dc_tiles(a), kDcMaxTiles);
-  if (dc_tiles(a) * (nslab / (2 * (kDcWaves / s.ks))) >= kDcGrid) s.ns = 2;
-  return s;
-}
-inline DcSplit dc_split_down(const nvfp4_moe_decode_args_t* a) {
-  return dc_split((int)a->I, dc_groups(a), (int)(a->H >> 4), a->T <= 32 ? 4 : 2, 2, dc_tiles(a),
-                  kDcMaxParts);
 }
 
 struct DcLayout {
