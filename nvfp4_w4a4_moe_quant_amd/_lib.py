@@ -541,11 +541,11 @@ def nvfp4_moe_decode(x: torch.Tensor, logits: torch.Tensor, wgu: NVFP4, wd: NVFP
     _nvfp4_experts(wgu, E, 2 * I, H, dev, "wgu")
     _nvfp4_experts(wd, E, H, I, dev, "wd")
     if out is None:
-        out = torch.empty((T, H), dtype=x.dtype, device=dev)
+        out = torch.empty(T, H, dtype=x.dtype, device=dev)
     elif out.shape != x.shape or out.dtype != x.dtype or out.device != dev:
         _refuse("out like x")
-    ids = torch.empty((T, k), dtype=torch.int32, device=dev)
-    wts = torch.empty((T, k), dtype=torch.float32, device=dev)
+    ids = torch.empty(T, k, dtype=torch.int32, device=dev)
+    wts = torch.empty(T, k, dtype=torch.float32, device=dev)
     args = MoEDecodeArgs(
         T, E, k, H, I, x.data_ptr(), xd, _row_stride(x, "x"),
         logits.data_ptr(), _row_stride(logits, "logits"),
@@ -576,9 +576,9 @@ def token_logprobs(logits: torch.Tensor, targets: Optional[torch.Tensor] = None,
     it = _vector(inv_temperature, T, torch.float32, dev, "inv_temperature")
     lp = torch.empty(T, dtype=torch.float32, device=dev) if targets is not None else None
     ent = torch.empty(T, dtype=torch.float32, device=dev)
-    norm = torch.empty((T, 2), dtype=torch.float32, device=dev)
-    ids = torch.empty((T, top_k), dtype=torch.int32, device=dev) if top_k > 0 else None
-    tlp = torch.empty((T, top_k), dtype=torch.float32, device=dev) if top_k > 0 else None
+    norm = torch.empty(T, 2, dtype=torch.float32, device=dev)
+    ids = torch.empty(T, top_k, dtype=torch.int32, device=dev) if top_k > 0 else None
+    tlp = torch.empty(T, top_k, dtype=torch.float32, device=dev) if top_k > 0 else None
     L = lib()
     n = L.token_logprobs_workspace_size(T, V, top_k)
     ws = _ws(n, dev) if n else None
@@ -614,7 +614,7 @@ def token_logprobs_backward(logits: torch.Tensor, targets: Optional[torch.Tensor
     if norm.shape != (T, 2) or norm.dtype != f32 or norm.device != dev or not norm.is_contiguous():
         _refuse("norm: float32 [T, 2]")
     if out is None:
-        out = torch.empty((T, V), dtype=logits.dtype, device=dev)
+        out = torch.empty(T, V, dtype=logits.dtype, device=dev)
     elif out.shape != logits.shape or out.dtype != logits.dtype or out.device != dev:
         _refuse("out like logits")
     _call(dev, lib().token_logprobs_backward, logits.data_ptr(), dt, T, V,
