@@ -503,6 +503,11 @@ __device__ __forceinline__ void dc_fill(DcFrags<PIECES>& fr, DcRaw<F32, PIECES>&
 // fragment read lie in different banks.  All of it without branches, so that
 // waits for older loads stay exact: past the end of the work a wave loads its
 // last slab again, past the end of K the last pieces (activations are 0 there).
+// Codes are not kept in the caches, which the scales' short runs and the rows
+// then have to themselves: 16 tokens of the 256-expert layer 442 against 474 us,
+// 4 tokens 139 / 151; 16 tokens of the 128-expert layer, which the last-level
+// cache would hold from one call to the next, 67.5 / 66.2.  With the scales
+// loaded that way too the first takes 484 us.
 template <int NG>
 struct DcSlab {
   word4 code[NG];
@@ -534,7 +539,8 @@ struct DcWalk {
     const uint32_t oc = (lane / Slot::kPieces) * K2 + piece * 16;
 #pragma unroll
     for (int i = 0; i < NG; ++i)
-      s.code[i] = *reinterpret_cast<const word4*>(codes + (row + i * kRows) * K2 + oc);
+      s.code[i] = __builtin_nontemporal_load(
+          reinterpret_cast<const word4*>(codes + (row + i * kRows) * K2 + oc));
     const uint8_t* ps = scales + row * K16 + (uint32_t)((lane >> 2) * K16);
     const int os = g * 8 + (lane & 3) * (2 * NG);
     if constexpr (!WHOLE) {
