@@ -17,8 +17,8 @@
 // 4.9 here); its arithmetic, of which a quarter-rate exponential per logit is
 // the largest part, takes about two thirds of that.  A single row is bound by
 // the arithmetic of the CU that it is on, and by latency: 1 x 32768 with 5
-// alternatives 8 us.  The backward pass reads and writes 2048 x 131072 in 165
-// us, 6.5 TB/s.
+// alternatives 8 us.  The backward pass reads and writes 2048 x 131072 in 183
+// us, 5.9 TB/s; the forward pass before it takes 97 us.
 #include "common.h"
 
 namespace {
@@ -53,6 +53,7 @@ struct Lanes<float> {
   }
 };
 typedef __bf16 lp_bf16x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t lp_word4 __attribute__((ext_vector_type(4)));
 template <>
 struct Lanes<uint16_t> {
   static constexpr int N = 8;
@@ -602,7 +603,9 @@ __global__ __launch_bounds__(64) void k_logprob_join(
 // The gradient: one pass, each element read and written by the same thread
 // (so the gradient may replace the logits).  With k0 = -it (a + b H) and
 // k1 = -it b ln 2, grad_j = p_j (k0 + k1 d_j), plus it a at the target.
-template <typename E, int NT, bool VEC>
+// STREAM: the gradient is not kept in the caches, and rows go from the last to
+// the first, whose end the forward pass left in the last-level cache.
+template <typename E, int NT, bool VEC, bool STREAM>
 __global__ __launch_bounds__(NT) void k_logprob_bwd(
     const E* logits, int64_t T, int V, int64_t ld, const int64_t* __restrict__ targets,
     const float* __restrict__ inv_t, const float* __restrict__ norm,
@@ -610,7 +613,8 @@ __global__ __launch_bounds__(NT) void k_logprob_bwd(
     const float* __restrict__ g_ent, E* grad, int64_t ldg) {
   typedef Lanes<E> LE;
   constexpr int N = LE::N;
-  for (int64_t t = blockIdx.y; t < T; t += gridDim.y) {
+  for (int64_t n = blockIdx.y; n < T; n += gridDim.y) {
+    const int64_t t = STREAM ? T - 1 - n : n;
     const E* row = logits + t * ld;
     E* out = grad + t * ldg;
     const float it = inv_t ? inv_t[t] : 1.0f, c = it * kLog2e;
@@ -640,13 +644,19 @@ __global__ __launch_bounds__(NT) void k_logprob_bwd(
           min((int)((16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15) / (int)sizeof(E), V);
       const int nv = (V - head) / N, tail = head + nv * N;
       const uint4* vec = reinterpret_cast<const uint4*>(row + head);
-      uint4* dst = reinterpret_cast<uint4*>(out + head);
+      auto put = [&](int i, const uint4& v) {
+        if constexpr (STREAM)
+          __builtin_nontemporal_store(lp_word4{v.x, v.y, v.z, v.w},
+                                      reinterpret_cast<lp_word4*>(out + head) + i);
+        else
+          reinterpret_cast<uint4*>(out + head)[i] = v;
+      };
       for (int i0 = blockIdx.x * (NT * kLpBwdU); i0 < nv; i0 += gridDim.x * (NT * kLpBwdU)) {
         if (none) {
 #pragma unroll
           for (int u = 0; u < kLpBwdU; ++u) {
             const int i = i0 + u * NT + threadIdx.x;
-            if (i < nv) dst[i] = make_uint4(0, 0, 0, 0);
+            if (i < nv) put(i, make_uint4(0, 0, 0, 0));
           }
           continue;
         }
@@ -669,7 +679,7 @@ __global__ __launch_bounds__(NT) void k_logprob_bwd(
               for (int e = 0; e < N; ++e)
                 if (e == rel) g[e] = __builtin_fmaf(it, a, g[e]);
             }
-            dst[i] = LE::pack(g);
+            put(i, LE::pack(g));
           }
         }
       }
@@ -754,23 +764,31 @@ struct LpGradCall {
   int64_t ldg;
 };
 
-template <typename E, int NT, bool VEC>
+template <typename E, int NT, bool VEC, bool STREAM = false>
 void lp_launch_bwd_nt(const LpGradCall& a, hipStream_t s) {
   const int64_t per = VEC ? (int64_t)NT * kLpBwdU * Lanes<E>::N : NT;
   const dim3 grid((unsigned)((a.V + per - 1) / per), (unsigned)(a.T < 65535 ? a.T : 65535));
-  hipLaunchKernelGGL((k_logprob_bwd<E, NT, VEC>), grid, dim3(NT), 0, s, (const E*)a.logits, a.T,
-                     a.V, a.ld, a.targets, a.inv_t, a.norm, a.entropy, a.g_lp, a.g_ent,
+  hipLaunchKernelGGL((k_logprob_bwd<E, NT, VEC, STREAM>), grid, dim3(NT), 0, s,
+                     (const E*)a.logits, a.T, a.V, a.ld, a.targets, a.inv_t, a.norm, a.entropy, a.g_lp, a.g_ent,
                      (E*)a.grad, a.ldg);
 }
 
 // 16-byte pieces where every row of the gradient starts at the same place of
-// a 16-byte block as its row of logits; single elements otherwise.
+// a 16-byte block as its row of logits; single elements otherwise.  From 160 MB
+// on logits and gradient are more than the last-level cache of 256 MB holds,
+// and the gradient goes past it: forward and backward of 2048 x 131072 bf16 271
+// against 292 us, 4096 x 32000 121 / 157, and with a kernel after them that reads
+// the gradient 383 / 398 and 197 / 221; smaller ones lose with such a reader (512 x
+// 131072 111 / 99).
+constexpr int64_t kLpStreamBytes = (int64_t)160 << 20;
 template <typename E>
 int lp_launch_bwd(const LpGradCall& a, hipStream_t s) {
   const bool vec = ((reinterpret_cast<uintptr_t>(a.logits) ^ reinterpret_cast<uintptr_t>(a.grad)) & 15) == 0 &&
                    (((a.ld - a.ldg) * (int64_t)sizeof(E)) & 15) == 0;
   if (!vec) lp_launch_bwd_nt<E, 256, false>(a, s);
   else if (a.V <= 64 * kLpBwdU * Lanes<E>::N) lp_launch_bwd_nt<E, 64, true>(a, s);
+  else if (a.T * a.V * (int64_t)sizeof(E) >= kLpStreamBytes)
+    lp_launch_bwd_nt<E, 256, true, true>(a, s);
   else lp_launch_bwd_nt<E, 256, true>(a, s);
   return nv_launch_status();
 }

@@ -300,6 +300,32 @@ def test_more_rows_than_a_grid_dimension():
     near(g.float(), want, tol, "gradient")
 
 
+@pytest.mark.parametrize("off", [0, 3])
+def test_gradient_larger_than_the_caches(off):
+    """1300 x 65537 bf16 (170 MB), whose gradient takes another way to memory
+    than one of a few rows does: the same bits, ignored rows, aligned or not,
+    in place or not."""
+    say(f"logprobs gradient 1300 x 65537 off={off}")
+    T, V = 1300, 65537
+    big = torch.empty((T, V + 7 + off), dtype=torch.bfloat16, device=DEV)
+    big.normal_(generator=torch.Generator(device=DEV).manual_seed(off))
+    z = big[:, off:off + V]
+    y = torch.from_numpy(np.random.default_rng(off).integers(-V // 4, V, T)).to(DEV)
+    y[y < 0] = -100
+    r = L.token_logprobs(z, y)
+    ga = torch.randn(T, device=DEV)
+    parts = [L.token_logprobs_backward(z[i:i + 100], y[i:i + 100], r.norm[i:i + 100], None,
+                                       ga[i:i + 100]) for i in range(0, T, 100)]
+    want = torch.cat(parts)
+    same = torch.full_like(big, 7.0)
+    L.token_logprobs_backward(z, y, r.norm, None, ga, out=same[:, off:off + V])
+    assert torch.equal(same[:, off:off + V], want)
+    same[:, off:off + V] = 7.0
+    assert (same == 7.0).all()
+    L.token_logprobs_backward(z, y, r.norm, None, ga, out=z)
+    assert torch.equal(z, want)
+
+
 def test_one_long_row():
     """A row of 2^24 + 9 tokens in 64 parts, at an odd address."""
     say("logprobs: 1 x 16777225")
