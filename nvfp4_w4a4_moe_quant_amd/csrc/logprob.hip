@@ -13,7 +13,7 @@
 // Reported log-probabilities are (l_j - m) inv_temperature - ln 2 log2 S.
 //
 // The forward pass is bound by reading the logits where there are rows enough:
-// 4096 x 131072 bf16 with 8 alternatives 195 us, 5.5 TB/s (a large copy reaches
+// 4096 x 131072 bf16 with 20 alternatives 177-188 us, 5.9 TB/s (a large copy reaches
 // 4.9 here); its arithmetic, of which a quarter-rate exponential per logit is
 // the largest part, takes about two thirds of that.  A single row is bound by
 // the arithmetic of the CU that it is on, and by latency: 1 x 32768 with 5
@@ -304,8 +304,9 @@ __device__ __forceinline__ void lp_target(const E* row, int V, const int64_t* ta
 // one; the few elements at or above it become candidates, which one wave
 // ranks when there are many.  Rows start at any element: the pieces are those
 // that lie wholly inside the row at 16-byte addresses, and the up to N - 1
-// elements before and after them go one to a thread.
-template <typename E, int NT, bool TOP>
+// elements before and after them go one to a thread.  STREAM: the logits are
+// not kept in the caches.
+template <typename E, int NT, bool TOP, bool STREAM>
 __global__ __launch_bounds__(NT, 4) void k_logprob(
     const E* __restrict__ logits, int V, int64_t ld, const int64_t* __restrict__ targets,
     const float* __restrict__ inv_t, int top_k, int parts, float* __restrict__ logprobs,
@@ -334,7 +335,15 @@ __global__ __launch_bounds__(NT, 4) void k_logprob(
     for (int u = 0; u < U; ++u) {
       const int i = b + u * NT + tid;
       x[u] = make_uint4(LE::kNone, LE::kNone, LE::kNone, LE::kNone);
-      if (i < v1) x[u] = vec[i];
+      if constexpr (STREAM) {
+        if (i < v1) {
+          const lp_word4 w =
+              __builtin_nontemporal_load(reinterpret_cast<const lp_word4*>(row + head) + i);
+          x[u] = make_uint4(w.x, w.y, w.z, w.w);
+        }
+      } else {
+        if (i < v1) x[u] = vec[i];
+      }
     }
   };
   fetch(v0);
@@ -716,12 +725,19 @@ inline int lp_parts(int64_t T, int64_t V) {
   return (int)(n < 64 ? n : 64);
 }
 
-template <typename E, int NT, bool TOP>
+template <typename E, int NT, bool TOP, bool STREAM = false>
 void lp_launch_nt(const LpCall& a, hipStream_t s) {
-  hipLaunchKernelGGL((k_logprob<E, NT, TOP>), dim3((unsigned)(a.T * a.parts)), dim3(NT), 0, s,
+  hipLaunchKernelGGL((k_logprob<E, NT, TOP, STREAM>), dim3((unsigned)(a.T * a.parts)), dim3(NT), 0, s,
                      (const E*)a.logits, a.V, a.ld, a.targets, a.inv_t, a.top_k, a.parts,
                      a.logprobs, a.entropy, a.norm, a.top_ids, a.top_lp, a.ws);
 }
+
+// Logits of which the caches could keep only a part, with alternatives (a
+// rollout's record, which no gradient follows), are read past them: 2048 x
+// 131072 bf16 91 against 102 us, 4096 x 131072 177-188 / 199-219; 512 x 131072 the
+// same either way.  Where the backward pass follows it would miss the part
+// that was kept: 8192 x 32768 265 / 255 for both passes, 4096 x 32000 137 / 121.
+constexpr int64_t kLpPastCache = (int64_t)256 << 20;
 
 template <typename E>
 int lp_launch(const LpCall& a, hipStream_t s) {
@@ -734,6 +750,8 @@ int lp_launch(const LpCall& a, hipStream_t s) {
   if (a.top_k) {
     if (small) lp_launch_nt<E, 64, true>(a, s);
     else if (wide) lp_launch_nt<E, 1024, true>(a, s);
+    else if (a.T * a.V * (int64_t)sizeof(E) >= kLpPastCache)
+      lp_launch_nt<E, 256, true, true>(a, s);
     else lp_launch_nt<E, 256, true>(a, s);
   } else {
     if (small) lp_launch_nt<E, 64, false>(a, s);

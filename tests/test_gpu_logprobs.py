@@ -374,3 +374,24 @@ def test_repeatable_on_streams_and_graphs():
         step(*cases[2])
         torch.cuda.synchronize()
         assert same(graphs[0][1], ref[n]) and same(graphs[1][1], ref[1])
+
+
+@pytest.mark.parametrize("dtype,T", [("bf16", 2064), ("f32", 1032)])
+def test_logits_larger_than_the_caches(dtype, T):
+    """270 MB of logits with alternatives, read another way than a few rows
+    are: the same bits."""
+    say(f"logprobs {T} x 65539 {dtype}")
+    V = 65539
+    z = torch.empty((T, V), dtype=torch.float32 if dtype == "f32" else torch.bfloat16, device=DEV)
+    z.normal_(generator=torch.Generator(device=DEV).manual_seed(8))
+    y = torch.from_numpy(np.random.default_rng(8).integers(0, V, T)).to(DEV)
+    it = torch.full((T,), 0.75, device=DEV)
+    r = L.token_logprobs(z, y, top_k=5, inv_temperature=it)
+    n = T // 4
+    parts = [L.token_logprobs(z[i:i + n], y[i:i + n], top_k=5, inv_temperature=it[i:i + n])
+             for i in range(0, T, n)]
+    for k in range(5):
+        assert torch.equal(r[k], torch.cat([p[k] for p in parts])), k
+    rows = [0, 1, T - 1]
+    check(z[rows].clone(), host(y[rows]), host(it[rows]), 5,
+          L.LogprobsOut(*(t[rows] for t in r)))
