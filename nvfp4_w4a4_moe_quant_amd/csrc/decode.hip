@@ -15,12 +15,12 @@
 //
 // Both products stream W once, 0.5625 bytes a weight, and that is what bounds
 // them: 16 tokens of a layer of 256 experts, H 7168, I 2048 (103 experts, 1.70
-// and 0.85 GB) take 325 and 159-190 us, 5.2 and 4.5-5.3 TB/s where a large
-// copy reaches 4.9 on this card; the same with the arithmetic taken out takes
-// as long.  One token (8 experts) takes 28 and 21 us: some 8 us of the first
+// and 0.85 GB) take 282-299 and 150-177 us, 5.7-6.0 and 4.8-5.7 TB/s where a
+// large copy reaches 4.9 on this card; the same with the arithmetic taken out
+// takes as long.  One token (8 experts) takes 28 and 21 us: some 8 us of the first
 // and 5 us of the second pass before the stream runs (routing 3, first loads
 // 4), and the join of the parts is another 4 us of the second, which is all of
-// it in small layers (128 experts, H 2048, I 768: 10 and 9 us, 16 tokens 66 us
+// it in small layers (128 experts, H 2048, I 768: 10 and 9 us, 16 tokens 68 us
 // for 47 us of bytes).
 //
 // v_mfma_f32_16x16x32_f16 (16 tokens x 16 columns): lane (c, q) of a wave

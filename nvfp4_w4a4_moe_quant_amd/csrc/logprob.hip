@@ -13,7 +13,7 @@
 // Reported log-probabilities are (l_j - m) inv_temperature - ln 2 log2 S.
 //
 // The forward pass is bound by reading the logits where there are rows enough:
-// 4096 x 131072 bf16 with 20 alternatives 177-188 us, 5.9 TB/s (a large copy reaches
+// 4096 x 131072 bf16 with 20 alternatives 168-188 us, 6 TB/s (a large copy reaches
 // 4.9 here); its arithmetic, of which a quarter-rate exponential per logit is
 // the largest part, takes about two thirds of that.  A single row is bound by
 // the arithmetic of the CU that it is on, and by latency: 1 x 32768 with 5
