@@ -507,7 +507,9 @@ __device__ __forceinline__ void dc_fill(DcFrags<PIECES>& fr, DcRaw<F32, PIECES>&
 // then have to themselves: 16 tokens of the 256-expert layer 442 against 474 us,
 // 4 tokens 139 / 151; 16 tokens of the 128-expert layer, which the last-level
 // cache would hold from one call to the next, 67.5 / 66.2.  With the scales
-// loaded that way too the first takes 484 us.
+// loaded that way too the first takes 484 us.  Rows that are not whole 64-byte
+// pieces share them between runs and do go through the caches (8 tokens of 19
+// experts, H 6112: 54.5 us, 60.6 past them).
 template <int NG>
 struct DcSlab {
   word4 code[NG];
@@ -538,9 +540,11 @@ struct DcWalk {
     const int piece = min(g * 4 + lane % Slot::kPieces, (K2 >> 4) - 1);
     const uint32_t oc = (lane / Slot::kPieces) * K2 + piece * 16;
 #pragma unroll
-    for (int i = 0; i < NG; ++i)
-      s.code[i] = __builtin_nontemporal_load(
-          reinterpret_cast<const word4*>(codes + (row + i * kRows) * K2 + oc));
+    for (int i = 0; i < NG; ++i) {
+      const word4* at = reinterpret_cast<const word4*>(codes + (row + i * kRows) * K2 + oc);
+      if constexpr (WHOLE) s.code[i] = __builtin_nontemporal_load(at);
+      else s.code[i] = *at;
+    }
     const uint8_t* ps = scales + row * K16 + (uint32_t)((lane >> 2) * K16);
     const int os = g * 8 + (lane & 3) * (2 * NG);
     if constexpr (!WHOLE) {
