@@ -205,7 +205,9 @@ class GraphedMoEDecode:
     caller's x [T, H] and logits [T, E] when given, after copying inputs that
     live elsewhere.  A batch of fewer tokens fills the remaining logits rows
     with -inf: such rows cost nothing and give 0.  The returned MoEDecodeOut is
-    the graph's own, overwritten by the next call."""
+    the graph's own, overwritten by the next call.  The object keeps the weights
+    (the graph holds their addresses only); values written into their tensors
+    are what the next call computes with."""
 
     def __init__(self, wgu: QuantWeights, wd: QuantWeights, topk: int, T: int, E: int,
                  x_dtype: torch.dtype, device, warmup: int = 2,
@@ -216,6 +218,7 @@ class GraphedMoEDecode:
         if self.x.shape != (T, wgu.K) or self.x.dtype != x_dtype or self.logits.shape != (T, E):
             raise ValueError("x [T, H] of x_dtype and logits [T, E]")
         args = (wgu, wd, topk)
+        self.weights = (wgu, wd)
         with torch.cuda.device(device):
             side = torch.cuda.Stream()
             side.wait_stream(torch.cuda.current_stream())

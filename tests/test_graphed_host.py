@@ -1,0 +1,67 @@
+"""Host-side checks (no GPU needed) of the captured layers, with the capture
+itself replaced by a stand-in: what the object holds, and which calls it
+refuses."""
+import contextlib
+import gc
+import types
+import weakref
+
+import pytest
+import torch
+
+from nvfp4_w4a4_moe_quant_amd import _lib as L
+from nvfp4_w4a4_moe_quant_amd import pipeline as P
+
+T, E, H, I, K = 4, 3, 32, 32, 2
+
+
+@pytest.fixture
+def capture(monkeypatch):
+    """Streams and graphs that do nothing; counts the replays."""
+    seen = types.SimpleNamespace(replays=0)
+
+    class Graph:
+        def replay(self):
+            seen.replays += 1
+
+    stream = lambda *a, **k: types.SimpleNamespace(wait_stream=lambda other: None)  # noqa: E731
+    nothing = lambda *a, **k: contextlib.nullcontext()  # noqa: E731
+    for name, fake in (("Stream", stream), ("current_stream", stream), ("stream", nothing),
+                       ("device", nothing), ("graph", nothing), ("CUDAGraph", Graph)):
+        monkeypatch.setattr(torch.cuda, name, fake)
+    monkeypatch.setattr(L, "nvfp4_moe_decode", lambda x, lg, wgu, wd, k, out=None: L.MoEDecodeOut(
+        torch.zeros_like(x), torch.zeros((x.shape[0], k), dtype=torch.int32),
+        torch.zeros((x.shape[0], k))))
+    return seen
+
+
+def weights(N, Kw):
+    return P.QuantWeights(L.NVFP4(torch.zeros((E, N, Kw // 2), dtype=torch.uint8),
+                                  torch.zeros((E, N, Kw // 16), dtype=torch.uint8),
+                                  torch.zeros(E)), N, Kw)
+
+
+def decode(wgu=None, wd=None, **kw):
+    return P.GraphedMoEDecode(wgu or weights(2 * I, H), wd or weights(H, I), K, T=T, E=E,
+                              x_dtype=torch.bfloat16, device="cpu", **kw)
+
+
+def tensors(*ws):
+    """Weak references to the tensors of weights."""
+    return [weakref.ref(t) for w in ws for t in w.w]
+
+
+def test_captured_decode_layer_keeps_its_weights(capture):
+    """The captured kernels hold addresses only, so the object keeps what lies
+    there: weights that only the constructor call had stay alive as long as
+    it does, and no longer."""
+    wgu, wd = weights(2 * I, H), weights(H, I)
+    refs, g = tensors(wgu, wd), decode(wgu, wd)
+    del wgu, wd
+    gc.collect()
+    assert all(r() is not None for r in refs)
+    g()
+    assert capture.replays == 1
+    del g
+    gc.collect()
+    assert all(r() is None for r in refs)
