@@ -163,8 +163,8 @@ class GraphedMoEBlock:
     copies inputs that live elsewhere into those buffers and replays; the
     returned tensor is the graph's static output, overwritten by the next
     call.  Every kernel of the block only reads device memory the graph owns,
-    the static inputs or the caller's weights, and nothing in it is a memset
-    node."""
+    the static inputs or the weights, which the object keeps, and nothing in
+    it is a memset node."""
 
     def __init__(self, wgu: QuantWeights, wd: QuantWeights, topk: int, n_sel_x: Optional[int],
                  n_sel_h: Optional[int], T: int, E: int, x_dtype: torch.dtype, device,
@@ -179,6 +179,7 @@ class GraphedMoEBlock:
         self.logits = (logits if logits is not None
                        else torch.zeros((T, E), dtype=torch.float32, device=device))
         args = (wgu, wd, topk, n_sel_x, n_sel_h, out_dtype)
+        self.weights = (wgu, wd)
         side = torch.cuda.Stream(device)
         side.wait_stream(torch.cuda.current_stream(device))
         with torch.cuda.stream(side):

@@ -65,3 +65,16 @@ def test_captured_decode_layer_keeps_its_weights(capture):
     del g
     gc.collect()
     assert all(r() is None for r in refs)
+
+
+def test_captured_block_keeps_its_weights(capture, monkeypatch):
+    monkeypatch.setattr(P, "moe_block", lambda x, *a: dict(out=torch.zeros_like(x)))
+    wgu, wd = weights(2 * I, H), weights(H, I)
+    refs, g = tensors(wgu, wd), P.GraphedMoEBlock(wgu, wd, K, None, None, T=T, E=E,
+                                                  x_dtype=torch.bfloat16, device="cpu")
+    del wgu, wd
+    gc.collect()
+    assert all(r() is not None for r in refs)
+    del g
+    gc.collect()
+    assert all(r() is None for r in refs)
