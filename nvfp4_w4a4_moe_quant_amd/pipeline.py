@@ -244,10 +244,12 @@ class GraphedMoEDecode:
 class GraphedDense:
     """dense_forward captured once as a HIP graph for fixed [rows, K] (the
     decode shape): a call copies x into the static input and replays every
-    kernel of quantize + RAC + GEMM with no host work per launch."""
+    kernel of quantize + RAC + GEMM with no host work per launch.  The object
+    keeps the weights."""
 
     def __init__(self, wq: QuantWeights, n_select: Optional[int], rows: int,
                  x_dtype: torch.dtype, device, warmup: int = 2):
+        self.weights = wq
         self.x = torch.zeros((rows, wq.K), dtype=x_dtype, device=device)
         self.offsets = torch.tensor([0, rows], dtype=torch.int32, device=device)
         side = torch.cuda.Stream(device)

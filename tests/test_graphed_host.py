@@ -78,3 +78,15 @@ def test_captured_block_keeps_its_weights(capture, monkeypatch):
     del g
     gc.collect()
     assert all(r() is None for r in refs)
+
+
+def test_captured_linear_keeps_its_weights(capture, monkeypatch):
+    monkeypatch.setattr(P, "dense_forward", lambda x, *a: dict(y=torch.zeros_like(x)))
+    w = weights(I, H)
+    refs, g = tensors(w), P.GraphedDense(w, None, rows=T, x_dtype=torch.bfloat16, device="cpu")
+    del w
+    gc.collect()
+    assert all(r() is not None for r in refs)
+    del g
+    gc.collect()
+    assert all(r() is None for r in refs)
