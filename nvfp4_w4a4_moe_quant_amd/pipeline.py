@@ -203,9 +203,10 @@ class GraphedMoEBlock:
 class GraphedMoEDecode:
     """moe_decode captured once as a HIP graph for a fixed number of tokens (at
     most 64): a call replays the layer on the static inputs, its own or the
-    caller's x [T, H] and logits [T, E] when given, after copying inputs that
-    live elsewhere.  A batch of fewer tokens fills the remaining logits rows
-    with -inf: such rows cost nothing and give 0.  The returned MoEDecodeOut is
+    caller's x [T, H] and logits [T, E] when given, after copying inputs of the
+    same shape and type that live elsewhere.  A batch of fewer tokens is written
+    into the first rows and the remaining logits rows are filled with -inf: such
+    rows cost nothing and give 0.  The returned MoEDecodeOut is
     the graph's own, overwritten by the next call.  The object keeps the weights
     (the graph holds their addresses only); values written into their tensors
     are what the next call computes with."""
@@ -231,12 +232,22 @@ class GraphedMoEDecode:
             with torch.cuda.graph(self.graph):
                 self.out = moe_decode(self.x, self.logits, *args)
 
+    @staticmethod
+    def _lives_in(static: torch.Tensor, t: torch.Tensor) -> bool:
+        """t is the static input itself, element for element."""
+        return t.data_ptr() == static.data_ptr() and all(
+            n == 1 or a == b for n, a, b in zip(t.shape, t.stride(), static.stride()))
+
     def __call__(self, x: Optional[torch.Tensor] = None,
                  logits: Optional[torch.Tensor] = None) -> L.MoEDecodeOut:
-        if x is not None and x.data_ptr() != self.x.data_ptr():
-            self.x.copy_(x)
-        if logits is not None and logits.data_ptr() != self.logits.data_ptr():
-            self.logits.copy_(logits)
+        given = ((self.x, x), (self.logits, logits))
+        for static, t in given:
+            if t is not None and (t.shape != static.shape or t.dtype != static.dtype):
+                raise ValueError(f"{static.dtype} {tuple(static.shape)} instead of "
+                                 f"{t.dtype} {tuple(t.shape)}")
+        for static, t in given:
+            if t is not None and not self._lives_in(static, t):
+                static.copy_(t)
         self.graph.replay()
         return self.out
 

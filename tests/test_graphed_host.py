@@ -90,3 +90,50 @@ def test_captured_linear_keeps_its_weights(capture, monkeypatch):
     del g
     gc.collect()
     assert all(r() is None for r in refs)
+
+
+@pytest.mark.parametrize("x,logits", [
+    ((1, H), (1, E)),             # one token would have filled every row
+    ((2, H), (2, E)),
+    ((T, 1), None), ((H,), None), ((T, H, 1), None),
+    (None, (T, 1)), (None, (E,)), (None, (1, E)), ((T, H), (1, E)),
+])
+def test_captured_decode_layer_refuses_other_shapes(capture, x, logits):
+    g = decode()
+    g.x.fill_(3), g.logits.fill_(4)
+    xs = None if x is None else torch.ones(x, dtype=torch.bfloat16)
+    lg = None if logits is None else torch.ones(logits)
+    with pytest.raises(ValueError):
+        g(xs, lg)
+    assert (g.x == 3).all() and (g.logits == 4).all() and capture.replays == 0
+
+
+def test_captured_decode_layer_refuses_other_types(capture):
+    g = decode()
+    for xs, lg in ((torch.ones((T, H)), None), (torch.ones((T, H), dtype=torch.float16), None),
+                   (None, torch.ones((T, E), dtype=torch.bfloat16)),
+                   (None, torch.ones((T, E), dtype=torch.float64))):
+        with pytest.raises(ValueError):
+            g(xs, lg)
+    assert capture.replays == 0
+    xs, lg = torch.rand((T, H)).bfloat16(), torch.rand((T, E))
+    g(xs, lg)
+    assert torch.equal(g.x, xs) and torch.equal(g.logits, lg) and capture.replays == 1
+
+
+def test_captured_decode_layer_views_of_its_inputs(capture):
+    """A tensor that starts where the static input does is that input only if
+    it is laid out alike."""
+    g = decode()
+    g.x.copy_(torch.rand((T, H)))
+    want = g.x.clone()
+    g(g.x), g(g.x[:]), g(g.x.view(-1).view(T, H))
+    assert torch.equal(g.x, want) and capture.replays == 3
+    g(g.x[:1].expand(T, H))
+    assert torch.equal(g.x, want[:1].expand(T, H))
+    with pytest.raises(ValueError):
+        g(g.x[:2], g.logits[:2])      # the first rows of a batch
+    one = P.GraphedMoEDecode(weights(2 * I, H), weights(H, I), K, T=1, E=E,
+                             x_dtype=torch.bfloat16, device="cpu")
+    one(one.x.as_strided((1, H), (7, 1)))   # one row: its stride says nothing
+    assert capture.replays == 5
