@@ -147,11 +147,20 @@ def moe_block(x: torch.Tensor, logits: torch.Tensor, wgu: QuantWeights, wd: Quan
     return d
 
 
+def _no_gradient(x: Optional[torch.Tensor], logits: Optional[torch.Tensor]):
+    if torch.is_grad_enabled() and ((x is not None and x.requires_grad) or
+                                    (logits is not None and logits.requires_grad)):
+        raise RuntimeError("the decode-step layer has no gradient: detach its inputs or call it "
+                           "under torch.no_grad()")
+
+
 def moe_decode(x: torch.Tensor, logits: torch.Tensor, wgu: QuantWeights, wd: QuantWeights,
                topk: int, out: Optional[torch.Tensor] = None) -> L.MoEDecodeOut:
     """The MoE FFN layer for up to 64 tokens, in token order, on the same
-    quantized weights as moe_block but with unquantized activations (what the
-    trainer's fake-quantized forward computes)."""
+    quantized weights as moe_block but with unquantized activations (the values
+    of the trainer's fake-quantized forward).  There is no backward pass: with
+    gradients enabled, x or logits that require one are refused."""
+    _no_gradient(x, logits)
     return L.nvfp4_moe_decode(x, logits, wgu.w, wd.w, topk, out=out)
 
 
@@ -240,6 +249,7 @@ class GraphedMoEDecode:
 
     def __call__(self, x: Optional[torch.Tensor] = None,
                  logits: Optional[torch.Tensor] = None) -> L.MoEDecodeOut:
+        _no_gradient(x, logits)
         given = ((self.x, x), (self.logits, logits))
         for static, t in given:
             if t is not None and (t.shape != static.shape or t.dtype != static.dtype):

@@ -137,3 +137,25 @@ def test_captured_decode_layer_views_of_its_inputs(capture):
                              x_dtype=torch.bfloat16, device="cpu")
     one(one.x.as_strided((1, H), (7, 1)))   # one row: its stride says nothing
     assert capture.replays == 5
+
+
+def test_decode_layer_refuses_to_cut_gradients(capture):
+    """The layer has no backward pass: under autograd, inputs that require a
+    gradient are refused instead of giving a result without one."""
+    wgu, wd = weights(2 * I, H), weights(H, I)
+    x, lg = torch.ones((T, H), dtype=torch.bfloat16), torch.ones((T, E))
+    xg, lgg = x.clone().requires_grad_(), lg.clone().requires_grad_()
+    g = decode()
+    for a, b in ((xg, lg), (x, lgg), (xg * 2, lg)):
+        with pytest.raises(RuntimeError, match="gradient"):
+            P.moe_decode(a, b, wgu, wd, K)
+        with pytest.raises(RuntimeError, match="gradient"):
+            g(a, b)
+        with torch.no_grad():
+            assert not P.moe_decode(a, b, wgu, wd, K).out.requires_grad
+            g(a, b)
+    with pytest.raises(RuntimeError, match="gradient"):
+        decode(x=xg)
+    assert not g.x.requires_grad and not g.logits.requires_grad
+    assert not P.moe_decode(x, lg, wgu, wd, K).out.requires_grad
+    assert not P.moe_decode(xg.detach(), lg, wgu, wd, K).out.requires_grad
