@@ -228,6 +228,11 @@ class GraphedMoEDecode:
                        else torch.zeros((T, E), dtype=torch.float32, device=device))
         if self.x.shape != (T, wgu.K) or self.x.dtype != x_dtype or self.logits.shape != (T, E):
             raise ValueError("x [T, H] of x_dtype and logits [T, E]")
+        dev = torch.device(device)
+        if dev.type == "cuda" and dev.index is None:
+            dev = torch.device("cuda", torch.cuda.current_device())
+        if self.x.device != dev or self.logits.device != dev:
+            raise ValueError(f"x and logits on the graph's device, {dev}")
         args = (wgu, wd, topk)
         self.weights = (wgu, wd)
         with torch.cuda.device(device):

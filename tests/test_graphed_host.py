@@ -159,3 +159,13 @@ def test_decode_layer_refuses_to_cut_gradients(capture):
     assert not g.x.requires_grad and not g.logits.requires_grad
     assert not P.moe_decode(x, lg, wgu, wd, K).out.requires_grad
     assert not P.moe_decode(xg.detach(), lg, wgu, wd, K).out.requires_grad
+
+
+def test_captured_decode_layer_refuses_inputs_elsewhere(capture):
+    """Inputs on another device than the graph's: the launches would go to that
+    device's stream, outside the capture, and replays would do nothing."""
+    x, lg = torch.ones((T, H), dtype=torch.bfloat16), torch.ones((T, E))
+    for kw in (dict(x=x.to("meta"), logits=lg), dict(x=x, logits=lg.to("meta"))):
+        with pytest.raises(ValueError, match="device"):
+            decode(**kw)
+    assert decode(x=x, logits=lg).x is x
