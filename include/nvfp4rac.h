@@ -421,6 +421,7 @@ int fp8_grouped_gemm(const fp8_gemm_args_t* args, void* stream);
  * scales 16-byte aligned, ws 16-byte aligned.  Inputs and out may not
  * overlap.  Finite x is a precondition for the row it is in only; logits of
  * +inf give their row NaN weights, and such slots are left out of the sum.
+ * An h beyond FP32's range enters the down product as its infinity.
  * The result is deterministic (sums in a fixed order).  Calls that may
  * overlap (on two streams, in two graphs) need workspaces and outputs of their
  * own.  With T == 0 nothing is enqueued.

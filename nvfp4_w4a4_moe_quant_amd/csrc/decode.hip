@@ -794,8 +794,13 @@ __device__ __forceinline__ void dc_gate_up(const DecodeParams& p, DcGateUpShared
       uint8_t* ex = p.hexp + pair * (Ip >> 4);
       const int at = place(slab * 16 + c);
       out[at] = __builtin_bit_cast(uint16_t, hi);
-      if constexpr (PIECES == 2) out[Ip + at] = __builtin_bit_cast(uint16_t, (_Float16)(v - (float)hi));
-      if (c == 0) ex[slab] = (uint8_t)(e + 128);
+      // an h beyond FP32's range stays an infinity: no second piece (inf - inf),
+      // and the largest exponent byte instead of 256
+      if constexpr (PIECES == 2) {
+        const float lo = __builtin_fabsf(v) == __builtin_inff() ? 0.0f : v - (float)hi;
+        out[Ip + at] = __builtin_bit_cast(uint16_t, (_Float16)lo);
+      }
+      if (c == 0) ex[slab] = (uint8_t)min(e + 128, 255);
       if (slab == nslab - 1) {  // zeros behind I, for the lanes that read them
         for (int z = p.I + c; z < Ip; z += 16) {
           out[place(z)] = 0;
