@@ -410,7 +410,9 @@ int fp8_grouped_gemm(const fp8_gemm_args_t* args, void* stream);
  * given logits of -inf: their out row is 0 and their x row is not read.
  * Products are exact and sums are FP32; x and h enter the matrix cores as
  * fp16 pieces scaled per row and K range by a power of two: one piece (11
- * bits, which holds a bf16 x exactly) for bf16, two (22 bits) for FP32.
+ * bits, which holds a bf16 x exactly and h to an eighth of bf16's step) for
+ * bf16, two (22 bits) for FP32.  SiLU and the routing weights take the
+ * hardware's exponential (a weight is within 2^-20 of its value).
  *
  * x [T, H] (row stride ldx) and out [T, H] (row stride ldo) have x_dtype;
  * logits is float [T, E] (row stride ld_logits).  gu_* hold [E, 2I, H] with
@@ -475,8 +477,13 @@ int nvfp4_moe_decode(const nvfp4_moe_decode_args_t* args, void* ws, size_t ws_by
  * top_logprobs are required if top_k > 0.  inv_temperature must be positive
  * and finite.  Requires 1 <= V <= 2^30, 0 <= top_k <= min(V, 32), T < 2^24,
  * arrays aligned to their elements.  ws may be NULL where its size is 0; calls
- * that may overlap need workspaces of their own.  Sums are FP32; the result
- * is deterministic.
+ * that may overlap need workspaces of their own.  Sums are FP32, and
+ * exponentials and logarithms the hardware's in base 2: results are off by some
+ * 2^-23 of the sizes that meet in them (1, |log p|, and the logit's distance from
+ * the row's maximum), and by the rounding of sums of V terms, V / 64 or fewer in
+ * a chain.  The result is deterministic.  Rows in which more
+ * than 512 16-byte pieces hold a logit that could be among the top_k (ties,
+ * rising rows) take top_k further passes over the row.
  *
  * token_logprobs_backward -- the gradient of the logits:
  *   grad[t, j] = inv_temperature[t] * ( a ([j = y] - p_j)
@@ -488,7 +495,10 @@ int nvfp4_moe_decode(const nvfp4_moe_decode_args_t* args, void* ws, size_t ws_by
  * logits are not read, whatever they are.  targets is required with
  * grad_logprobs, entropy with grad_entropy.  grad_logits has row stride ldg
  * >= V and may be the logits themselves (same ld), but not overlap them in
- * another way.  The forward call's limits hold.  No workspace.
+ * another way.  Where row t of both starts at the same offset from a 16-byte
+ * boundary (the same ld and base alignment, say) memory is accessed in 16-byte
+ * pieces, else by elements, several times slower.  The forward call's limits
+ * hold.  No workspace.
  * ------------------------------------------------------------------------ */
 size_t token_logprobs_workspace_size(int64_t T, int64_t V, int64_t top_k);
 int token_logprobs(const void* logits, int dtype, int64_t T, int64_t V, int64_t ld,

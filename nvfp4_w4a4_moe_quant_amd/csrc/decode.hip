@@ -13,15 +13,19 @@
 //   k_dc_down     the down product, weighted and summed over each token's
 //                 experts, to the output
 //
-// Both products stream W once, 0.5625 bytes a weight, and that is what bounds
-// them: 16 tokens of a layer of 256 experts, H 7168, I 2048 (103 experts, 1.70
-// and 0.85 GB) take 282-299 and 150-177 us, 5.7-6.0 and 4.8-5.7 TB/s where a
-// large copy reaches 4.9 on this card; the same with the arithmetic taken out
-// takes as long.  One token (8 experts) takes 28 and 21 us: some 8 us of the first
-// and 5 us of the second pass before the stream runs (routing 3, first loads
-// 4), and the join of the parts is another 4 us of the second, which is all of
-// it in small layers (128 experts, H 2048, I 768: 10 and 9 us, 16 tokens 68 us
-// for 47 us of bytes).
+// Both products stream W, 0.5625 bytes a weight, once for every 16 rows of an
+// expert, and with few rows an expert that is what bounds them: 16 tokens of a
+// layer of 256 experts, H 7168, I 2048 (103 experts, 1.70 and 0.85 GB) take 285
+// (279-298) and 158 (151-173) us, 6.0 and 5.4 TB/s where a large copy reaches 4.9
+// on this card; the same with the arithmetic taken out takes as long.  (Medians
+// and ranges of settled calls: the first 40 after an idle time are up to a
+// third slower.)  One token (8 experts) takes 27 and 20 us: some 8 us of the
+// first and 5 us of the second pass before the stream runs (routing 3, first
+// loads 4), and the join of the parts is another 4 us of the second, which is
+// all of it in small layers (128 experts, H 2048, I 768: 10 and 9 us, 16 tokens 67
+// us for 47 us of bytes).  With more than 16 rows an expert W is read again: 64
+// tokens of 16 experts, top-8, H 4096, I 2048 (39 tiles of rows) take 163 us for
+// 46 us of bytes.
 //
 // v_mfma_f32_16x16x32_f16 (16 tokens x 16 columns): lane (c, q) of a wave
 // takes column c and, of each group of 128 k, the 16 code bytes of k = 32 q ..
@@ -506,8 +510,12 @@ __device__ __forceinline__ void dc_fill(DcFrags<PIECES>& fr, DcRaw<F32, PIECES>&
 // Codes are not kept in the caches, which the scales' short runs and the rows
 // then have to themselves: 16 tokens of the 256-expert layer 442 against 474 us,
 // 4 tokens 139 / 151; 16 tokens of the 128-expert layer, which the last-level
-// cache would hold from one call to the next, 67.5 / 66.2.  With the scales
-// loaded that way too the first takes 484 us.  Rows that are not whole 64-byte
+// cache would hold from one call to the next, 67.5 / 66.2.  Where experts have
+// several tiles of rows the second reading of their codes finds less in the
+// caches: H 4096, I 2048, 64 tokens of 10 experts, top-10 (40 tiles) 169 against
+// 157 us, of 16 experts, top-8 (39) 163 / 149, of 32 (44) 178 / 173; of 8, top-2,
+// I 14336 (10) 282 / 282.  With the scales loaded past the caches too the first
+// takes 484 us.  Rows that are not whole 64-byte
 // pieces share them between runs and do go through the caches (8 tokens of 19
 // experts, H 6112: 54.5 us, 60.6 past them).
 template <int NG>

@@ -13,12 +13,16 @@
 // Reported log-probabilities are (l_j - m) inv_temperature - ln 2 log2 S.
 //
 // The forward pass is bound by reading the logits where there are rows enough:
-// 4096 x 131072 bf16 with 20 alternatives 168-188 us, 6 TB/s (a large copy reaches
-// 4.9 here); its arithmetic, of which a quarter-rate exponential per logit is
-// the largest part, takes about two thirds of that.  A single row is bound by
+// 4096 x 131072 bf16 with 8 alternatives 174 us (163-185), 6.2 TB/s (a large copy
+// reaches 4.9 here); its arithmetic, of which a quarter-rate exponential per
+// logit is the largest part, takes about two thirds of that.  A single row is bound by
 // the arithmetic of the CU that it is on, and by latency: 1 x 32768 with 5
-// alternatives 8 us.  The backward pass reads and writes 2048 x 131072 in 183
-// us, 5.9 TB/s; the forward pass before it takes 97 us.
+// alternatives 8 us.  The backward pass reads and writes 2048 x 131072 in 181
+// us (177-190), 5.9 TB/s; the forward pass before it takes 88 us (84-96).  These
+// are medians and ranges of settled calls: over the first 40 after an idle time
+// they are 222, 187 and 96 us.  (The base 2 costs little accuracy: of 4096 x 131072
+// the log-probabilities are off by 1.2e-7 of their norm, with natural
+// exponentials in FP32 by 6.7e-8.)
 #include "common.h"
 
 namespace {
@@ -465,7 +469,9 @@ __global__ __launch_bounds__(NT, 4) void k_logprob(
       const int n = pc.n;
       if (n > kLpPieces) {
         // more than can wait (ties, rising rows): top_k rounds of an arg-max
-        // over everything read so far
+        // over everything read so far.  Rows of ties with 20 alternatives: 16 x
+        // 131072 177 us for 19; 4096 x 131072 of equal or rising logits, with 8,
+        // 10.8 ms for 0.17
         float pv = kInf;
         int pi = -1;
         const int j0 = head + v0 * N, j1 = head + min(next, v1) * N;
@@ -792,7 +798,9 @@ void lp_launch_bwd_nt(const LpGradCall& a, hipStream_t s) {
 }
 
 // 16-byte pieces where every row of the gradient starts at the same place of
-// a 16-byte block as its row of logits; single elements otherwise.  From 160 MB
+// a 16-byte block as its row of logits; single elements otherwise: 2048 x 50257
+// bf16 in rows of 50304 with a gradient of the same row stride 65 us, with one
+// in rows of 50257 339 us; 300 rows 17 / 51.  From 160 MB
 // on logits and gradient are more than the last-level cache of 256 MB holds,
 // and the gradient goes past it: forward and backward of 2048 x 131072 bf16 271
 // against 292 us, 4096 x 32000 121 / 157, and with a kernel after them that reads

@@ -339,9 +339,12 @@ def token_logprobs(logits: torch.Tensor, targets: torch.Tensor,
     """(log-probabilities of targets, entropies) of logits [T, V], with the
     gradient of the logits (the trainer's side of the rollout-trainer
     log-prob gap).  Targets and temperatures get no gradient, and there is no
-    second derivative.  Leaf logits that require a gradient are refused under
-    graph capture, where another living graph of the same leaf ends the
-    process: capture the two library calls instead."""
+    second derivative.  The gradient is contiguous; logits whose rows are spaced
+    otherwise (a view of a padded vocabulary) take a slower backward pass.  Leaf
+    logits that require a gradient are refused under graph capture, where
+    another living graph of the same leaf ends the process: capture the two
+    library calls instead.  Captured logits that an operation gave are fine as
+    long as no eager graph of their leaves lives, as for any backward pass."""
     if inv_temperature is not None and inv_temperature.requires_grad:
         raise ValueError("inv_temperature gets no gradient")
     if logits.requires_grad and logits.is_leaf and torch.cuda.is_current_stream_capturing():
