@@ -72,7 +72,7 @@ typedef enum {
   NVFP4_EPI_F32 = 0,           /* out: float [total_rows, N] */
   NVFP4_EPI_SILU_MUL_BF16 = 1, /* out: bf16 [total_rows, N/2], h = silu(gate) * up */
   NVFP4_EPI_BF16 = 2           /* out: bf16 [total_rows, N], y rounded to nearest even
-                                  (fp8_grouped_gemm only) */
+                                  (fp8_ and int8_grouped_gemm only) */
 } nvfp4_epilogue_t;
 
 /* Text for a status code (static storage). */
@@ -510,6 +510,106 @@ int token_logprobs_backward(const void* logits, int dtype, int64_t T, int64_t V,
                             const float* norm, const float* entropy,
                             const float* grad_logprobs, const float* grad_entropy,
                             void* grad_logits, int64_t ldg, void* stream);
+
+/* ------------------------------------------------------------------------
+ * INT8 (W8A8) comparator: matrix products in 8-bit integers with one FP32
+ * scale per activation row (token, at run time) and per weight output channel,
+ * the other 8-bit form that a rollout can take where the pages take NVFP4
+ * (arXiv abstract on the mlsanity page; blog post, section "What it buys",
+ * compares with FP8).  Every product and sum is exact, so the only errors are
+ * the two roundings to 8 bits and the one to the output's type.
+ *
+ * int8_quantize_rows: for each row of x [rows, K] (FP32 or bf16, row stride
+ * ldx elements):
+ *   s = RN32(amax_row / 127)   (double quotient rounded once), at least 2^-126;
+ *                              0 for a zero row
+ *   r = RN32(1 / s)            (0 when s == 0)
+ *   codes[row, k] = nearest integer to RN32(x r), ties to even, in [-127, 127]
+ * A row that holds an infinity or a NaN gets the scale NaN and codes 0, which
+ * makes its outputs NaN and no other row's.  codes is int8 [rows, K];
+ * row_scales is float [rows].  Requires K % 16 == 0, K <= 2^24, ldx >= K, ldx %
+ * 8 == 0, x and codes 16-byte aligned.
+ * ------------------------------------------------------------------------ */
+int int8_quantize_rows(const void* x, int in_dtype, int64_t rows, int64_t K, int64_t ldx,
+                       int8_t* codes, float* row_scales, void* stream);
+
+/* int8_grouped_gemm: grouped (per-expert) INT8 GEMM with the grouping, gather
+ * and epilogues of w4a4_grouped_gemm_rac and fp8_grouped_gemm:
+ *   y[j, n] = RN32(RN32(a_scales[src] w_scales[g*N + n]) float(sum_k A[src,k] W_g[n,k]))
+ * with the sum exact in 32 bits.  Epilogue F32 writes y, BF16 writes bf16(y),
+ * SILU_MUL_BF16 h[j, i] = bf16(silu(y[j, i]) * y[j, I + i]) to [total_rows, I].
+ * The activations come either quantized (a_codes, a_scales) or as x, which the
+ * call quantizes as int8_quantize_rows does: into the workspace, or, for few
+ * rows, inside the product's own launch.
+ * group_offsets may be NULL with one group.  Rows of out that belong to no
+ * group are left alone.  Requires 1 <= N <= 2^24 (even for SiLU), K % 16 == 0,
+ * 16 <= K <= 131056 (no sum of 8-bit products can leave 32 bits), num_groups <=
+ * 2^20, total_rows < 2^31; codes and x 16-byte aligned, out aligned to its
+ * elements, ws 16-byte aligned.  Without a gather, src_rows >= total_rows.
+ * Calls that may overlap need workspaces of their own. */
+typedef struct {
+  int64_t num_groups;           /* G >= 1 */
+  int64_t N;                    /* output columns (2I for SILU_MUL) */
+  int64_t K;                    /* contraction length */
+  int64_t total_rows;           /* rows of the grouped output */
+  const int32_t* group_offsets; /* [G+1], ascending, [0] = 0, [G] = total_rows */
+  const int32_t* gather_rows;   /* [total_rows] or NULL (identity) */
+  const int8_t* a_codes;        /* [src_rows, K], or NULL where x is given */
+  const float* a_scales;        /* [src_rows] */
+  const void* x;                /* [src_rows, K], or NULL where a_codes is given */
+  int64_t x_dtype, ldx;         /* nvfp4_in_dtype_t; row stride in elements */
+  int64_t src_rows;             /* rows of x (read with x only) */
+  const int8_t* w_codes;        /* [G, N, K] */
+  const float* w_scales;        /* [G, N] */
+  int64_t epilogue;             /* nvfp4_epilogue_t */
+  void* out;                    /* float or bf16 [total_rows, N], or bf16 [total_rows, N/2] */
+} int8_gemm_args_t;
+
+size_t int8_grouped_gemm_workspace_size(const int8_gemm_args_t* args);
+int int8_grouped_gemm(const int8_gemm_args_t* args, void* ws, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * moe_balance_loss -- what a trainer adds for the router of the MoE layers
+ * (the pages train an MoE policy and describe no router): the slots that each
+ * expert got, each expert's mean probability, the balance loss and the z-loss.
+ *
+ * Row t counts if mask[t] != 0 (or mask is NULL) and not all of its logits are
+ * -inf; n = number of such rows, p_t = softmax(logits[t, :]), lse_t = its log-sum
+ * of exponentials (an expert of logit -inf has probability 0).
+ *   counts[e]     = slots s of counted rows with topk_ids[t, s] == e
+ *   tokens[0]     = n
+ *   mean_probs[e] = P_e = (1/n) sum_t p_te
+ *   losses[0]     = E / (k n) sum_e counts[e] P_e   (1 where both are even)
+ *   losses[1]     = (1/n) sum_t lse_t^2
+ * all 0 for n == 0.  An id outside [0, E) is a dropped slot: it is not counted,
+ * and k n stays the divisor.  Rows that do not count are not read where the
+ * mask says so.  A NaN or +inf logit of a counted row makes the losses (and,
+ * backward, its own row's gradient) NaN.
+ *
+ * moe_balance_loss_backward -- the gradient of the logits from that of the two
+ * losses (grad_losses, float [2], device), with counts held constant:
+ *   grad[t, j] = p_tj (a (counts[j] - sum_e counts[e] p_te) + b lse_t),
+ *   a = grad_losses[0] E / (k n^2),  b = grad_losses[1] 2 / n,
+ * rounded once to the logits' dtype; 0 in rows that do not count.
+ *
+ * logits [T, E] float or bf16, row stride ld elements (any ld >= E, no
+ * alignment beyond the element's; rows that start on 16 bytes are read in
+ * 16-byte pieces).  topk_ids int32 [T, k] (moe_route's), mask uint8 [T] or
+ * NULL.  mean_probs is nullable.  grad_logits has row stride ldg >= E and may
+ * be the logits themselves (same ld).  Requires 1 <= E <= 1024, 1 <= k <= E, T k <
+ * 2^31.  Sums are FP32 over at most some hundreds of rows and FP64 above that;
+ * exponentials and logarithms are the hardware's.  The results are
+ * deterministic.  Calls that may overlap need workspaces of their own.
+ * ------------------------------------------------------------------------ */
+size_t moe_balance_loss_workspace_size(int64_t T, int64_t E);
+int moe_balance_loss(const void* logits, int dtype, int64_t T, int64_t E, int64_t ld,
+                     const int32_t* topk_ids, int64_t k, const uint8_t* mask, int32_t* counts,
+                     int32_t* tokens, float* mean_probs, float* losses, void* ws,
+                     size_t ws_bytes, void* stream);
+int moe_balance_loss_backward(const void* logits, int dtype, int64_t T, int64_t E, int64_t ld,
+                              int64_t k, const uint8_t* mask, const int32_t* counts,
+                              const int32_t* tokens, const float* grad_losses,
+                              void* grad_logits, int64_t ldg, void* stream);
 
 #ifdef __cplusplus
 }

@@ -63,6 +63,17 @@ class MoEDecodeArgs(ctypes.Structure):
     ]
 
 
+class Int8GemmArgs(ctypes.Structure):
+    """Mirror of int8_gemm_args_t."""
+    _fields_ = [
+        ("num_groups", _I64), ("N", _I64), ("K", _I64), ("total_rows", _I64),
+        ("group_offsets", _P), ("gather_rows", _P),
+        ("a_codes", _P), ("a_scales", _P),
+        ("x", _P), ("x_dtype", _I64), ("ldx", _I64), ("src_rows", _I64),
+        ("w_codes", _P), ("w_scales", _P), ("epilogue", _I64), ("out", _P),
+    ]
+
+
 _SIGS = {
     "nvfp4_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "nvfp4_quantize_workspace_size": (_SZ, [_I64, _I64]),
@@ -99,6 +110,14 @@ _SIGS = {
                                       _P, _P, _P, _P, _SZ, _P]),
     "token_logprobs_backward": (ctypes.c_int, [_P, ctypes.c_int, _I64, _I64, _I64, _P, _P, _P,
                                                _P, _P, _P, _P, _I64, _P]),
+    "int8_quantize_rows": (ctypes.c_int, [_P, ctypes.c_int, _I64, _I64, _I64, _P, _P, _P]),
+    "int8_grouped_gemm_workspace_size": (_SZ, [ctypes.POINTER(Int8GemmArgs)]),
+    "int8_grouped_gemm": (ctypes.c_int, [ctypes.POINTER(Int8GemmArgs), _P, _SZ, _P]),
+    "moe_balance_loss_workspace_size": (_SZ, [_I64, _I64]),
+    "moe_balance_loss": (ctypes.c_int, [_P, ctypes.c_int, _I64, _I64, _I64, _P, _I64, _P, _P, _P,
+                                        _P, _P, _P, _SZ, _P]),
+    "moe_balance_loss_backward": (ctypes.c_int, [_P, ctypes.c_int, _I64, _I64, _I64, _I64, _P, _P,
+                                                 _P, _P, _P, _I64, _P]),
 }
 EXPORTS = tuple(_SIGS)
 
@@ -185,6 +204,13 @@ class LogprobsOut(NamedTuple):
     norm: torch.Tensor                    # float32 [T, 2], for the backward call
     top_ids: Optional[torch.Tensor]       # int32 [T, top_k]
     top_logprobs: Optional[torch.Tensor]  # float32 [T, top_k]
+
+
+class BalanceOut(NamedTuple):
+    losses: torch.Tensor      # float32 [2]: balance loss, z-loss
+    counts: torch.Tensor      # int32 [E]
+    mean_probs: torch.Tensor  # float32 [E]
+    tokens: torch.Tensor      # int32 [1]: rows counted, for the backward call
 
 
 class RouteOut(NamedTuple):
@@ -620,4 +646,158 @@ def token_logprobs_backward(logits: torch.Tensor, targets: Optional[torch.Tensor
     _call(dev, lib().token_logprobs_backward, logits.data_ptr(), dt, T, V,
           _row_stride(logits, "logits"), y, it, norm.data_ptr(), h, ga, gb, out.data_ptr(),
           _row_stride(out, "out"))
+    return out
+
+
+# ------------------------------------------------- INT8 W8A8 comparator
+class INT8(NamedTuple):
+    codes: torch.Tensor    # int8 [rows, K], or [G, N, K] for weights
+    scales: torch.Tensor   # float32 [rows], or [G, N]
+
+
+def int8_quantize_rows(x: torch.Tensor, out: Optional[INT8] = None) -> INT8:
+    """Per-row quantization of x [rows, K] (bf16 or FP32, row stride honoured)
+    to 8-bit integers: scale amax / 127."""
+    if x.dim() != 2:
+        _refuse("x [rows, K]")
+    rows, K = x.shape
+    dev = x.device
+    dt = _dtype_code(x)
+    if dev.type != "cuda":
+        _refuse("x on a GPU")
+    if out is None:
+        out = INT8(torch.empty(rows, K, dtype=torch.int8, device=dev),
+                   torch.empty(rows, dtype=torch.float32, device=dev))
+    else:
+        _int8(out, (rows, K), dev, "out")
+    _call(dev, lib().int8_quantize_rows, x.data_ptr(), dt, rows, K, _row_stride(x, "x"),
+          out.codes.data_ptr(), out.scales.data_ptr())
+    return out
+
+
+def _int8(q: INT8, shape, dev, name: str):
+    c, s = q
+    if c.shape != shape or c.dtype != torch.int8 or c.device != dev or not c.is_contiguous():
+        _refuse(f"{name}: contiguous int8 codes {shape} on {dev}")
+    if s.shape != shape[:-1] or s.dtype != torch.float32 or s.device != dev \
+            or not s.is_contiguous():
+        _refuse(f"{name}: contiguous float32 scales {shape[:-1]} on {dev}")
+
+
+def int8_grouped_gemm(a, w: INT8, group_offsets: Optional[torch.Tensor] = None, *, N: int, K: int,
+                      total_rows: int, gather_rows: Optional[torch.Tensor] = None,
+                      epilogue: int = NVFP4_EPI_F32, out: Optional[torch.Tensor] = None,
+                      validate: bool = False) -> torch.Tensor:
+    """a: INT8 rows, or x [src_rows, K] (bf16 or FP32, row stride honoured), which
+    the call quantizes as int8_quantize_rows does.  w: codes [G, N, K], scales
+    [G, N].  group_offsets [G + 1] may be None for one group.  epilogue F32,
+    SILU_MUL_BF16 or BF16.  validate=True checks the offsets and gather indices
+    on the host first (check_groups; synchronizes)."""
+    quantized = isinstance(a, INT8)
+    x = a.codes if quantized else a
+    if x.dim() != 2 or x.shape[1] != K:
+        _refuse("activations [src_rows, K]")
+    src_rows = x.shape[0]
+    dev = x.device
+    if dev.type != "cuda":
+        _refuse("activations on a GPU")
+    G = 1 if group_offsets is None else group_offsets.numel() - 1
+    _int8(w, (G, N, K), dev, "w")
+    args = Int8GemmArgs(num_groups=G, N=N, K=K, total_rows=total_rows,
+                        w_codes=w.codes.data_ptr(), w_scales=w.scales.data_ptr(),
+                        epilogue=epilogue)
+    if group_offsets is not None:
+        args.group_offsets = _vector(group_offsets, G + 1, torch.int32, dev, "group_offsets")
+    if gather_rows is not None:
+        args.gather_rows = _vector(gather_rows, total_rows, torch.int32, dev, "gather_rows")
+    elif src_rows < total_rows:
+        _refuse("activations of at least total_rows rows")
+    if quantized:
+        _int8(a, (src_rows, K), dev, "a")
+        args.a_codes, args.a_scales = a.codes.data_ptr(), a.scales.data_ptr()
+    else:
+        args.x, args.x_dtype = x.data_ptr(), _dtype_code(x)
+        args.ldx, args.src_rows = _row_stride(x, "x"), src_rows
+    if validate:
+        if group_offsets is None:
+            group_offsets = torch.tensor([0, total_rows], dtype=torch.int32)
+        check_groups(group_offsets, total_rows, gather_rows, src_rows)
+    odt = torch.float32 if epilogue == NVFP4_EPI_F32 else torch.bfloat16
+    cols = N // 2 if epilogue == NVFP4_EPI_SILU_MUL_BF16 else N
+    if out is None:
+        out = torch.empty(total_rows, cols, dtype=odt, device=dev)
+    elif out.shape != (total_rows, cols) or out.dtype != odt or out.device != dev \
+            or not out.is_contiguous():
+        _refuse(f"out: contiguous {odt} {(total_rows, cols)} on {dev}")
+    args.out = out.data_ptr()
+    L = lib()
+    ref = ctypes.byref(args)
+    n = L.int8_grouped_gemm_workspace_size(ref)
+    ws = _ws(n, dev) if n else None
+    _call(dev, L.int8_grouped_gemm, ref, None if ws is None else ws.data_ptr(), n)
+    return out
+
+
+# ------------------------------------------------- the router's balance loss
+def _mask(mask: Optional[torch.Tensor], T: int, dev):
+    if mask is None:
+        return None
+    if mask.dtype != torch.bool and mask.dtype != torch.uint8:
+        _refuse("mask: bool [T]")
+    return _vector(mask, T, mask.dtype, dev, "mask")
+
+
+def moe_balance_loss(logits: torch.Tensor, topk_ids: torch.Tensor, *,
+                     mask: Optional[torch.Tensor] = None) -> BalanceOut:
+    """Slots per expert, mean router probabilities, balance loss and z-loss of
+    logits [T, E] (bf16 or FP32, row stride honoured) and topk_ids [T, k]
+    (int32, moe_route's; an id outside [0, E) is a dropped slot).  Rows with
+    mask [T] (bool) false, or whose logits are all -inf, do not count."""
+    if logits.dim() != 2 or topk_ids.dim() != 2 or topk_ids.shape[0] != logits.shape[0]:
+        _refuse("logits [T, E] and topk_ids [T, k]")
+    T, E = logits.shape
+    k = topk_ids.shape[1]
+    dev = logits.device
+    dt = _dtype_code(logits)
+    if dev.type != "cuda":
+        _refuse("logits on a GPU")
+    if topk_ids.dtype != torch.int32 or topk_ids.device != dev or not topk_ids.is_contiguous():
+        _refuse(f"topk_ids: contiguous int32 [T, k] on {dev}")
+    m = _mask(mask, T, dev)
+    losses = torch.empty(2, dtype=torch.float32, device=dev)
+    counts = torch.empty(E, dtype=torch.int32, device=dev)
+    mean = torch.empty(E, dtype=torch.float32, device=dev)
+    tokens = torch.empty(1, dtype=torch.int32, device=dev)
+    L = lib()
+    ws = _ws(L.moe_balance_loss_workspace_size(T, E), dev)
+    _call(dev, L.moe_balance_loss, logits.data_ptr(), dt, T, E, _row_stride(logits, "logits"),
+          topk_ids.data_ptr(), k, m, counts.data_ptr(), tokens.data_ptr(), mean.data_ptr(),
+          losses.data_ptr(), ws.data_ptr(), ws.numel())
+    return BalanceOut(losses, counts, mean, tokens)
+
+
+def moe_balance_loss_backward(logits: torch.Tensor, k: int, counts: torch.Tensor,
+                              tokens: torch.Tensor, grad_losses: torch.Tensor, *,
+                              mask: Optional[torch.Tensor] = None,
+                              out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Gradient of the logits from that of moe_balance_loss's losses (float32
+    [2]), with its counts and tokens.  out: where to write it, which may be
+    logits itself."""
+    if logits.dim() != 2:
+        _refuse("logits [T, E]")
+    T, E = logits.shape
+    dev = logits.device
+    dt = _dtype_code(logits)
+    if dev.type != "cuda":
+        _refuse("logits on a GPU")
+    m = _mask(mask, T, dev)
+    c = _vector(counts, E, torch.int32, dev, "counts")
+    n = _vector(tokens, 1, torch.int32, dev, "tokens")
+    g = _vector(grad_losses, 2, torch.float32, dev, "grad_losses")
+    if out is None:
+        out = torch.empty(T, E, dtype=logits.dtype, device=dev)
+    elif out.shape != logits.shape or out.dtype != logits.dtype or out.device != dev:
+        _refuse("out like logits")
+    _call(dev, lib().moe_balance_loss_backward, logits.data_ptr(), dt, T, E,
+          _row_stride(logits, "logits"), k, m, c, n, g, out.data_ptr(), _row_stride(out, "out"))
     return out

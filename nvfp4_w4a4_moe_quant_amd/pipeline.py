@@ -18,6 +18,9 @@ For up to 64 tokens moe_decode computes the whole layer in two or three
 launches with unquantized activations, on the same weights; token_logprobs
 gives the log-probabilities and entropies of the tokens that both sides of
 the rollout-trainer gap are measured by, with their gradient.
+int8_linear and int8_moe_block are the dense layer and the MoE block in 8-bit
+integers (per-token and per-channel scales), a rollout to compare with;
+moe_balance_loss is the trainer's loss on the router that moe_route follows.
 Weights are quantized once, per expert and projection, by the same
 nvfp4_quantize (every engine quantizes the synchronized weights the same way:
 blog post, section "The failure mode").
@@ -351,3 +354,88 @@ def token_logprobs(logits: torch.Tensor, targets: torch.Tensor,
         raise RuntimeError("leaf logits under capture: use the library's token_logprobs and "
                            "token_logprobs_backward")
     return _TokenLogprobs.apply(logits, targets, inv_temperature)
+
+
+# ------------------------------------------------- INT8 W8A8 comparator
+def int8_quantize_weights(mats: Iterable[Tuple[int, torch.Tensor]], G: int, N: int, K: int,
+                          device) -> L.INT8:
+    """mats yields (group index, W_g [N, K] on any device); one scale for every
+    output channel."""
+    w = L.INT8(torch.empty((G, N, K), dtype=torch.int8, device=device),
+               torch.empty((G, N), dtype=torch.float32, device=device))
+    for g, wg in mats:
+        L.int8_quantize_rows(wg.to(device, non_blocking=True),
+                             out=L.INT8(w.codes[g], w.scales[g]))
+    return w
+
+
+def _int8_no_gradient(*tensors: torch.Tensor):
+    if torch.is_grad_enabled() and any(t.requires_grad for t in tensors):
+        raise RuntimeError("the INT8 layers have no gradient: detach their inputs or call them "
+                           "under torch.no_grad()")
+
+
+def int8_linear(x: torch.Tensor, w: L.INT8,
+                out_dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
+    """y = x W^T of x [rows, K] (bf16 or FP32), quantized per row by the call, and
+    w (codes [1, N, K], scales [1, N]), as bf16 or FP32 [rows, N]."""
+    _int8_no_gradient(x)
+    if out_dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"unsupported dtype {out_dtype}")
+    N, K = w.codes.shape[-2:]
+    return L.int8_grouped_gemm(
+        x, w, N=N, K=K, total_rows=x.shape[0],
+        epilogue=L.NVFP4_EPI_F32 if out_dtype == torch.float32 else L.NVFP4_EPI_BF16)
+
+
+def int8_moe_block(x: torch.Tensor, logits: torch.Tensor, wgu: L.INT8, wd: L.INT8, topk: int,
+                   out_dtype: torch.dtype = torch.bfloat16) -> Dict:
+    """moe_block in 8-bit integers: routing, gate/up on the rows of x quantized
+    per token, SiLU*mul, down on the rows of h quantized per row, combine.  wgu
+    holds [E, 2I, H] (gate rows first), wd [E, H, I]."""
+    _int8_no_gradient(x, logits)
+    rows = x.shape[0] * topk
+    rt = L.moe_route(logits, topk)
+    h = L.int8_grouped_gemm(x, wgu, rt.expert_offsets, N=wgu.codes.shape[1], K=wgu.codes.shape[2],
+                            total_rows=rows, gather_rows=rt.gather_rows,
+                            epilogue=L.NVFP4_EPI_SILU_MUL_BF16)
+    y = L.int8_grouped_gemm(h, wd, rt.expert_offsets, N=wd.codes.shape[1], K=wd.codes.shape[2],
+                            total_rows=rows)
+    out = L.moe_combine(y, rt.row_of, rt.topk_weights, out_dtype=out_dtype)
+    return dict(route=rt, h=h, y=y, out=out)
+
+
+# ------------------------------------------------- the router's balance loss
+class _BalanceLoss(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, topk_ids, mask):
+        r = L.moe_balance_loss(logits, topk_ids, mask=mask)
+        ctx.save_for_backward(logits, mask, r.counts, r.tokens)
+        ctx.k = topk_ids.shape[1]
+        ctx.mark_non_differentiable(r.counts, r.mean_probs, r.tokens)
+        ctx.set_materialize_grads(False)
+        return tuple(r)
+
+    @staticmethod
+    def backward(ctx, g_losses, *_):
+        if torch.is_grad_enabled():  # under create_graph
+            raise RuntimeError("moe_balance_loss has no second derivative")
+        logits, mask, counts, tokens = ctx.saved_tensors
+        if g_losses is None:
+            return None, None, None
+        return L.moe_balance_loss_backward(logits, ctx.k, counts, tokens, g_losses.contiguous(),
+                                           mask=mask), None, None
+
+
+def moe_balance_loss(logits: torch.Tensor, topk_ids: torch.Tensor,
+                     mask: Optional[torch.Tensor] = None) -> L.BalanceOut:
+    """The router's balance loss and z-loss (losses [2]) with the gradient of
+    logits [T, E], and the counts and mean probabilities, which get none.
+    topk_ids [T, k] is moe_route's choice.  There is no second derivative.  Leaf
+    logits that require a gradient are refused under graph capture, where
+    another living graph of the same leaf ends the process: capture the two
+    library calls instead."""
+    if logits.requires_grad and logits.is_leaf and torch.cuda.is_current_stream_capturing():
+        raise RuntimeError("leaf logits under capture: use the library's moe_balance_loss and "
+                           "moe_balance_loss_backward")
+    return L.BalanceOut(*_BalanceLoss.apply(logits, topk_ids, mask))
