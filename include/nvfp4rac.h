@@ -545,8 +545,8 @@ int int8_quantize_rows(const void* x, int in_dtype, int64_t rows, int64_t K, int
  * group are left alone.  Requires 1 <= N <= 2^24 (even for SiLU), K % 16 == 0,
  * 16 <= K <= 131056 (no sum of 8-bit products can leave 32 bits), num_groups <=
  * 2^20, total_rows < 2^31; codes and x 16-byte aligned, out aligned to its
- * elements, ws 16-byte aligned.  Without a gather, src_rows >= total_rows.
- * Calls that may overlap need workspaces of their own. */
+ * elements, ws 16-byte aligned.  Without a gather, src_rows >= total_rows;
+ * src_rows K <= 2^36.  Calls that may overlap need workspaces of their own. */
 typedef struct {
   int64_t num_groups;           /* G >= 1 */
   int64_t N;                    /* output columns (2I for SILU_MUL) */
@@ -558,7 +558,7 @@ typedef struct {
   const float* a_scales;        /* [src_rows] */
   const void* x;                /* [src_rows, K], or NULL where a_codes is given */
   int64_t x_dtype, ldx;         /* nvfp4_in_dtype_t; row stride in elements */
-  int64_t src_rows;             /* rows of x (read with x only) */
+  int64_t src_rows;             /* rows of a_codes or of x */
   const int8_t* w_codes;        /* [G, N, K] */
   const float* w_scales;        /* [G, N] */
   int64_t epilogue;             /* nvfp4_epilogue_t */

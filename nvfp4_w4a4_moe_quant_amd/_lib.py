@@ -705,7 +705,7 @@ def int8_grouped_gemm(a, w: INT8, group_offsets: Optional[torch.Tensor] = None, 
     _int8(w, (G, N, K), dev, "w")
     args = Int8GemmArgs(num_groups=G, N=N, K=K, total_rows=total_rows,
                         w_codes=w.codes.data_ptr(), w_scales=w.scales.data_ptr(),
-                        epilogue=epilogue)
+                        src_rows=src_rows, epilogue=epilogue)
     if group_offsets is not None:
         args.group_offsets = _vector(group_offsets, G + 1, torch.int32, dev, "group_offsets")
     if gather_rows is not None:
@@ -717,7 +717,7 @@ def int8_grouped_gemm(a, w: INT8, group_offsets: Optional[torch.Tensor] = None, 
         args.a_codes, args.a_scales = a.codes.data_ptr(), a.scales.data_ptr()
     else:
         args.x, args.x_dtype = x.data_ptr(), _dtype_code(x)
-        args.ldx, args.src_rows = _row_stride(x, "x"), src_rows
+        args.ldx = _row_stride(x, "x")
     if validate:
         if group_offsets is None:
             group_offsets = torch.tensor([0, total_rows], dtype=torch.int32)

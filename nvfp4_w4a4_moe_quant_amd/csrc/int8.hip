@@ -219,33 +219,46 @@ struct I8Tile {
   static constexpr int NW = WM * WN, NT = 64 * NW;
   static constexpr int BM = WM * FM * 32, BN = WN * FN * 32, ROWS = BM + BN;
   static constexpr int NPI = ROWS * 8 / NT;  // 16-byte pieces per thread per chunk
+  static constexpr int NPA = BM * 8 / NT;    // of them in A rows, which come first
   static constexpr int STAGE = ROWS * KC;
-  static_assert(ROWS * 8 % NT == 0, "whole wave-loads");
+#ifndef I8DS
+#define I8DS 2
+#endif
+  static constexpr int DS = NPI % I8DS ? 1 : I8DS;
+  static_assert(BM * 8 % NT == 0 && BN * 8 % NT == 0, "whole wave-loads");
   static_assert(!SILU || FN % 2 == 0, "SiLU pairs gate and up fragments");
   static_assert(NS >= 2 && (NS - 2) * NPI <= 63, "vmcnt range");
 
   const I8Params& p;
   uint8_t* lds;
-  const uint8_t* src[NPI];
+  const uint8_t *abase, *wbase, *ubase;  // the tile's first row of A, of W, of W's up half
+  uint32_t off[NPI];  // bytes from there to piece j; in a gather 16-byte units from A's start
   int lane, wave, wm, wn, lr, lh, nt, beg, end, cols, nfull, rem;
 
-  // Chunk into buffer `buf`; the chunk behind the last whole one holds `rem`
-  // bytes a row, and its pieces behind them read the chunk's first piece.
+  // Piece j of a chunk into buffer `buf`.  The chunk behind the last whole one
+  // (TAIL) holds `rem` bytes a row; its pieces behind them read the chunk's first
+  // piece, and the products skip them.
+  template <bool TAIL>
   __device__ __forceinline__ void issue1(int j, int chunk, int buf) {
     const uint32_t st = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)(lds + buf * STAGE);
     const uint32_t m0 = __builtin_amdgcn_readfirstlane(st + (j * NW + wave) * 1024);
-    const uint8_t* g = src[j] + (int64_t)chunk * KC;
-    if (chunk == nfull) {  // uniform
+    uint32_t back = 0;
+    if (TAIL && chunk == nfull) {
       const int slot = (j * NW + wave) * 64 + lane, row = slot >> 3;
-      const int at = ((slot & 7) ^ (int)i8_swz((uint32_t)row)) * 16;
-      if (at >= rem) g -= at;
+      const uint32_t at = ((uint32_t)(slot & 7) ^ i8_swz((uint32_t)row)) * 16;
+      back = at >= (uint32_t)rem ? at : 0u;
     }
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
-                 :: "s"(m0), "v"(g) : "memory", "m0");
-  }
-  __device__ __forceinline__ void issue(int chunk, int buf) {
-#pragma unroll
-    for (int j = 0; j < NPI; ++j) issue1(j, chunk, buf);
+    if (GATHER && j < NPA) {
+      const uint8_t* g = abase + (int64_t)chunk * KC - back + (uint64_t)off[j] * 16u;
+      asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
+                   :: "s"(m0), "v"(g) : "memory", "m0");
+    } else {
+      // wave-loads of gate and of up rows alternate by 32 rows
+      const bool up = SILU && ((((j - NPA) * NW + wave) >> 2) & 1);
+      const uint8_t* g = (j < NPA ? abase : up ? ubase : wbase) + (int64_t)chunk * KC;
+      asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+                   :: "s"(m0), "v"(off[j] - back), "s"(g) : "memory", "m0");
+    }
   }
 
   // Waits until this wave's pieces of the oldest chunk in flight have landed,
@@ -281,40 +294,55 @@ struct I8Tile {
         for (int e = 0; e < 16; ++e) acc[a][b][e] = 0;
     const int total = nfull + (rem ? 1 : 0);
     const uint32_t x = (lh ^ i8_swz((uint32_t)lr)) << 4;
-    const uint8_t* abase = lds + (wm * 32 + lr) * KC;
-    const uint8_t* wbase = lds + (BM + wn * FN * 32 + lr) * KC;
+    const uint8_t* al = lds + (wm * 32 + lr) * KC;
+    const uint8_t* wl = lds + (BM + wn * FN * 32 + lr) * KC;
     int4v af[2][NL ? NL : 1], wf[2][FN];
     // fragment i of step s: the W ones first
     auto load = [&](int i, int buf, int s, int4v* av, int4v* wv) {
       const uint32_t o = buf * STAGE + (x ^ (s << 5));
       if (i < FN)
-        wv[i] = *reinterpret_cast<const int4v*>(wbase + o + i * 32 * KC);
+        wv[i] = *reinterpret_cast<const int4v*>(wl + o + i * 32 * KC);
       else
-        av[i - FN] = *reinterpret_cast<const int4v*>(abase + o + (i - FN) * WM * 32 * KC);
+        av[i - FN] = *reinterpret_cast<const int4v*>(al + o + (i - FN) * WM * 32 * KC);
     };
     constexpr int NR = NL ? NL + FN : 0, NM = NL * FN;
-#pragma unroll
+    // A buffer is free from a chunk's last step on; the pieces of the chunk that
+    // takes it are issued over that step and the first DS - 1 of the next chunk.
+    constexpr int PART = NPI / DS;
+    static_assert(NPI % DS == 0 && DS <= 3, "pieces per step");
     for (int c = 0; c < NS; ++c)
-      if (c < total) issue(c, c);
-    if (total > NS - 1)
-      asm volatile("s_waitcnt vmcnt(%0)" ::"n"((NS - 1) * NPI) : "memory");
+      if (c < total) {
+#pragma unroll
+        for (int j = 0; j < NPI; ++j)
+          if (c < NS - 1 || j < PART) issue1<true>(j, c, c);
+      }
+    if (total >= NS)
+      asm volatile("s_waitcnt vmcnt(%0)" ::"n"((NS - 2) * NPI + PART) : "memory");
     else
       asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     barrier();
 #pragma unroll
     for (int i = 0; i < NR; ++i) load(i, 0, 0, af[0], wf[0]);
     int buf = 0;
-    for (int ch = 0; ch < nfull; ++ch) {
-      const int nb = buf + 1 == NS ? 0 : buf + 1;
+    // STEADY: the chunks ahead are there and whole
+    auto chunk = [&](auto steady, int ch) {
+      constexpr bool STEADY = decltype(steady)::value;
+      const int nb = buf + 1 == NS ? 0 : buf + 1, pb = buf == 0 ? NS - 1 : buf - 1;
 #pragma unroll
       for (int s = 0; s < 4; ++s) {
         if (s == 3) {
           // every wave has read the chunk and holds its last step; the next one
           // has landed
-          if (ch + 1 < total) landed(total - ch - 2);
+          if (STEADY)
+            landed(NS - 2);
+          else if (ch + 1 < total)
+            landed(total - ch - 2);
           barrier();
         }
-        const bool more = s == 3 && ch + NS < total;
+        const bool tail = s == 3 || s < DS - 1;  // a step that issues
+        const int nx = s == 3 ? ch + NS : ch + NS - 1, to = s == 3 ? buf : pb;
+        const int j0 = s == 3 ? 0 : (s + 1) * PART;
+        const bool more = tail && (STEADY || nx < total);
         const int cur = s & 1;
         constexpr int steps = NM ? NM : 1;
 #pragma unroll
@@ -322,10 +350,10 @@ struct I8Tile {
 #pragma unroll
           for (int j = i * 2; j < NR && j < i * 2 + 2; ++j)
             load(j, s == 3 ? nb : buf, (s + 1) & 3, af[cur ^ 1], wf[cur ^ 1]);
-          if (s == 3) {
+          if (more) {
 #pragma unroll
-            for (int j = i * NPI / steps; j < (i + 1) * NPI / steps; ++j)
-              if (more) issue1(j, ch + NS, buf);
+            for (int j = i * PART / steps; j < (i + 1) * PART / steps; ++j)
+              issue1<!STEADY>(j0 + j, nx, to);
           }
           if constexpr (NM > 0) {
             const int a = i / FN, b = i % FN;
@@ -335,7 +363,10 @@ struct I8Tile {
         }
       }
       buf = nb;
-    }
+    };
+    int ch = 0;
+    for (; ch + NS < nfull; ++ch) chunk(std::true_type{}, ch);
+    for (; ch < nfull; ++ch) chunk(std::false_type{}, ch);
     if (rem) {
       asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
       barrier();
@@ -425,8 +456,11 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_i8_gemm(I8Params p, int n_t
   constexpr int BM = Tile::BM, BN = Tile::BN;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[NS * Tile::STAGE];
   __shared__ __attribute__((aligned(16))) float sw[BN];  // the columns' scales
-  const NvTile t = i8_find_tile(p, BM, n_tiles);
-  if (t.grp < 0) return;  // identical in every wave
+  NvTile t = i8_find_tile(p, BM, n_tiles);
+  if (t.grp < 0) return;  // identical in every lane of every wave
+  t.grp = __builtin_amdgcn_readfirstlane(t.grp);
+  t.local = __builtin_amdgcn_readfirstlane(t.local);
+  t.nt = __builtin_amdgcn_readfirstlane(t.nt);
   Tile k{p, lds};
   k.lane = threadIdx.x & 63;
   k.wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -441,29 +475,33 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_i8_gemm(I8Params p, int n_t
   k.nfull = p.K / KC;
   k.rem = p.K % KC;
   const int64_t wrow = (int64_t)t.grp * p.N;
-  // W row of tile column i; columns past the last repeat it
+  // output column of W row i of the tile; those past the last repeat it
+  const int n0 = min(t.nt * (Tile::SILU ? BN / 2 : BN), k.cols - 1);
   auto column = [&](int i) {
     if constexpr (Tile::SILU) {
       const int f = i >> 5, b = f % FN;
-      return min(t.nt * (BN / 2) + (f / FN) * (FN / 2) * 32 + (b >> 1) * 32 + (i & 31), k.cols - 1) +
-             ((b & 1) ? k.cols : 0);
+      i = (f / FN) * (FN / 2) * 32 + (b >> 1) * 32 + (i & 31);
     }
-    return min(t.nt * BN + i, k.cols - 1);
+    return min(n0 + i, k.cols - 1);
   };
-  for (int i = threadIdx.x; i < BN; i += Tile::NT) sw[i] = p.w_scales[wrow + column(i)];
+  for (int i = threadIdx.x; i < BN; i += Tile::NT)
+    sw[i] = p.w_scales[wrow + column(i) + (Tile::SILU && (i >> 5 & 1) ? k.cols : 0)];
+  k.abase = reinterpret_cast<const uint8_t*>(p.a_codes) + (GATHER ? 0 : (int64_t)k.beg * p.K);
+  k.wbase = reinterpret_cast<const uint8_t*>(p.w_codes) + (wrow + n0) * p.K;
+  k.ubase = k.wbase + (int64_t)k.cols * p.K;
 #pragma unroll
   for (int j = 0; j < Tile::NPI; ++j) {
     const int slot = (j * Tile::NW + k.wave) * 64 + k.lane, row = slot >> 3;
-    const uint32_t piece = (uint32_t)(slot & 7) ^ i8_swz((uint32_t)row);
-    const uint8_t* base;
-    if (row < BM) {
-      const int m = min(k.beg + row, k.end - 1);
-      base = reinterpret_cast<const uint8_t*>(p.a_codes) +
-             (GATHER ? (int64_t)p.gather[m] : (int64_t)m) * p.K;
+    const uint32_t at = ((uint32_t)(slot & 7) ^ i8_swz((uint32_t)row)) * 16;
+    if (j < Tile::NPA) {
+      const int r = min(row, k.end - 1 - k.beg);
+      if constexpr (GATHER)
+        k.off[j] = (uint32_t)p.gather[k.beg + r] * (uint32_t)(p.K >> 4) + (at >> 4);
+      else
+        k.off[j] = (uint32_t)r * (uint32_t)p.K + at;
     } else {
-      base = reinterpret_cast<const uint8_t*>(p.w_codes) + (wrow + column(row - BM)) * p.K;
+      k.off[j] = (uint32_t)(column(row - BM) - n0) * (uint32_t)p.K + at;
     }
-    k.src[j] = base + piece * 16;
   }
   // fragments of 32 rows that hold rows: frag a of wave row wm starts at row
   // (a WM + wm) 32
@@ -544,12 +582,14 @@ int check_gemm(const int8_gemm_args_t* a) {
                    a->K % 16 || a->K > kMaxK ||
                    (a->epilogue == NVFP4_EPI_SILU_MUL_BF16 && a->N % 2),
                NVFP4_ERR_SHAPE);
+  // gathered rows are addressed by 32 bits of 16-byte units
+  NV_RETURN_IF(a->src_rows < 0 || a->src_rows > 0x7fffffff || a->src_rows * a->K > (1LL << 36) ||
+                   (!a->gather_rows && a->src_rows < a->total_rows) ||
+                   (a->src_rows == 0 && a->total_rows > 0),
+               NVFP4_ERR_SHAPE);
   if (a->x) {
     NV_RETURN_IF(a->x_dtype != NVFP4_IN_F32 && a->x_dtype != NVFP4_IN_BF16, NVFP4_ERR_DTYPE);
-    NV_RETURN_IF(a->src_rows < 0 || a->src_rows > 0x7fffffff || a->ldx < a->K ||
-                     (!a->gather_rows && a->src_rows < a->total_rows) ||
-                     (a->src_rows == 0 && a->total_rows > 0),
-                 NVFP4_ERR_SHAPE);
+    NV_RETURN_IF(a->ldx < a->K, NVFP4_ERR_SHAPE);
   }
   return NVFP4_OK;
 }

@@ -33,8 +33,8 @@ def test_rows_validation(lib):
 
 def _gemm(lib, ws=None, wsb=0, size=False, **kw):
     a = L.Int8GemmArgs(num_groups=2, N=100, K=48, total_rows=10, group_offsets=FAKE,
-                       a_codes=FAKE, a_scales=FAKE, w_codes=FAKE, w_scales=FAKE, epilogue=0,
-                       out=FAKE)
+                       a_codes=FAKE, a_scales=FAKE, src_rows=10, w_codes=FAKE, w_scales=FAKE,
+                       epilogue=0, out=FAKE)
     for k, v in kw.items():
         setattr(a, k, v)
     if size:
@@ -57,6 +57,10 @@ def test_gemm_validation(lib):
     assert g(N=101, epilogue=1) == ESHAPE               # gate and up columns in pairs
     assert g(num_groups=0) == ESHAPE and g(num_groups=(1 << 20) + 1) == ESHAPE
     assert g(total_rows=-1) == ESHAPE and g(total_rows=1 << 31) == ESHAPE
+    assert g(src_rows=9) == ESHAPE                      # fewer than total_rows, no gather
+    assert g(src_rows=0, gather_rows=FAKE) == ESHAPE
+    assert g(src_rows=1 << 33, K=48) == ESHAPE
+    assert g(src_rows=(1 << 30) + 1, K=64, gather_rows=FAKE) == ESHAPE    # 2^36 bytes
     assert g(a_codes=MIS[8]) == EALIGN and g(w_codes=MIS[8]) == EALIGN
     assert g(a_scales=MIS[2]) == EALIGN and g(w_scales=MIS[2]) == EALIGN
     assert g(out=MIS[2]) == EALIGN and g(out=MIS[1], epilogue=2) == EALIGN
