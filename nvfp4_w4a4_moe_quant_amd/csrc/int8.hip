@@ -83,30 +83,67 @@ __device__ __forceinline__ uint2 i8_encode8(const float* v, float r) {
   return o;
 }
 
-// One wave per row, four rows per workgroup; the row is read twice (the
-// second read hits the caches).
-template <bool BF16>
-__global__ __launch_bounds__(256) void k_i8_rows(const void* x, int64_t rows, int K, int64_t ldx,
+// RW waves per row (RW divides the workgroup's eight).  A lane holds VPL vectors
+// of 8 elements between the maximum and the encode; longer rows (K > 512 VPL RW)
+// are read again (the second read hits the caches).
+template <bool BF16, int RW, int VPL>
+__global__ __launch_bounds__(512) void k_i8_rows(const void* x, int64_t rows, int K, int64_t ldx,
                                                  int8_t* codes, float* scales) {
-  const int lane = threadIdx.x & 63;
+  constexpr int RPW = 8 / RW;  // rows of a workgroup
+  __shared__ uint32_t mags[8];
+  const int wave = threadIdx.x >> 6, tid = threadIdx.x % (64 * RW);
   const int nv = K >> 3;
-  for (int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); row < rows;
-       row += (int64_t)gridDim.x * 4) {
+  for (int64_t r0 = (int64_t)blockIdx.x * RPW; r0 < rows; r0 += (int64_t)gridDim.x * RPW) {
+    const int64_t row = r0 + wave / RW;
+    const bool live = row < rows;  // uniform in the row's waves
+    const int64_t at = live ? row * ldx : 0;
+    float v[VPL][8];
     uint32_t mag = 0;
-    for (int c = lane; c < nv; c += 64) {
-      float v[8];
-      i8_load8<BF16>(x, row * ldx + 8 * c, v);
+    if (live) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) mag = max(mag, i8_mag(v[e]));
+      for (int i = 0; i < VPL; ++i) {
+        const int c = tid + 64 * RW * i;
+        if (c < nv) {
+          i8_load8<BF16>(x, at + 8 * c, v[i]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[i][e] = 0.0f;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < VPL; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) mag = max(mag, i8_mag(v[i][e]));
+      for (int c = tid + 64 * RW * VPL; c < nv; c += 64 * RW) {
+        float w[8];
+        i8_load8<BF16>(x, at + 8 * c, w);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) mag = max(mag, i8_mag(w[e]));
+      }
+      mag = i8_wave_max(mag);
     }
+    if constexpr (RW > 1) {
+      __syncthreads();  // the last row's maxima have been read
+      if ((threadIdx.x & 63) == 0) mags[wave] = mag;
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < RW; ++i) mag = max(mag, mags[wave / RW * RW + i]);
+    }
+    if (!live) continue;
     float s, r;
-    i8_row_scale(i8_wave_max(mag), s, r);
-    for (int c = lane; c < nv; c += 64) {
-      float v[8];
-      i8_load8<BF16>(x, row * ldx + 8 * c, v);
-      *reinterpret_cast<uint2*>(codes + row * (int64_t)K + 8 * c) = i8_encode8(v, r);
+    i8_row_scale(mag, s, r);
+    int8_t* out = codes + row * (int64_t)K;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      const int c = tid + 64 * RW * i;
+      if (c < nv) *reinterpret_cast<uint2*>(out + 8 * c) = i8_encode8(v[i], r);
     }
-    if (lane == 0) scales[row] = s;
+    for (int c = tid + 64 * RW * VPL; c < nv; c += 64 * RW) {
+      float w[8];
+      i8_load8<BF16>(x, at + 8 * c, w);
+      *reinterpret_cast<uint2*>(out + 8 * c) = i8_encode8(w, r);
+    }
+    if (tid == 0) scales[row] = s;
   }
 }
 
@@ -129,66 +166,6 @@ __device__ __forceinline__ float i8_silu_mul(float g, float u) {
   return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)) * u;
 }
 
-// A wave computes 16 rows of one group by 16 output columns (with SiLU*mul 16
-// gate and the 16 up columns) over the whole of K, its operands read from
-// memory in v_mfma_i32_16x16x64_i8's layout: lane l feeds row (or column) l % 16
-// with the 16 bytes k = 16 (l / 16) + 0..15 of a 64-k step.  Workgroups of four
-// waves (64 columns), grid (column blocks, groups).
-template <int EPI, bool GATHER>
-__global__ __launch_bounds__(256) void k_i8_direct(I8Params p) {
-  constexpr bool SILU = EPI == NVFP4_EPI_SILU_MUL_BF16;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int c = lane & 15, q = lane >> 4;
-  const int cols = SILU ? p.N >> 1 : p.N;
-  const int n0 = (int)(blockIdx.x * 4 + wave) * 16;
-  if (n0 >= cols) return;
-  const int nw = min(n0 + c, cols - 1);
-  for (int grp = (int)blockIdx.y; grp < p.G; grp += (int)gridDim.y) {
-    const int beg = p.offsets ? p.offsets[grp] : 0;
-    const int end = p.offsets ? p.offsets[grp + 1] : p.total_rows;
-    const int64_t wrow = (int64_t)grp * p.N + nw;
-    const int8_t* w0 = p.w_codes + wrow * p.K;
-    const int8_t* w1 = w0 + (SILU ? (int64_t)cols * p.K : 0);
-    for (int m0 = beg; m0 < end; m0 += 16) {
-      const int m = min(m0 + c, end - 1);
-      const int64_t src = GATHER ? (int64_t)p.gather[m] : (int64_t)m;
-      const int8_t* a = p.a_codes + src * p.K;
-      int4v acc = {0, 0, 0, 0}, acc1 = {0, 0, 0, 0};
-      for (int k = 0; k < p.K; k += 64) {
-        const int kk = k + 16 * q;
-        int4v av = {0, 0, 0, 0}, wv = {0, 0, 0, 0}, uv = {0, 0, 0, 0};
-        if (kk < p.K) {
-          av = *reinterpret_cast<const int4v*>(a + kk);
-          wv = *reinterpret_cast<const int4v*>(w0 + kk);
-          if constexpr (SILU) uv = *reinterpret_cast<const int4v*>(w1 + kk);
-        }
-        acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(av, wv, acc, 0, 0, 0);
-        if constexpr (SILU) acc1 = __builtin_amdgcn_mfma_i32_16x16x64_i8(av, uv, acc1, 0, 0, 0);
-      }
-      // element i of lane (c, q): row m0 + 4 q + i, column n0 + c
-      if (n0 + c >= cols) continue;
-      const float sw = p.w_scales[wrow];
-      const float su = SILU ? p.w_scales[wrow + cols] : 0.0f;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int row = m0 + 4 * q + i;
-        if (row >= end) break;
-        const float sa = p.a_scales[GATHER ? (int64_t)p.gather[row] : (int64_t)row];
-        const float y = (sa * sw) * (float)acc[i];
-        const int64_t o = (int64_t)row * cols + n0 + c;
-        if constexpr (SILU)
-          reinterpret_cast<uint16_t*>(p.out)[o] = i8_bf16(i8_silu_mul(y, (sa * su) * (float)acc1[i]));
-        else if constexpr (EPI == NVFP4_EPI_BF16)
-          reinterpret_cast<uint16_t*>(p.out)[o] = i8_bf16(y);
-        else
-          reinterpret_cast<float*>(p.out)[o] = y;
-      }
-    }
-  }
-}
-
-// ------------------------------------------------------------ prefill tiles
-
 // Tile of a workgroup, in the order of nv_find_tile<8> (bands of eight m-tiles,
 // contiguous ranges of tiles per XCD).  Without offsets the one group's tiles
 // need no scan.
@@ -205,6 +182,153 @@ __device__ __forceinline__ NvTile i8_find_tile(const I8Params& p, int bm, int n_
   t.nt = j / gm;
   return t;
 }
+
+// ----------------------------------------------------------------- few rows
+
+// A workgroup of eight waves computes a tile of up to 16 RT rows of one group: CW =
+// 8 / KW blocks of 16 output columns (with SiLU*mul 16 gate and the 16 up
+// columns), KW waves to a block, which split K and add up through LDS.  W and the
+// rows go from memory to registers in v_mfma_i32_16x16x64_i8's layout (lane l: W
+// row or row l % 16, the 16 bytes k = 16 (l / 16) of a 64-k step), a batch of
+// steps ahead of its use.  D holds row l % 16 and columns 4 (l / 16) + 0..3 in
+// lane l.
+constexpr int kFewSteps = 4;
+
+template <int EPI, bool GATHER, int KW, int RT>
+__global__ __launch_bounds__(512) void k_i8_few(I8Params p, int n_tiles) {
+  constexpr bool SILU = EPI == NVFP4_EPI_SILU_MUL_BF16;
+  constexpr int FB = SILU ? 2 : 1, CW = 8 / KW;
+  __shared__ int4v red[8][FB * RT][64];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int c = lane & 15, q = lane >> 4;
+  const int cols = SILU ? p.N >> 1 : p.N;
+  // row tile and column block of the workgroup
+  const int mt = (int)(blockIdx.x / (unsigned)n_tiles), nt = (int)(blockIdx.x % (unsigned)n_tiles);
+  int grp = 0, beg = mt * 16 * RT, end = p.total_rows;
+  if (p.offsets) {
+    int run = 0;
+    grp = -1;
+    for (int g0 = 0; g0 < p.G; g0 += 64) {
+      const int tiles = nv_group_tiles(p.offsets, p.G, g0 + lane, 16 * RT);
+      int inc = tiles;
+#pragma unroll
+      for (int o = 1; o < 64; o <<= 1) {
+        const int n = __shfl_up(inc, o, 64);
+        if (lane >= o) inc += n;
+      }
+      const unsigned long long hit = __ballot(run + inc > mt);
+      if (hit) {
+        const int l = __ffsll((long long)hit) - 1;
+        grp = __builtin_amdgcn_readfirstlane(g0 + l);
+        const int local = mt - run - __builtin_amdgcn_readlane(inc - tiles, l);
+        beg = p.offsets[grp] + local * 16 * RT;
+        end = p.offsets[grp + 1];
+        break;
+      }
+      run += __builtin_amdgcn_readlane(inc, 63);
+    }
+    if (grp < 0) return;  // a surplus workgroup
+  }
+  const int n0 = (nt * CW + wave / KW) * 16;
+  const int steps = (p.K + 63) >> 6, part = wave % KW;
+  const int s0 = n0 < cols ? (int)((int64_t)steps * part / KW) : 0;
+  const int s1 = n0 < cols ? (int)((int64_t)steps * (part + 1) / KW) : 0;
+  const int64_t wrow = (int64_t)grp * p.N;
+  const int n = n0 + 4 * q;
+  const int8_t* w0 = p.w_codes + (wrow + min(n0 + c, cols - 1)) * p.K;
+  const int8_t* w1 = w0 + (SILU ? (int64_t)cols * p.K : 0);
+  const int8_t* row[RT];
+  bool mv[RT];
+  float sa[RT], sw[FB][4];
+#pragma unroll
+  for (int t = 0; t < RT; ++t) {
+    const int m = beg + t * 16 + c;
+    mv[t] = m < end;
+    const int64_t src = mv[t] ? (GATHER ? (int64_t)p.gather[m] : (int64_t)m) : 0;
+    row[t] = p.a_codes + src * p.K;
+    sa[t] = mv[t] ? p.a_scales[src] : 0.0f;
+  }
+  const int4v zero = {0, 0, 0, 0};
+  int4v wf[2][FB][kFewSteps], af[2][RT][kFewSteps];
+  auto load = [&](int s, int h) {
+#pragma unroll
+    for (int u = 0; u < kFewSteps; ++u) {
+      const int k = (s + u) * 64 + q * 16;
+      const bool on = s + u < s1 && k < p.K;
+      wf[h][0][u] = on ? *reinterpret_cast<const int4v*>(w0 + k) : zero;
+      if constexpr (SILU) wf[h][1][u] = on ? *reinterpret_cast<const int4v*>(w1 + k) : zero;
+#pragma unroll
+      for (int t = 0; t < RT; ++t)
+        af[h][t][u] = on && mv[t] ? *reinterpret_cast<const int4v*>(row[t] + k) : zero;
+    }
+  };
+  load(s0, 0);
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int f = 0; f < FB; ++f) sw[f][i] = p.w_scales[wrow + f * cols + min(n + i, cols - 1)];
+  int4v acc[RT][FB];
+#pragma unroll
+  for (int t = 0; t < RT; ++t)
+#pragma unroll
+    for (int f = 0; f < FB; ++f) acc[t][f] = zero;
+  auto multiply = [&](int h) {
+#pragma unroll
+    for (int u = 0; u < kFewSteps; ++u)
+#pragma unroll
+      for (int t = 0; t < RT; ++t)
+#pragma unroll
+        for (int f = 0; f < FB; ++f)
+          acc[t][f] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wf[h][f][u], af[h][t][u], acc[t][f], 0, 0, 0);
+  };
+  for (int s = s0; s < s1; s += 2 * kFewSteps) {
+    load(s + kFewSteps, 1);
+    multiply(0);
+    load(s + 2 * kFewSteps, 0);
+    multiply(1);
+  }
+#pragma unroll
+  for (int t = 0; t < RT; ++t)
+#pragma unroll
+    for (int f = 0; f < FB; ++f) red[wave][t * FB + f][lane] = acc[t][f];
+  __syncthreads();
+  // the KW waves of a block share its row tiles
+#pragma unroll
+  for (int t = 0; t < RT; ++t) {
+    if (t % KW != part || !mv[t] || n >= cols) continue;
+    int4v sum[FB];
+#pragma unroll
+    for (int f = 0; f < FB; ++f) {
+      sum[f] = zero;
+#pragma unroll
+      for (int i = 0; i < KW; ++i) sum[f] += red[wave - part + i][t * FB + f][lane];
+    }
+    float y[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      y[i] = (sa[t] * sw[0][i]) * (float)sum[0][i];
+      if constexpr (SILU) y[i] = i8_silu_mul(y[i], (sa[t] * sw[1][i]) * (float)sum[1][i]);
+    }
+    using OutT = std::conditional_t<EPI == NVFP4_EPI_F32, float, uint16_t>;
+    OutT* out = reinterpret_cast<OutT*>(p.out) + (int64_t)(beg + t * 16 + c) * cols + n;
+    if (p.vec) {  // whole pieces of four columns
+      if constexpr (EPI == NVFP4_EPI_F32)
+        *reinterpret_cast<float4*>(out) = make_float4(y[0], y[1], y[2], y[3]);
+      else
+        *reinterpret_cast<uint2*>(out) = make_uint2(i8_bf16(y[0]) | (uint32_t)i8_bf16(y[1]) << 16,
+                                                    i8_bf16(y[2]) | (uint32_t)i8_bf16(y[3]) << 16);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (n + i < cols) {
+          if constexpr (EPI == NVFP4_EPI_F32) out[i] = y[i];
+          else out[i] = i8_bf16(y[i]);
+        }
+    }
+  }
+}
+
+// ------------------------------------------------------------ prefill tiles
 
 constexpr int KC = 128;  // k (= bytes) per row per chunk: eight 16-byte pieces
 
@@ -227,7 +351,7 @@ struct I8Tile {
   static constexpr int DS = NPI % I8DS ? 1 : I8DS;
   static_assert(BM * 8 % NT == 0 && BN * 8 % NT == 0, "whole wave-loads");
   static_assert(!SILU || FN % 2 == 0, "SiLU pairs gate and up fragments");
-  static_assert(NS >= 2 && (NS - 2) * NPI <= 63, "vmcnt range");
+  static_assert(NS >= 2 && (NS - 1) * NPI <= 63, "vmcnt range");
 
   const I8Params& p;
   uint8_t* lds;
@@ -533,40 +657,119 @@ int launch_tiles(const I8Params& p, hipStream_t s) {
   return nv_launch_status();
 }
 
-// One group: 256 x 256 tiles of eight 64 x 128 waves (65536 x 4096 x 8192: 1872
-// us; 320 x 256 tiles 1931).  Groups: 320 x 256 tiles, whose waves skip 32-row
-// fragments without rows, so that an expert of some 256 rows takes one tile and
-// not two (65536 x 4096 x 7168 over 256 experts: 2204 against 2724 us).
+template <int EPI, int KW, int RT>
+int launch_few(const I8Params& p, int64_t tiles, hipStream_t s) {
+  const int cols = EPI == NVFP4_EPI_SILU_MUL_BF16 ? p.N / 2 : p.N;
+  const int n_tiles = (cols + 128 / KW - 1) / (128 / KW);
+  const dim3 grid((unsigned)(tiles * n_tiles)), block(512);
+  if (p.gather)
+    hipLaunchKernelGGL((k_i8_few<EPI, true, KW, RT>), grid, block, 0, s, p, n_tiles);
+  else
+    hipLaunchKernelGGL((k_i8_few<EPI, false, KW, RT>), grid, block, 0, s, p, n_tiles);
+  return nv_launch_status();
+}
+
+// Which kernel takes a call.
+struct I8Plan {
+  int few;        // k_i8_few with so many waves to a block of columns, or 0
+  int rt;         // its row tiles of 16 to a workgroup
+  int64_t tiles;  // workgroups' row tiles at most
+  int tile;       // else: the tile shape
+};
+
+I8Plan plan_of(const int8_gemm_args_t* a) {
+  I8Plan pl{};
+  const bool silu = a->epilogue == NVFP4_EPI_SILU_MUL_BF16;
+  const int64_t cols = silu ? a->N / 2 : a->N, rows = a->total_rows, G = a->num_groups;
+#ifndef I8FEW
+#define I8FEW 1024
+#endif
+  pl.rt = G > 1 || rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
+  pl.tiles = G == 1 ? (rows + 16 * pl.rt - 1) / (16 * pl.rt) : (rows < G ? rows : G) + rows / 16;
+  const int64_t units = pl.tiles * ((cols + 15) / 16);
+  if (rows <= (G == 1 ? 256 : 16 * G) && units <= I8FEW)
+#ifdef I8KW
+    pl.few = I8KW;
+#else
+    pl.few = units * 2 >= 1536 ? 2 : units * 4 >= 1536 ? 4 : 8;
+#endif
+  const double mean = (double)rows / (double)G;
+  if (G == 1) {
+    auto rounds = [&](int64_t bm, int64_t bn) {
+      return (double)((((rows + bm - 1) / bm) * ((a->N + bn - 1) / bn) + 255) / 256);
+    };
+    const double c[4] = {rounds(64, 128) * 0.19 + 0.1, rounds(128, 256) * 0.62, rounds(256, 256),
+                         rounds(320, 256) * 1.25};
+    for (int i = 1; i < 4; ++i)
+      if (c[i] < c[pl.tile]) pl.tile = i;
+  } else if (mean <= 48) {
+    pl.tile = 0;
+  } else if (mean <= 112) {
+    pl.tile = 1;
+  } else {
+    const double most = mean + 2 * __builtin_sqrt(mean);
+    pl.tile = __builtin_ceil(most / 320) * 1.22 < __builtin_ceil(most / 256) ? 3 : 2;
+  }
+  return pl;
+}
+
 template <int EPI>
-int launch_prefill(const I8Params& p, hipStream_t s) {
+int launch_gemm(const I8Params& p, const I8Plan& pl, hipStream_t s) {
+  if (pl.few) {
+    if (pl.rt == 1) {
+      if (pl.few == 2) return launch_few<EPI, 2, 1>(p, pl.tiles, s);
+      if (pl.few == 4) return launch_few<EPI, 4, 1>(p, pl.tiles, s);
+      return launch_few<EPI, 8, 1>(p, pl.tiles, s);
+    }
+    if (pl.rt == 2) {
+      if (pl.few == 2) return launch_few<EPI, 2, 2>(p, pl.tiles, s);
+      if (pl.few == 4) return launch_few<EPI, 4, 2>(p, pl.tiles, s);
+      return launch_few<EPI, 8, 2>(p, pl.tiles, s);
+    }
+    if (pl.few == 2) return launch_few<EPI, 2, 4>(p, pl.tiles, s);
+    if (pl.few == 4) return launch_few<EPI, 4, 4>(p, pl.tiles, s);
+    return launch_few<EPI, 8, 4>(p, pl.tiles, s);
+  }
 #ifdef I8CFG
   return launch_tiles<I8CFG, EPI>(p, s);
 #else
-  if (!p.offsets) return launch_tiles<4, 2, 2, 4, 2, EPI>(p, s);
+  if (pl.tile == 0) return launch_tiles<2, 2, 1, 2, 2, EPI>(p, s);
+  if (pl.tile == 1) return launch_tiles<2, 4, 2, 2, 3, EPI>(p, s);
+  if (pl.tile == 2) return launch_tiles<4, 2, 2, 4, 2, EPI>(p, s);
   return launch_tiles<2, 4, 5, 2, 2, EPI>(p, s);
 #endif
 }
 
-template <int EPI>
-int launch_direct(const I8Params& p, hipStream_t s) {
-  const int cols = EPI == NVFP4_EPI_SILU_MUL_BF16 ? p.N / 2 : p.N;
-  const dim3 grid((unsigned)((cols + 63) / 64), (unsigned)min(p.G, 65535));
-  if (p.gather)
-    hipLaunchKernelGGL((k_i8_direct<EPI, true>), grid, dim3(256), 0, s, p);
-  else
-    hipLaunchKernelGGL((k_i8_direct<EPI, false>), grid, dim3(256), 0, s, p);
+template <bool BF16, int RW, int VPL>
+int launch_rows_of(const void* x, int64_t rows, int K, int64_t ldx, int8_t* codes, float* scales,
+                   hipStream_t s) {
+  const int64_t wgs = (rows * RW + 7) / 8;
+  const dim3 grid((unsigned)(wgs < (1 << 20) ? wgs : (1 << 20)));
+  hipLaunchKernelGGL((k_i8_rows<BF16, RW, VPL>), grid, dim3(512), 0, s, x, rows, K, ldx, codes,
+                     scales);
   return nv_launch_status();
+}
+
+template <bool BF16>
+int launch_rows_bf16(const void* x, int64_t rows, int K, int64_t ldx, int8_t* codes, float* scales,
+                     hipStream_t s) {
+  const int nv = K / 8;
+  if (rows <= 512 && nv > 64) {
+    if (nv <= 512) return launch_rows_of<BF16, 8, 1>(x, rows, K, ldx, codes, scales, s);
+    return launch_rows_of<BF16, 8, 4>(x, rows, K, ldx, codes, scales, s);
+  }
+  if (nv <= 64) return launch_rows_of<BF16, 1, 1>(x, rows, K, ldx, codes, scales, s);
+  if (nv <= 128) return launch_rows_of<BF16, 1, 2>(x, rows, K, ldx, codes, scales, s);
+  if (nv <= 256) return launch_rows_of<BF16, 1, 4>(x, rows, K, ldx, codes, scales, s);
+  if (nv <= 512) return launch_rows_of<BF16, 2, 4>(x, rows, K, ldx, codes, scales, s);
+  if (nv <= 1024) return launch_rows_of<BF16, 4, 4>(x, rows, K, ldx, codes, scales, s);
+  return launch_rows_of<BF16, 8, 4>(x, rows, K, ldx, codes, scales, s);
 }
 
 int launch_rows(const void* x, int64_t dtype, int64_t rows, int K, int64_t ldx, int8_t* codes,
                 float* scales, hipStream_t s) {
-  const int64_t wgs = (rows + 3) / 4;
-  const dim3 grid((unsigned)(wgs < (1 << 20) ? wgs : (1 << 20)));
-  if (dtype == NVFP4_IN_BF16)
-    hipLaunchKernelGGL(k_i8_rows<true>, grid, dim3(256), 0, s, x, rows, K, ldx, codes, scales);
-  else
-    hipLaunchKernelGGL(k_i8_rows<false>, grid, dim3(256), 0, s, x, rows, K, ldx, codes, scales);
-  return nv_launch_status();
+  return dtype == NVFP4_IN_BF16 ? launch_rows_bf16<true>(x, rows, K, ldx, codes, scales, s)
+                                : launch_rows_bf16<false>(x, rows, K, ldx, codes, scales, s);
 }
 
 bool misaligned(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) != 0; }
@@ -647,6 +850,7 @@ int int8_grouped_gemm(const int8_gemm_args_t* a, void* ws, size_t ws_bytes, void
   p.out = a->out;
   const int64_t cols = a->epilogue == NVFP4_EPI_SILU_MUL_BF16 ? a->N / 2 : a->N;
   p.vec = !misaligned(a->out, 16) && cols * esize % 16 == 0;
+  const I8Plan pl = plan_of(a);
   if (a->x) {
     int8_t* codes = reinterpret_cast<int8_t*>(ws);
     float* scales = reinterpret_cast<float*>(codes + nv_round256((size_t)a->src_rows * p.K));
@@ -655,14 +859,10 @@ int int8_grouped_gemm(const int8_gemm_args_t* a, void* ws, size_t ws_bytes, void
     const int st = launch_rows(a->x, a->x_dtype, a->src_rows, p.K, a->ldx, codes, scales, s);
     if (st != NVFP4_OK) return st;
   }
-  if (p.total_rows > 16 * p.G) {
-    if (a->epilogue == NVFP4_EPI_SILU_MUL_BF16) return launch_prefill<NVFP4_EPI_SILU_MUL_BF16>(p, s);
-    if (a->epilogue == NVFP4_EPI_BF16) return launch_prefill<NVFP4_EPI_BF16>(p, s);
-    return launch_prefill<NVFP4_EPI_F32>(p, s);
-  }
-  if (a->epilogue == NVFP4_EPI_SILU_MUL_BF16) return launch_direct<NVFP4_EPI_SILU_MUL_BF16>(p, s);
-  if (a->epilogue == NVFP4_EPI_BF16) return launch_direct<NVFP4_EPI_BF16>(p, s);
-  return launch_direct<NVFP4_EPI_F32>(p, s);
+  if (a->epilogue == NVFP4_EPI_SILU_MUL_BF16)
+    return launch_gemm<NVFP4_EPI_SILU_MUL_BF16>(p, pl, s);
+  if (a->epilogue == NVFP4_EPI_BF16) return launch_gemm<NVFP4_EPI_BF16>(p, pl, s);
+  return launch_gemm<NVFP4_EPI_F32>(p, pl, s);
 }
 
 }  // extern "C"
