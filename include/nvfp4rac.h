@@ -544,7 +544,7 @@ int int8_quantize_rows(const void* x, int in_dtype, int64_t rows, int64_t K, int
  * group_offsets may be NULL with one group.  Rows of out that belong to no
  * group are left alone.  Requires 1 <= N <= 2^24 (even for SiLU), K % 16 == 0,
  * 16 <= K <= 131056 (no sum of 8-bit products can leave 32 bits), num_groups <=
- * 2^20, total_rows < 2^31; codes and x 16-byte aligned, out aligned to its
+ * 2^20, total_rows <= 2^30; codes and x 16-byte aligned, out aligned to its
  * elements, ws 16-byte aligned.  Without a gather, src_rows >= total_rows;
  * src_rows K <= 2^36.  Calls that may overlap need workspaces of their own. */
 typedef struct {
@@ -597,7 +597,8 @@ int int8_grouped_gemm(const int8_gemm_args_t* args, void* ws, size_t ws_bytes, v
  * 16-byte pieces).  topk_ids int32 [T, k] (moe_route's), mask uint8 [T] or
  * NULL.  mean_probs is nullable.  grad_logits has row stride ldg >= E and may
  * be the logits themselves (same ld).  Requires 1 <= E <= 1024, 1 <= k <= E, T k <
- * 2^31.  Sums are FP32 over at most some hundreds of rows and FP64 above that;
+ * 2^31.  Sums over rows are FP32 over the rows of a workgroup (T / 256, half a
+ * hundred at least) and FP64 above that;
  * exponentials and logarithms are the hardware's.  The results are
  * deterministic.  Calls that may overlap need workspaces of their own.
  * ------------------------------------------------------------------------ */

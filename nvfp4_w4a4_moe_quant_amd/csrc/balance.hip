@@ -1,10 +1,13 @@
 // Balance loss of an MoE router: per-expert counts and mean probabilities, the
 // balance loss and the z-loss, and the gradient of the logits.
 //
-// Per counted row, p = softmax(l) and lse = m + ln sum e^(l - m).  Forward, a
-// lane keeps the sums of its experts' probabilities over the rows of its wave,
-// which never leave registers; workgroups write partial sums and a second
-// launch joins them.  Backward needs the counts alone besides the row itself:
+// Per counted row, p = softmax(l) and lse = m + ln sum e^(l - m).  A row is held by
+// LPR lanes, V logits to a load, so that a wave works on 64 / LPR rows at a time
+// with the next ones in flight.  Forward, a lane keeps the sums of its experts'
+// probabilities over the rows of its wave; workgroups write partial sums, and a
+// second launch joins them, a workgroup for 32 experts each, the last of them
+// adding up the loss.  At most 128 rows take one launch of one workgroup.
+// Backward needs the counts alone besides the row itself:
 //   grad_j = p_j (a (c_j - sum_e c_e p_e) + b lse).
 // The counts enter centred, c_j - (sum c) / E, which changes nothing since the p
 // sum to one and keeps the difference small where the experts are balanced.
@@ -17,8 +20,10 @@ namespace {
 
 constexpr int kMaxE = 1024;
 constexpr float kLog2E = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
-constexpr int kFwdWaves = 4;
-constexpr int kFwdBlocks = 256;  // workgroups (partial sums) at most
+constexpr int kFwdWaves = 16;
+constexpr int kFwdBlocks = 256;   // workgroups (partial sums) at most
+constexpr int64_t kOneBlock = 128;  // rows that one workgroup takes alone
+constexpr int kJoinCols = 32, kJoinParts = 32;
 
 struct BalParams {
   const void* logits;
@@ -30,233 +35,436 @@ struct BalParams {
   int32_t* tokens;
   float* mean;
   float* losses;
-  // partial sums: float p[nblk][E], z[nblk]; int32 counts[nblk][E], n[nblk]
-  float* part_p;
-  float* part_z;
-  int32_t* part_c;
-  int32_t* part_n;
+  // partial sums of nblk workgroups, and what the joining ones share
+  float* part_p;     // [nblk][E]
+  float* part_z;     // [nblk]
+  int32_t* part_c;   // [nblk][E]
+  int32_t* part_n;   // [nblk]
+  double* dots;      // [E / 32]
+  uint32_t* joined;
   const float* grad_losses;
   void* grad;
   int64_t ldg;
 };
 
-template <bool BF16>
-__device__ __forceinline__ float bal_load(const void* x, int64_t i) {
-  if constexpr (BF16) return nv_bf16_to_f32(reinterpret_cast<const uint16_t*>(x)[i]);
-  return reinterpret_cast<const float*>(x)[i];
+template <int CTRL>
+__device__ __forceinline__ float bal_dpp(float v) {
+  return __int_as_float(
+      __builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xf, 0xf, true));
 }
 
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
+// op over the LPR lanes of a row, in every lane of it: neighbours and quads by
+// quad_perm, 8 and 16 lanes by the half and whole row mirrored, 32 and 64 by the
+// lane swaps.
+template <int LPR, class Op>
+__device__ __forceinline__ float bal_reduce(float v, Op op) {
+  v = op(v, bal_dpp<0xB1>(v));
+  v = op(v, bal_dpp<0x4E>(v));
+  v = op(v, bal_dpp<0x141>(v));
+  if constexpr (LPR >= 16) v = op(v, bal_dpp<0x140>(v));
+  if constexpr (LPR >= 32) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = op(__uint_as_float(r[0]), __uint_as_float(r[1]));
+  }
+  if constexpr (LPR >= 64) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = op(__uint_as_float(r[0]), __uint_as_float(r[1]));
+  }
   return v;
 }
+struct BalAdd {
+  __device__ float operator()(float a, float b) const { return a + b; }
+};
+struct BalMax {
+  __device__ float operator()(float a, float b) const { return __builtin_fmaxf(a, b); }
+};
 
-// Logits of row t in registers (lane + 64 j), and whether the row counts.  m is
-// the largest logit; a NaN does not enter it, and reaches the sums by itself.
-template <bool BF16, int PER>
-__device__ __forceinline__ bool bal_row(const BalParams& p, int64_t t, float (&l)[PER], float& m) {
-  if (p.mask && !p.mask[t]) return false;
-  const int lane = threadIdx.x & 63;
-  m = -__builtin_inff();
-  bool real = false;
-#pragma unroll
-  for (int j = 0; j < PER; ++j) {
-    const int e = lane + 64 * j;
-    l[j] = e < p.E ? bal_load<BF16>(p.logits, t * p.ld + e) : -__builtin_inff();
-    real |= !(l[j] == -__builtin_inff());
-    m = __builtin_fmaxf(m, l[j]);
-  }
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) m = __builtin_fmaxf(m, __shfl_xor(m, o, 64));
-  return __ballot(real) != 0;
-}
+// One row group's share of a lane: V logits of PER pieces, piece j of the row at
+// expert (j LPR + lane) V.  V > 1: rows start on 16 bytes and a piece is 16
+// bytes; the piece that holds the last expert is read whole (its other bytes lie
+// in the same 16) and what is behind E is taken out.
+template <bool BF16, int V, int LPR, int PER>
+struct BalRow {
+  static constexpr int RPW = 64 / LPR;  // rows of a wave
+  uint4 raw[V > 1 ? PER : 1];
+  float one[V > 1 ? 1 : PER];
+  int32_t id;  // the lane's first slot
+  bool on;     // the row is there and the mask takes it
 
-// p = e^(l - m) / sum in place, the log-sum returned.  l - m before the factor
-// log2 e: a mask of the type's lowest value stays the number that it is.
-template <int PER>
-__device__ __forceinline__ float bal_softmax(float (&l)[PER], float m) {
-  float s = 0.0f;
+  __device__ __forceinline__ void load(const BalParams& p, int64_t t, int lir, bool want_ids) {
+    on = t < p.T && (!p.mask || p.mask[t]);
+    const int64_t at = on ? t * p.ld : 0;
+    id = on && want_ids && lir < p.k ? p.ids[t * p.k + lir] : -1;
 #pragma unroll
-  for (int j = 0; j < PER; ++j) {
-    l[j] = __builtin_amdgcn_exp2f((l[j] - m) * kLog2E);
-    s += l[j];
-  }
-  s = wave_sum(s);
-  const float r = 1.0f / s;
-#pragma unroll
-  for (int j = 0; j < PER; ++j) l[j] *= r;
-  return m + __builtin_amdgcn_logf(s) * kLn2;
-}
-
-template <bool BF16, int PER>
-__global__ __launch_bounds__(64 * kFwdWaves) void k_balance(BalParams p) {
-  __shared__ int32_t hist[kMaxE];
-  __shared__ float sp[kFwdWaves][kMaxE];
-  __shared__ float sz[kFwdWaves];
-  __shared__ int32_t sn[kFwdWaves];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  for (int e = tid; e < p.E; e += 64 * kFwdWaves) hist[e] = 0;
-  __syncthreads();
-  float sum[PER], z = 0.0f;
-  int n = 0;
-#pragma unroll
-  for (int j = 0; j < PER; ++j) sum[j] = 0.0f;
-  for (int64_t t = (int64_t)blockIdx.x * kFwdWaves + wave; t < p.T;
-       t += (int64_t)gridDim.x * kFwdWaves) {
-    float l[PER], m;
-    if (!bal_row<BF16, PER>(p, t, l, m)) continue;
-    const float lse = bal_softmax<PER>(l, m);
-    z += lse * lse;
-    ++n;
-#pragma unroll
-    for (int j = 0; j < PER; ++j) sum[j] += l[j];
-    for (int64_t s = lane; s < p.k; s += 64) {
-      const uint32_t e = (uint32_t)p.ids[t * p.k + s];
-      if (e < (uint32_t)p.E) atomicAdd(&hist[e], 1);
+    for (int j = 0; j < PER; ++j) {
+      const int e = (j * LPR + lir) * V;
+      if constexpr (V > 1) {
+        constexpr int SIZE = BF16 ? 2 : 4;
+        raw[j] = make_uint4(0u, 0u, 0u, 0u);
+        if (on && e < p.E)
+          raw[j] = *reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(p.logits) + (at + e) * SIZE);
+      } else {
+        one[j] = 0.0f;
+        if (on && e < p.E) {
+          if constexpr (BF16)
+            one[j] = nv_bf16_to_f32(reinterpret_cast<const uint16_t*>(p.logits)[at + e]);
+          else
+            one[j] = reinterpret_cast<const float*>(p.logits)[at + e];
+        }
+      }
     }
   }
+
+  // The probabilities, the log-sum, and whether the row counts (uniform in the
+  // row's lanes).  The maximum passes over a NaN, which reaches the sums by itself.
+  // l - m comes before the factor log2 e: a mask of the type's lowest value stays
+  // the number that it is.
+  __device__ __forceinline__ bool softmax(const BalParams& p, int lir, float (&l)[PER * V], float& lse) {
+    float m = -__builtin_inff(), real = 0.0f;
 #pragma unroll
-  for (int j = 0; j < PER; ++j)
-    if (lane + 64 * j < p.E) sp[wave][lane + 64 * j] = sum[j];
+    for (int j = 0; j < PER; ++j) {
+      if constexpr (V == 4) {
+        const uint32_t w[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) l[j * V + i] = __uint_as_float(w[i]);
+      } else if constexpr (V == 8) {
+        const uint32_t w[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          l[j * V + 2 * i] = __uint_as_float(w[i] << 16);
+          l[j * V + 2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        }
+      } else {
+        l[j] = one[j];
+      }
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        float& v = l[j * V + i];
+        if ((j * LPR + lir) * V + i >= p.E) v = -__builtin_inff();
+        m = __builtin_fmaxf(m, v);
+        real = v == -__builtin_inff() ? real : 1.0f;
+      }
+    }
+    m = bal_reduce<LPR>(m, BalMax());
+    real = bal_reduce<LPR>(real, BalMax());
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < PER * V; ++i) {
+      l[i] = __builtin_amdgcn_exp2f((l[i] - m) * kLog2E);
+      s += l[i];
+    }
+    s = bal_reduce<LPR>(s, BalAdd());
+    const float r = 1.0f / s;
+#pragma unroll
+    for (int i = 0; i < PER * V; ++i) l[i] *= r;
+    lse = m + __builtin_amdgcn_logf(s) * kLn2;
+    return on && real != 0.0f;
+  }
+};
+
+// dot = sum over the experts of counts and mean probabilities; the outputs.
+__device__ __forceinline__ void bal_finish(const BalParams& p, double dot, double z, int64_t n) {
+  const double inv = n > 0 ? 1.0 / (double)n : 0.0;
+  p.tokens[0] = (int32_t)n;
+  p.losses[0] = (float)(dot * inv * (double)p.E / (double)p.k);
+  p.losses[1] = (float)(z * inv);
+}
+
+template <bool BF16, int V, int LPR, int PER, bool ONE>
+__global__ __launch_bounds__(64 * kFwdWaves) void k_balance(BalParams p) {
+  using Row = BalRow<BF16, V, LPR, PER>;
+  constexpr int COLS = LPR * PER * V, NT = 64 * kFwdWaves;
+  __shared__ int32_t hist[COLS];
+  __shared__ float sp[kFwdWaves][COLS];
+  __shared__ float sz[kFwdWaves];
+  __shared__ int32_t sn[kFwdWaves];
+  __shared__ double sd[kFwdWaves];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int lir = lane % LPR, slot = lane / LPR;
+  for (int e = tid; e < COLS; e += NT) hist[e] = 0;
+  if (!ONE && blockIdx.x == 0 && tid == 0) *p.joined = 0u;
+  __syncthreads();
+  float sum[PER * V], z = 0.0f;
+  int n = 0;
+#pragma unroll
+  for (int i = 0; i < PER * V; ++i) sum[i] = 0.0f;
+  const int64_t stride = (int64_t)gridDim.x * kFwdWaves * Row::RPW;
+  int64_t t = ((int64_t)blockIdx.x * kFwdWaves + wave) * Row::RPW + slot;
+  Row cur, nxt;
+  cur.load(p, t, lir, true);
+  for (; t - slot < p.T; t += stride) {
+    nxt.load(p, t + stride, lir, true);
+    float l[PER * V], lse;
+    if (cur.softmax(p, lir, l, lse)) {
+#pragma unroll
+      for (int i = 0; i < PER * V; ++i) sum[i] += l[i];
+      if (lir == 0) {
+        z += lse * lse;
+        ++n;
+      }
+      if ((uint32_t)cur.id < (uint32_t)p.E) atomicAdd(&hist[cur.id], 1);
+      for (int64_t s = lir + LPR; s < p.k; s += LPR) {
+        const uint32_t e = (uint32_t)p.ids[t * p.k + s];
+        if (e < (uint32_t)p.E) atomicAdd(&hist[e], 1);
+      }
+    }
+    cur = nxt;
+  }
+  // the wave's row slots, then the waves
+#pragma unroll
+  for (int o = LPR; o < 64; o <<= 1) {
+#pragma unroll
+    for (int i = 0; i < PER * V; ++i) sum[i] += __shfl_xor(sum[i], o, 64);
+    z += __shfl_xor(z, o, 64);
+    n += __shfl_xor(n, o, 64);
+  }
+  if (slot == 0)
+#pragma unroll
+    for (int j = 0; j < PER; ++j)
+#pragma unroll
+      for (int i = 0; i < V; ++i) sp[wave][(j * LPR + lir) * V + i] = sum[j * V + i];
   if (lane == 0) {
     sz[wave] = z;
     sn[wave] = n;
   }
   __syncthreads();
   const int64_t b = blockIdx.x;
-  for (int e = tid; e < p.E; e += 64 * kFwdWaves) {
-    float s = sp[0][e];
-    for (int w = 1; w < kFwdWaves; ++w) s += sp[w][e];
-    p.part_p[b * p.E + e] = s;
-    p.part_c[b * p.E + e] = hist[e];
-  }
-  if (tid == 0) {
-    float s = sz[0];
-    int c = sn[0];
-    for (int w = 1; w < kFwdWaves; ++w) {
-      s += sz[w];
-      c += sn[w];
+  if constexpr (ONE) {
+    int64_t all = 0;
+    for (int w = 0; w < kFwdWaves; ++w) all += sn[w];
+    const double inv = all > 0 ? 1.0 / (double)all : 0.0;
+    double dot = 0.0;
+    for (int e = tid; e < p.E; e += NT) {
+      double s = 0.0;
+      for (int w = 0; w < kFwdWaves; ++w) s += sp[w][e];
+      p.counts[e] = hist[e];
+      if (p.mean) p.mean[e] = (float)(s * inv);
+      dot += (double)hist[e] * (s * inv);
     }
-    p.part_z[b] = s;
-    p.part_n[b] = c;
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) dot += __shfl_xor(dot, o, 64);
+    if (lane == 0) sd[wave] = dot;
+    __syncthreads();
+    if (tid == 0) {
+      double d = 0.0, zz = 0.0;
+      for (int w = 0; w < kFwdWaves; ++w) {
+        d += sd[w];
+        zz += sz[w];
+      }
+      bal_finish(p, d, zz, all);
+    }
+  } else {
+    for (int e = tid; e < p.E; e += NT) {
+      float s = sp[0][e];
+      for (int w = 1; w < kFwdWaves; ++w) s += sp[w][e];
+      p.part_p[b * p.E + e] = s;
+      p.part_c[b * p.E + e] = hist[e];
+    }
+    if (tid == 0) {
+      float s = sz[0];
+      int c = sn[0];
+      for (int w = 1; w < kFwdWaves; ++w) {
+        s += sz[w];
+        c += sn[w];
+      }
+      p.part_z[b] = s;
+      p.part_n[b] = c;
+    }
   }
 }
 
-// One workgroup adds the partial sums, in their order, in 64 bits.
-__global__ __launch_bounds__(kMaxE) void k_balance_join(BalParams p, int nblk) {
-  __shared__ double red[kMaxE / 64];
-  const int e = threadIdx.x, lane = e & 63, w = e >> 6;
+// Adds the partial sums of 32 experts in 64 bits, always in the same order.  The
+// workgroup that comes last adds up the loss, from all workgroups' shares in
+// their order.  The counter was cleared by the launch before.
+__global__ __launch_bounds__(kJoinCols* kJoinParts) void k_balance_join(BalParams p, int nblk) {
+  __shared__ double rs[kJoinParts][kJoinCols];
+  __shared__ int32_t rc[kJoinParts][kJoinCols];
+  __shared__ double wz[16];
+  __shared__ int64_t wn[16];
+  const int tid = threadIdx.x, col = tid % kJoinCols, part = tid / kJoinCols;
+  const int e = blockIdx.x * kJoinCols + col;
   double z = 0.0;
   int64_t n = 0;
-  for (int b = 0; b < nblk; ++b) {
-    z += p.part_z[b];
-    n += p.part_n[b];
+  if (tid < nblk) {  // nblk <= 256: four waves
+    z = p.part_z[tid];
+    n = p.part_n[tid];
   }
-  const double inv = n > 0 ? 1.0 / (double)n : 0.0;
-  double dot = 0.0;
+  double s = 0.0;
+  int c = 0;
   if (e < p.E) {
-    double s = 0.0;
-    int c = 0;
-    for (int b = 0; b < nblk; ++b) {
-      s += p.part_p[(int64_t)b * p.E + e];
-      c += p.part_c[(int64_t)b * p.E + e];
-    }
-    p.counts[e] = c;
-    if (p.mean) p.mean[e] = (float)(s * inv);
-    dot = (double)c * (s * inv);
-  }
 #pragma unroll
-  for (int o = 32; o > 0; o >>= 1) dot += __shfl_xor(dot, o, 64);
-  if (lane == 0) red[w] = dot;
-  __syncthreads();
-  if (e == 0) {
-    double d = 0.0;
-    for (int i = 0; i < kMaxE / 64; ++i) d += red[i];
-    p.tokens[0] = (int32_t)n;
-    p.losses[0] = (float)(d * inv * (double)p.E / (double)p.k);
-    p.losses[1] = (float)(z * inv);
-  }
-}
-
-template <bool BF16, int PER>
-__global__ __launch_bounds__(256) void k_balance_bwd(BalParams p) {
-  const int lane = threadIdx.x & 63;
-  float c[PER];
-  int total = 0;
-#pragma unroll
-  for (int j = 0; j < PER; ++j) {
-    const int e = lane + 64 * j;
-    total += e < p.E ? p.counts[e] : 0;
-  }
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) total += __shfl_xor(total, o, 64);
-  const double mean = (double)total / (double)p.E;
-#pragma unroll
-  for (int j = 0; j < PER; ++j) {
-    const int e = lane + 64 * j;
-    c[j] = e < p.E ? (float)((double)p.counts[e] - mean) : 0.0f;
-  }
-  const double n = (double)p.tokens[0], inv = n > 0.0 ? 1.0 / n : 0.0;
-  const float a = (float)((double)p.grad_losses[0] * (double)p.E / (double)p.k * inv * inv);
-  const float b = (float)((double)p.grad_losses[1] * 2.0 * inv);
-  for (int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); t < p.T;
-       t += (int64_t)gridDim.x * 4) {
-    float l[PER], m;
-    if (bal_row<BF16, PER>(p, t, l, m)) {
-      const float lse = bal_softmax<PER>(l, m);
-      float cp = 0.0f;
-#pragma unroll
-      for (int j = 0; j < PER; ++j) cp += c[j] * l[j];
-      cp = wave_sum(cp);
-#pragma unroll
-      for (int j = 0; j < PER; ++j) l[j] *= a * (c[j] - cp) + b * lse;
-    } else {
-#pragma unroll
-      for (int j = 0; j < PER; ++j) l[j] = 0.0f;
-    }
-#pragma unroll
-    for (int j = 0; j < PER; ++j) {
-      const int e = lane + 64 * j;
-      if (e < p.E) {
-        if constexpr (BF16)
-          reinterpret_cast<uint16_t*>(p.grad)[t * p.ldg + e] =
-              __builtin_bit_cast(uint16_t, (__bf16)l[j]);
-        else
-          reinterpret_cast<float*>(p.grad)[t * p.ldg + e] = l[j];
+    for (int i = 0; i < kFwdBlocks / kJoinParts; ++i) {
+      const int b = i * kJoinParts + part;
+      if (b < nblk) {
+        s += p.part_p[(int64_t)b * p.E + e];
+        c += p.part_c[(int64_t)b * p.E + e];
       }
     }
   }
+  rs[part][col] = s;
+  rc[part][col] = c;
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) {
+    z += __shfl_xor(z, o, 64);
+    n += __shfl_xor(n, o, 64);
+  }
+  if ((tid & 63) == 0) {
+    wz[tid >> 6] = z;
+    wn[tid >> 6] = n;
+  }
+  __syncthreads();
+  if (tid >= 64) return;
+  n = wn[0] + wn[1] + wn[2] + wn[3];
+  const double inv = n > 0 ? 1.0 / (double)n : 0.0;
+  double dot = 0.0;
+  if (part == 0) {
+    s = 0.0;
+    c = 0;
+    for (int i = 0; i < kJoinParts; ++i) {
+      s += rs[i][col];
+      c += rc[i][col];
+    }
+    if (e < p.E) {
+      p.counts[e] = c;
+      if (p.mean) p.mean[e] = (float)(s * inv);
+      dot = (double)c * (s * inv);
+    }
+  }
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) dot += __shfl_xor(dot, o, 64);
+  if (tid != 0) return;
+  __hip_atomic_store(&p.dots[blockIdx.x], dot, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  const uint32_t before =
+      __hip_atomic_fetch_add(p.joined, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
+  if (before + 1 != gridDim.x) return;
+  dot = 0.0;
+  for (uint32_t i = 0; i < gridDim.x; ++i)
+    dot += __hip_atomic_load(&p.dots[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  bal_finish(p, dot, wz[0] + wz[1] + wz[2] + wz[3], n);
 }
 
-int fwd_blocks(int64_t T) {
-  const int64_t n = (T + kFwdWaves - 1) / kFwdWaves;
-  return (int)(n < 1 ? 1 : n < kFwdBlocks ? n : kFwdBlocks);
+// VOUT: gradient rows start on 16 bytes too, and are written in 16-byte pieces
+// but for one that is not whole.
+template <bool BF16, int V, int LPR, int PER, bool VOUT>
+__global__ __launch_bounds__(256) void k_balance_bwd(BalParams p) {
+  using Row = BalRow<BF16, V, LPR, PER>;
+  constexpr int SIZE = BF16 ? 2 : 4;
+  const int lane = threadIdx.x & 63, lir = lane % LPR, slot = lane / LPR;
+  const int64_t stride = (int64_t)gridDim.x * 4 * Row::RPW;
+  int64_t t = ((int64_t)blockIdx.x * 4 + (threadIdx.x >> 6)) * Row::RPW + slot;
+  Row cur, nxt;
+  cur.load(p, t, lir, false);
+  float c[PER * V];
+  int total = 0;
+#pragma unroll
+  for (int j = 0; j < PER; ++j)
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int e = (j * LPR + lir) * V + i;
+      const int n = e < p.E ? p.counts[e] : 0;
+      c[j * V + i] = __int_as_float(n);
+      total += n;
+    }
+#pragma unroll
+  for (int o = LPR / 2; o > 0; o >>= 1) total += __shfl_xor(total, o, 64);
+  const double mean = (double)total / (double)p.E;
+#pragma unroll
+  for (int i = 0; i < PER * V; ++i) c[i] = (float)((double)__float_as_int(c[i]) - mean);
+  const double n = (double)p.tokens[0], inv = n > 0.0 ? 1.0 / n : 0.0;
+  const float a = (float)((double)p.grad_losses[0] * (double)p.E / (double)p.k * inv * inv);
+  const float b = (float)((double)p.grad_losses[1] * 2.0 * inv);
+  for (; t - slot < p.T; t += stride) {
+    nxt.load(p, t + stride, lir, false);
+    float l[PER * V], lse;
+    const bool live = cur.softmax(p, lir, l, lse);
+    float cp = 0.0f;
+#pragma unroll
+    for (int i = 0; i < PER * V; ++i) cp += c[i] * l[i];
+    cp = bal_reduce<LPR>(cp, BalAdd());
+#pragma unroll
+    for (int i = 0; i < PER * V; ++i) l[i] = live ? l[i] * (a * (c[i] - cp) + b * lse) : 0.0f;
+    if (t < p.T) {
+      char* out = reinterpret_cast<char*>(p.grad) + t * p.ldg * SIZE;
+#pragma unroll
+      for (int j = 0; j < PER; ++j) {
+        const int e = (j * LPR + lir) * V;
+        if (VOUT && e + V <= p.E) {
+          uint32_t w[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if constexpr (BF16)
+              w[i] = __builtin_bit_cast(uint16_t, (__bf16)l[(j * V + 2 * i) % (PER * V)]) |
+                     (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)l[(j * V + 2 * i + 1) % (PER * V)]) << 16;
+            else
+              w[i] = __float_as_uint(l[(j * V + i) % (PER * V)]);
+          }
+          *reinterpret_cast<uint4*>(out + e * SIZE) = make_uint4(w[0], w[1], w[2], w[3]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < V; ++i)
+            if (e + i < p.E) {
+              if constexpr (BF16)
+                reinterpret_cast<uint16_t*>(out)[e + i] = __builtin_bit_cast(uint16_t, (__bf16)l[j * V + i]);
+              else
+                reinterpret_cast<float*>(out)[e + i] = l[j * V + i];
+            }
+        }
+      }
+    }
+    cur = nxt;
+  }
 }
 
-template <bool BF16>
-int launch_fwd(const BalParams& p, hipStream_t s) {
-  const int nblk = fwd_blocks(p.T);
-  const dim3 grid((unsigned)nblk), block(64 * kFwdWaves);
-  if (p.E <= 64) hipLaunchKernelGGL((k_balance<BF16, 1>), grid, block, 0, s, p);
-  else if (p.E <= 128) hipLaunchKernelGGL((k_balance<BF16, 2>), grid, block, 0, s, p);
-  else if (p.E <= 256) hipLaunchKernelGGL((k_balance<BF16, 4>), grid, block, 0, s, p);
-  else if (p.E <= 512) hipLaunchKernelGGL((k_balance<BF16, 8>), grid, block, 0, s, p);
-  else hipLaunchKernelGGL((k_balance<BF16, 16>), grid, block, 0, s, p);
-  hipLaunchKernelGGL(k_balance_join, dim3(1), dim3(kMaxE), 0, s, p, nblk);
-  return nv_launch_status();
+int fwd_blocks(int64_t T, int rpw) {
+  if (T <= kOneBlock) return 1;
+  const int64_t n = (T + kFwdWaves * rpw - 1) / (kFwdWaves * rpw);
+  return (int)(n < kFwdBlocks ? n : kFwdBlocks);
 }
 
-template <bool BF16>
-int launch_bwd(const BalParams& p, hipStream_t s) {
-  const int64_t n = (p.T + 3) / 4;
+template <bool BF16, int V, int LPR, int PER>
+int launch(const BalParams& p, bool backward, bool vout, hipStream_t s) {
+  if (!backward) {
+    const int nblk = fwd_blocks(p.T, 64 / LPR);
+    const dim3 grid((unsigned)nblk), block(64 * kFwdWaves);
+    if (p.T <= kOneBlock) {
+      hipLaunchKernelGGL((k_balance<BF16, V, LPR, PER, true>), grid, block, 0, s, p);
+      return nv_launch_status();
+    }
+    hipLaunchKernelGGL((k_balance<BF16, V, LPR, PER, false>), grid, block, 0, s, p);
+    hipLaunchKernelGGL(k_balance_join, dim3((unsigned)((p.E + kJoinCols - 1) / kJoinCols)),
+                       dim3(kJoinCols * kJoinParts), 0, s, p, nblk);
+    return nv_launch_status();
+  }
+  const int64_t n = (p.T * LPR + 255) / 256;
   const dim3 grid((unsigned)(n < 2048 ? n : 2048)), block(256);
-  if (p.E <= 64) hipLaunchKernelGGL((k_balance_bwd<BF16, 1>), grid, block, 0, s, p);
-  else if (p.E <= 128) hipLaunchKernelGGL((k_balance_bwd<BF16, 2>), grid, block, 0, s, p);
-  else if (p.E <= 256) hipLaunchKernelGGL((k_balance_bwd<BF16, 4>), grid, block, 0, s, p);
-  else if (p.E <= 512) hipLaunchKernelGGL((k_balance_bwd<BF16, 8>), grid, block, 0, s, p);
-  else hipLaunchKernelGGL((k_balance_bwd<BF16, 16>), grid, block, 0, s, p);
+  if (vout)
+    hipLaunchKernelGGL((k_balance_bwd<BF16, V, LPR, PER, V != 1>), grid, block, 0, s, p);
+  else
+    hipLaunchKernelGGL((k_balance_bwd<BF16, V, LPR, PER, false>), grid, block, 0, s, p);
   return nv_launch_status();
+}
+
+// 16-byte pieces where the rows of logits start on 16 bytes, else single logits.
+template <bool BF16>
+int launch_by_experts(const BalParams& p, bool backward, hipStream_t s) {
+  constexpr int SIZE = BF16 ? 2 : 4, V = 16 / SIZE;
+  auto whole = [](const void* x, int64_t ld) { return nv_aligned16(x) && ld * SIZE % 16 == 0; };
+  const bool vin = whole(p.logits, p.ld), vout = backward && whole(p.grad, p.ldg);
+  if (!vin) {
+    if (p.E <= 16) return launch<BF16, 1, 16, 1>(p, backward, false, s);
+    if (p.E <= 64) return launch<BF16, 1, 64, 1>(p, backward, false, s);
+    if (p.E <= 128) return launch<BF16, 1, 64, 2>(p, backward, false, s);
+    if (p.E <= 256) return launch<BF16, 1, 64, 4>(p, backward, false, s);
+    if (p.E <= 512) return launch<BF16, 1, 64, 8>(p, backward, false, s);
+    return launch<BF16, 1, 64, 16>(p, backward, false, s);
+  }
+  if (p.E <= 8 * V) return launch<BF16, V, 8, 1>(p, backward, vout, s);
+  if (p.E <= 16 * V) return launch<BF16, V, 16, 1>(p, backward, vout, s);
+  if (p.E <= 32 * V) return launch<BF16, V, 32, 1>(p, backward, vout, s);
+  if (p.E <= 64 * V) return launch<BF16, V, 64, 1>(p, backward, vout, s);
+  if constexpr (!BF16)
+    if (p.E > 128 * V) return launch<BF16, V, 64, 4>(p, backward, vout, s);
+  return launch<BF16, V, 64, 2>(p, backward, vout, s);
 }
 
 bool misaligned(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) != 0; }
@@ -272,7 +480,8 @@ extern "C" {
 
 size_t moe_balance_loss_workspace_size(int64_t T, int64_t E) {
   if (T < 0 || E < 1 || E > kMaxE) return 0;
-  return nv_round256(8 * (size_t)fwd_blocks(T) * (size_t)(E + 1));
+  // the loss's shares and the counter, then the partial sums
+  return nv_round256(512 + (T <= kOneBlock ? 0 : 8 * (size_t)fwd_blocks(T, 1) * (size_t)(E + 1)));
 }
 
 int moe_balance_loss(const void* logits, int dtype, int64_t T, int64_t E, int64_t ld,
@@ -286,9 +495,9 @@ int moe_balance_loss(const void* logits, int dtype, int64_t T, int64_t E, int64_
                    misaligned(counts, 4) || misaligned(tokens, 4) || misaligned(mean_probs, 4) ||
                    misaligned(losses, 4),
                NVFP4_ERR_ALIGN);
-  NV_RETURN_IF(!ws || ws_bytes < moe_balance_loss_workspace_size(T, E) || misaligned(ws, 4),
+  NV_RETURN_IF(!ws || ws_bytes < moe_balance_loss_workspace_size(T, E) || misaligned(ws, 8),
                NVFP4_ERR_WORKSPACE);
-  const int64_t nblk = fwd_blocks(T);
+  const int64_t nblk = fwd_blocks(T, 1);
   BalParams p{};
   p.logits = logits;
   p.T = T;
@@ -301,12 +510,15 @@ int moe_balance_loss(const void* logits, int dtype, int64_t T, int64_t E, int64_
   p.tokens = tokens;
   p.mean = mean_probs;
   p.losses = losses;
-  p.part_p = reinterpret_cast<float*>(ws);
+  p.dots = reinterpret_cast<double*>(ws);
+  p.joined = reinterpret_cast<uint32_t*>(p.dots + kMaxE / kJoinCols);
+  p.part_p = reinterpret_cast<float*>(p.dots + 64);
   p.part_z = p.part_p + nblk * E;
   p.part_c = reinterpret_cast<int32_t*>(p.part_z + nblk);
   p.part_n = p.part_c + nblk * E;
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-  return dtype == NVFP4_IN_BF16 ? launch_fwd<true>(p, s) : launch_fwd<false>(p, s);
+  return dtype == NVFP4_IN_BF16 ? launch_by_experts<true>(p, false, s)
+                                : launch_by_experts<false>(p, false, s);
 }
 
 int moe_balance_loss_backward(const void* logits, int dtype, int64_t T, int64_t E, int64_t ld,
@@ -335,7 +547,8 @@ int moe_balance_loss_backward(const void* logits, int dtype, int64_t T, int64_t 
   p.grad = grad_logits;
   p.ldg = ldg;
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-  return dtype == NVFP4_IN_BF16 ? launch_bwd<true>(p, s) : launch_bwd<false>(p, s);
+  return dtype == NVFP4_IN_BF16 ? launch_by_experts<true>(p, true, s)
+                                : launch_by_experts<false>(p, true, s);
 }
 
 }  // extern "C"

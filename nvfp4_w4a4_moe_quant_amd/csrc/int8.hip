@@ -345,33 +345,27 @@ struct I8Tile {
   static constexpr int NPI = ROWS * 8 / NT;  // 16-byte pieces per thread per chunk
   static constexpr int NPA = BM * 8 / NT;    // of them in A rows, which come first
   static constexpr int STAGE = ROWS * KC;
-#ifndef I8DS
-#define I8DS 2
-#endif
-  static constexpr int DS = NPI % I8DS ? 1 : I8DS;
-  static_assert(BM * 8 % NT == 0 && BN * 8 % NT == 0, "whole wave-loads");
+  static constexpr int DS = NPI % 2 ? 1 : 2;  // steps over which a chunk's pieces are issued
+  static_assert(NW % 2 == 0 && BM * 8 % NT == 0 && BN * 8 % NT == 0, "whole wave-loads");
   static_assert(!SILU || FN % 2 == 0, "SiLU pairs gate and up fragments");
   static_assert(NS >= 2 && (NS - 1) * NPI <= 63, "vmcnt range");
 
   const I8Params& p;
   uint8_t* lds;
   const uint8_t *abase, *wbase, *ubase;  // the tile's first row of A, of W, of W's up half
+  uint32_t at;        // a piece's place in its chunk: the same for all pieces of a lane
   uint32_t off[NPI];  // bytes from there to piece j; in a gather 16-byte units from A's start
   int lane, wave, wm, wn, lr, lh, nt, beg, end, cols, nfull, rem;
 
-  // Piece j of a chunk into buffer `buf`.  The chunk behind the last whole one
-  // (TAIL) holds `rem` bytes a row; its pieces behind them read the chunk's first
-  // piece, and the products skip them.
-  template <bool TAIL>
-  __device__ __forceinline__ void issue1(int j, int chunk, int buf) {
+  // The chunk behind the last whole one holds `rem` bytes a row; its pieces behind
+  // them step back to the chunk's first piece, and the products skip them.
+  __device__ __forceinline__ uint32_t step_back(int chunk) const {
+    return chunk == nfull && at >= (uint32_t)rem ? at : 0u;
+  }
+  // Piece j of a chunk into buffer `buf`.
+  __device__ __forceinline__ void issue1(int j, int chunk, int buf, uint32_t back) {
     const uint32_t st = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)(lds + buf * STAGE);
     const uint32_t m0 = __builtin_amdgcn_readfirstlane(st + (j * NW + wave) * 1024);
-    uint32_t back = 0;
-    if (TAIL && chunk == nfull) {
-      const int slot = (j * NW + wave) * 64 + lane, row = slot >> 3;
-      const uint32_t at = ((uint32_t)(slot & 7) ^ i8_swz((uint32_t)row)) * 16;
-      back = at >= (uint32_t)rem ? at : 0u;
-    }
     if (GATHER && j < NPA) {
       const uint8_t* g = abase + (int64_t)chunk * KC - back + (uint64_t)off[j] * 16u;
       asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
@@ -403,13 +397,13 @@ struct I8Tile {
 
   template <int NL>
   __device__ __forceinline__ void run(const float* sw) {
-    float sa[NL ? NL : 1];
+    float sa[NL];
 #pragma unroll
     for (int a = 0; a < NL; ++a) {
       const int m = min(beg + (a * WM + wm) * 32 + lr, end - 1);
       sa[a] = p.a_scales[GATHER ? (int64_t)p.gather[m] : (int64_t)m];
     }
-    int16v acc[NL ? NL : 1][FN];
+    int16v acc[NL][FN];
 #pragma unroll
     for (int a = 0; a < NL; ++a)
 #pragma unroll
@@ -420,7 +414,7 @@ struct I8Tile {
     const uint32_t x = (lh ^ i8_swz((uint32_t)lr)) << 4;
     const uint8_t* al = lds + (wm * 32 + lr) * KC;
     const uint8_t* wl = lds + (BM + wn * FN * 32 + lr) * KC;
-    int4v af[2][NL ? NL : 1], wf[2][FN];
+    int4v af[2][NL], wf[2][FN];
     // fragment i of step s: the W ones first
     auto load = [&](int i, int buf, int s, int4v* av, int4v* wv) {
       const uint32_t o = buf * STAGE + (x ^ (s << 5));
@@ -429,7 +423,7 @@ struct I8Tile {
       else
         av[i - FN] = *reinterpret_cast<const int4v*>(al + o + (i - FN) * WM * 32 * KC);
     };
-    constexpr int NR = NL ? NL + FN : 0, NM = NL * FN;
+    constexpr int NR = NL + FN, NM = NL * FN;
     // A buffer is free from a chunk's last step on; the pieces of the chunk that
     // takes it are issued over that step and the first DS - 1 of the next chunk.
     constexpr int PART = NPI / DS;
@@ -438,7 +432,7 @@ struct I8Tile {
       if (c < total) {
 #pragma unroll
         for (int j = 0; j < NPI; ++j)
-          if (c < NS - 1 || j < PART) issue1<true>(j, c, c);
+          if (c < NS - 1 || j < PART) issue1(j, c, c, step_back(c));
       }
     if (total >= NS)
       asm volatile("s_waitcnt vmcnt(%0)" ::"n"((NS - 2) * NPI + PART) : "memory");
@@ -467,22 +461,20 @@ struct I8Tile {
         const int nx = s == 3 ? ch + NS : ch + NS - 1, to = s == 3 ? buf : pb;
         const int j0 = s == 3 ? 0 : (s + 1) * PART;
         const bool more = tail && (STEADY || nx < total);
+        const uint32_t back = STEADY ? 0u : step_back(nx);
         const int cur = s & 1;
-        constexpr int steps = NM ? NM : 1;
 #pragma unroll
-        for (int i = 0; i < steps; ++i) {
+        for (int i = 0; i < NM; ++i) {
 #pragma unroll
           for (int j = i * 2; j < NR && j < i * 2 + 2; ++j)
             load(j, s == 3 ? nb : buf, (s + 1) & 3, af[cur ^ 1], wf[cur ^ 1]);
           if (more) {
 #pragma unroll
-            for (int j = i * PART / steps; j < (i + 1) * PART / steps; ++j)
-              issue1<!STEADY>(j0 + j, nx, to);
+            for (int j = i * PART / NM; j < (i + 1) * PART / NM; ++j)
+              issue1(j0 + j, nx, to, back);
           }
-          if constexpr (NM > 0) {
-            const int a = i / FN, b = i % FN;
-            acc[a][b] = __builtin_amdgcn_mfma_i32_32x32x32_i8(wf[cur][b], af[cur][a], acc[a][b], 0, 0, 0);
-          }
+          const int a = i / FN, b = i % FN;
+          acc[a][b] = __builtin_amdgcn_mfma_i32_32x32x32_i8(wf[cur][b], af[cur][a], acc[a][b], 0, 0, 0);
           __builtin_amdgcn_sched_barrier(0);
         }
       }
@@ -507,7 +499,64 @@ struct I8Tile {
       }
     }
     barrier();
-    if constexpr (NL > 0) store<NL>(acc, sa, sw);
+    store<NL>(acc, sa, sw);
+  }
+
+  // The same products in little code, for tiles of one fragment row a wave
+  // (FM == 1): calls of their size are over before a long loop's code is fetched.
+  // Waves without rows compute on repeated rows and store nothing; the chunk
+  // behind the last whole one is masked like every other.
+  __device__ __forceinline__ void run_small(const float* sw) {
+    const int m = min(beg + wm * 32 + lr, end - 1);
+    const float sa = p.a_scales[GATHER ? (int64_t)p.gather[m] : (int64_t)m];
+    int16v acc[1][FN];
+#pragma unroll
+    for (int b = 0; b < FN; ++b)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[0][b][e] = 0;
+    const int total = nfull + (rem ? 1 : 0);
+#pragma unroll 1
+    for (int c = 0; c < NS && c < total; ++c) {
+      const uint32_t back = step_back(c);
+#pragma unroll
+      for (int j = 0; j < NPI; ++j) issue1(j, c, c, back);
+    }
+    const uint32_t x = (lh ^ i8_swz((uint32_t)lr)) << 4;
+    const uint8_t* al = lds + (wm * 32 + lr) * KC;
+    const uint8_t* wl = lds + (BM + wn * FN * 32 + lr) * KC;
+    int buf = 0;
+#pragma unroll 1
+    for (int ch = 0; ch < total; ++ch) {
+      // this wave's pieces of chunk ch have landed, and every wave's behind the barrier
+      if (ch + NS <= total)
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"((NS - 1) * NPI) : "memory");
+      else
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      barrier();
+      int4v af[4], wf[4][FN];
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        const uint32_t o = buf * STAGE + (x ^ (s << 5));
+        af[s] = *reinterpret_cast<const int4v*>(al + o);
+#pragma unroll
+        for (int b = 0; b < FN; ++b) wf[s][b] = *reinterpret_cast<const int4v*>(wl + o + b * 32 * KC);
+      }
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        if (ch * KC + s * 32 + lh * 16 >= p.K) af[s] = int4v{0, 0, 0, 0};
+#pragma unroll
+        for (int b = 0; b < FN; ++b)
+          acc[0][b] = __builtin_amdgcn_mfma_i32_32x32x32_i8(wf[s][b], af[s], acc[0][b], 0, 0, 0);
+      }
+      barrier();  // every wave holds its fragments
+      if (ch + NS < total) {
+        const uint32_t back = step_back(ch + NS);
+#pragma unroll
+        for (int j = 0; j < NPI; ++j) issue1(j, ch + NS, buf, back);
+      }
+      buf = buf + 1 == NS ? 0 : buf + 1;
+    }
+    if (beg + wm * 32 < end) store<1>(acc, &sa, sw);
   }
 
   // Element e of fragment (a, b): tile row (a WM + wm) 32 + lr, tile column
@@ -613,10 +662,12 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_i8_gemm(I8Params p, int n_t
   k.abase = reinterpret_cast<const uint8_t*>(p.a_codes) + (GATHER ? 0 : (int64_t)k.beg * p.K);
   k.wbase = reinterpret_cast<const uint8_t*>(p.w_codes) + (wrow + n0) * p.K;
   k.ubase = k.wbase + (int64_t)k.cols * p.K;
+  // rows 8 NW j apart share their swizzle (NW is even)
+  k.at = ((uint32_t)(k.lane & 7) ^ i8_swz((uint32_t)(k.wave * 8 + (k.lane >> 3)))) * 16;
 #pragma unroll
   for (int j = 0; j < Tile::NPI; ++j) {
-    const int slot = (j * Tile::NW + k.wave) * 64 + k.lane, row = slot >> 3;
-    const uint32_t at = ((uint32_t)(slot & 7) ^ i8_swz((uint32_t)row)) * 16;
+    const int row = (j * Tile::NW + k.wave) * 8 + (k.lane >> 3);
+    const uint32_t at = k.at;
     if (j < Tile::NPA) {
       const int r = min(row, k.end - 1 - k.beg);
       if constexpr (GATHER)
@@ -627,16 +678,19 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_i8_gemm(I8Params p, int n_t
       k.off[j] = (uint32_t)(column(row - BM) - n0) * (uint32_t)p.K + at;
     }
   }
-  // fragments of 32 rows that hold rows: frag a of wave row wm starts at row
-  // (a WM + wm) 32
-  const int frags = (min(k.end - k.beg, BM) + 31) >> 5;
-  const int nl = (frags - k.wm + WM - 1) / WM;
-  if (nl >= FM) k.template run<FM>(sw);
-  else if (FM > 4 && nl == 4) k.template run<(FM > 4 ? 4 : 0)>(sw);
-  else if (FM > 3 && nl == 3) k.template run<(FM > 3 ? 3 : 0)>(sw);
-  else if (FM > 2 && nl == 2) k.template run<(FM > 2 ? 2 : 0)>(sw);
-  else if (FM > 1 && nl == 1) k.template run<(FM > 1 ? 1 : 0)>(sw);
-  else k.template run<0>(sw);
+  if constexpr (FM == 1) {
+    k.run_small(sw);
+  } else {
+    // fragments of 32 rows that hold rows: frag a of wave row wm starts at row (a
+    // WM + wm) 32.  A wave without rows computes on repeated ones.
+    const int frags = (min(k.end - k.beg, BM) + 31) >> 5;
+    const int nl = (frags - k.wm + WM - 1) / WM;
+    if (nl >= FM) k.template run<FM>(sw);
+    else if (FM > 4 && nl == 4) k.template run<(FM > 4 ? 4 : 1)>(sw);
+    else if (FM > 3 && nl == 3) k.template run<(FM > 3 ? 3 : 1)>(sw);
+    else if (FM > 2 && nl == 2) k.template run<(FM > 2 ? 2 : 1)>(sw);
+    else k.template run<1>(sw);
+  }
 }
 
 template <int WM, int WN, int FM, int FN, int NS, int EPI>
@@ -674,27 +728,34 @@ struct I8Plan {
   int few;        // k_i8_few with so many waves to a block of columns, or 0
   int rt;         // its row tiles of 16 to a workgroup
   int64_t tiles;  // workgroups' row tiles at most
-  int tile;       // else: the tile shape
+  int tile;       // else: the tile shape of launch_gemm
 };
 
+// Times below are those of the product alone, from quantized rows, in a graph of
+// calls back to back.
 I8Plan plan_of(const int8_gemm_args_t* a) {
   I8Plan pl{};
-  const bool silu = a->epilogue == NVFP4_EPI_SILU_MUL_BF16;
-  const int64_t cols = silu ? a->N / 2 : a->N, rows = a->total_rows, G = a->num_groups;
-#ifndef I8FEW
-#define I8FEW 1024
-#endif
+  const int64_t rows = a->total_rows, G = a->num_groups;
+  const int64_t cols = a->epilogue == NVFP4_EPI_SILU_MUL_BF16 ? a->N / 2 : a->N;
+  // Few rows: the tile kernels have one workgroup for 128 columns of a row tile,
+  // which leaves CUs idle up to about 1024 units of 16 columns and rows (4096^2: 1
+  // row 4.7 us for 11.7, 64 rows 12.1 for 12.4, 128 rows 21 for 12.6; 128
+  // experts, K 2048, N 1536, one token's 8 rows 7.9 for 9.7, four tokens' 32 rows
+  // 21.6 for 18.0; K 768, N 2048: 4.9 for 6.6).  With the fewest waves to a block
+  // of columns that make 1536 in all (1 row of 4096^2: 8, 4, 2 waves 4.7, 6.8, 10.8 us;
+  // 8 rows of 128 experts, K 2048: 9.3, 7.8, 12.1; K 768: 6.8, 5.0, 4.9).
   pl.rt = G > 1 || rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
   pl.tiles = G == 1 ? (rows + 16 * pl.rt - 1) / (16 * pl.rt) : (rows < G ? rows : G) + rows / 16;
   const int64_t units = pl.tiles * ((cols + 15) / 16);
-  if (rows <= (G == 1 ? 256 : 16 * G) && units <= I8FEW)
-#ifdef I8KW
-    pl.few = I8KW;
-#else
+  if (rows <= (G == 1 ? 64 : 16 * G) && units <= 1024) {
     pl.few = units * 2 >= 1536 ? 2 : units * 4 >= 1536 ? 4 : 8;
-#endif
+    return pl;
+  }
   const double mean = (double)rows / (double)G;
   if (G == 1) {
+    // rounds over the chip times a tile's time beside the 256 x 256 tile's (N = K =
+    // 4096: 512 rows 20, 24, 41 us for tiles 0, 1, 2; 1024 rows 25, 26, 43; 2048
+    // rows 54, 36, 48; 4096 rows 98, 70, 60 and 64 for tile 3)
     auto rounds = [&](int64_t bm, int64_t bn) {
       return (double)((((rows + bm - 1) / bm) * ((a->N + bn - 1) / bn) + 255) / 256);
     };
@@ -703,41 +764,39 @@ I8Plan plan_of(const int8_gemm_args_t* a) {
     for (int i = 1; i < 4; ++i)
       if (c[i] < c[pl.tile]) pl.tile = i;
   } else if (mean <= 48) {
+    // 128 experts, N 1536, K 2048: 32 rows each 77 us (tile 1: 79), 64 rows 92
+    // (87); 256 experts, N 4096, K 7168: 64 rows 1522 (1316)
     pl.tile = 0;
   } else if (mean <= 112) {
-    pl.tile = 1;
+    pl.tile = 1;  // 128 rows each: tile 2 104.5 us, tile 1 114.5; 64 rows: 93 and 87
   } else {
+    // fewest tiles for rows that vary by twice the square root of their mean: a
+    // second tile reads all of W again (256 experts of 256 +- 16 rows, N 4096, K
+    // 7168: 2137 us on 320-row tiles, 2476 on 256-row ones)
     const double most = mean + 2 * __builtin_sqrt(mean);
     pl.tile = __builtin_ceil(most / 320) * 1.22 < __builtin_ceil(most / 256) ? 3 : 2;
   }
   return pl;
 }
 
+template <int EPI, int RT>
+int launch_few_of(const I8Params& p, const I8Plan& pl, hipStream_t s) {
+  if (pl.few == 2) return launch_few<EPI, 2, RT>(p, pl.tiles, s);
+  if (pl.few == 4) return launch_few<EPI, 4, RT>(p, pl.tiles, s);
+  return launch_few<EPI, 8, RT>(p, pl.tiles, s);
+}
+
 template <int EPI>
 int launch_gemm(const I8Params& p, const I8Plan& pl, hipStream_t s) {
   if (pl.few) {
-    if (pl.rt == 1) {
-      if (pl.few == 2) return launch_few<EPI, 2, 1>(p, pl.tiles, s);
-      if (pl.few == 4) return launch_few<EPI, 4, 1>(p, pl.tiles, s);
-      return launch_few<EPI, 8, 1>(p, pl.tiles, s);
-    }
-    if (pl.rt == 2) {
-      if (pl.few == 2) return launch_few<EPI, 2, 2>(p, pl.tiles, s);
-      if (pl.few == 4) return launch_few<EPI, 4, 2>(p, pl.tiles, s);
-      return launch_few<EPI, 8, 2>(p, pl.tiles, s);
-    }
-    if (pl.few == 2) return launch_few<EPI, 2, 4>(p, pl.tiles, s);
-    if (pl.few == 4) return launch_few<EPI, 4, 4>(p, pl.tiles, s);
-    return launch_few<EPI, 8, 4>(p, pl.tiles, s);
+    if (pl.rt == 1) return launch_few_of<EPI, 1>(p, pl, s);
+    if (pl.rt == 2) return launch_few_of<EPI, 2>(p, pl, s);
+    return launch_few_of<EPI, 4>(p, pl, s);
   }
-#ifdef I8CFG
-  return launch_tiles<I8CFG, EPI>(p, s);
-#else
-  if (pl.tile == 0) return launch_tiles<2, 2, 1, 2, 2, EPI>(p, s);
-  if (pl.tile == 1) return launch_tiles<2, 4, 2, 2, 3, EPI>(p, s);
-  if (pl.tile == 2) return launch_tiles<4, 2, 2, 4, 2, EPI>(p, s);
-  return launch_tiles<2, 4, 5, 2, 2, EPI>(p, s);
-#endif
+  if (pl.tile == 0) return launch_tiles<2, 2, 1, 2, 2, EPI>(p, s);  // 64 x 128, three to a CU
+  if (pl.tile == 1) return launch_tiles<2, 4, 2, 2, 3, EPI>(p, s);  // 128 x 256
+  if (pl.tile == 2) return launch_tiles<4, 2, 2, 4, 2, EPI>(p, s);  // 256 x 256
+  return launch_tiles<2, 4, 5, 2, 2, EPI>(p, s);                    // 320 x 256
 }
 
 template <bool BF16, int RW, int VPL>
@@ -781,7 +840,7 @@ int check_gemm(const int8_gemm_args_t* a) {
                    a->epilogue != NVFP4_EPI_BF16,
                NVFP4_ERR_DTYPE);
   NV_RETURN_IF(a->num_groups < 1 || a->num_groups > (1 << 20) || a->total_rows < 0 ||
-                   a->total_rows > 0x7fffffff || a->N < 1 || a->N > (1 << 24) || a->K < 16 ||
+                   a->total_rows > (1 << 30) || a->N < 1 || a->N > (1 << 24) || a->K < 16 ||
                    a->K % 16 || a->K > kMaxK ||
                    (a->epilogue == NVFP4_EPI_SILU_MUL_BF16 && a->N % 2),
                NVFP4_ERR_SHAPE);

@@ -141,7 +141,9 @@ GROUPS = [
     (3, [0], 32, 48), (4, [64, 0, 1, 200, 16], 384, 256), (5, [2] * 70, 96, 208),
     (6, [300, 12], 514, 1040), (7, [0] * 63 + [9] + [0] * 64 + [20], 64, 128),
     (8, [1000, 0, 600, 24], 768, 320), (9, [30] * 40, 256, 2048), (10, [0, 2, 1, 0, 4] * 60, 48, 96),
-    (11, [15, 16, 17, 31, 32, 33, 47, 48, 49], 320, 624), (12, [127, 128, 129, 255, 256, 257], 260, 176),
+    (13, [256, 240, 288, 250, 230], 300, 1104), (14, [1200, 0, 0, 0, 50], 514, 400),
+    (15, [100, 64, 0, 65, 128, 33], 270, 1104), (16, [200, 190, 129], 258, 1136),
+    (17, [321, 200, 33], 260, 272), (11, [15, 16, 17, 31, 32, 33, 47, 48, 49], 320, 624), (12, [127, 128, 129, 255, 256, 257], 260, 176),
 ]
 
 
@@ -290,6 +292,35 @@ def test_moe_block_together():
             e = P.int8_moe_block(sx.clone(), sl.clone(), wgu, wd, w.topk)["out"]
             torch.cuda.synchronize()
             assert torch.equal(o, e)
+
+
+def test_offsets_beyond_32_bits():
+    """Rows, codes and weights more than 4 GB into their tensors."""
+    say("int8 beyond 4 GB")
+    K, src = 65536, 70000
+    g = torch.Generator(device=DEV)
+    g.manual_seed(3)
+    codes = torch.randint(-127, 128, (src, K), generator=g, device=DEV, dtype=torch.int8)
+    sa = torch.rand(src, generator=g, device=DEV) + 0.5
+    w = torch.randint(-127, 128, (2, 96, K), generator=g, device=DEV, dtype=torch.int8)
+    sw = torch.rand(2, 96, generator=g, device=DEV) + 0.5
+    for rows in (9, 80, 140, 300):
+        gat = torch.randint(src - 200, src, (rows,), generator=g, device=DEV, dtype=torch.int32)
+        gat[::3] = torch.randint(0, src, gat[::3].shape, generator=g, device=DEV, dtype=torch.int32)
+        off = torch.tensor([0, rows // 2, rows], dtype=torch.int32, device=DEV)
+        y = L.int8_grouped_gemm(L.INT8(codes, sa), L.INT8(w, sw), off, N=96, K=K, total_rows=rows,
+                                gather_rows=gat)
+        idx = host(gat)
+        ref = R.product(host(codes[gat.long()]), host(sa)[idx], host(w), host(sw), host(off))
+        eq(host(y), ref, f"{rows} gathered rows")
+    x = torch.empty(40000, K, dtype=torch.bfloat16, device=DEV)
+    x[:-3] = 0
+    x[-3:] = torch.randn(3, K, generator=g, device=DEV)
+    q = L.int8_quantize_rows(x)
+    c, s = R.quantize(host(x[-3:].float()))
+    eq(host(q.codes[-3:]), c, "last rows' codes")
+    eq(host(q.scales[-3:]), s, "last rows' scales")
+    assert not q.codes[:-3].any()
 
 
 def test_deterministic():
