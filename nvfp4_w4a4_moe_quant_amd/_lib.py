@@ -703,21 +703,19 @@ def int8_grouped_gemm(a, w: INT8, group_offsets: Optional[torch.Tensor] = None, 
         _refuse("activations on a GPU")
     G = 1 if group_offsets is None else group_offsets.numel() - 1
     _int8(w, (G, N, K), dev, "w")
-    args = Int8GemmArgs(num_groups=G, N=N, K=K, total_rows=total_rows,
-                        w_codes=w.codes.data_ptr(), w_scales=w.scales.data_ptr(),
-                        src_rows=src_rows, epilogue=epilogue)
+    offs = gat = codes = scales = xp = None
+    xd = ldx = 0
     if group_offsets is not None:
-        args.group_offsets = _vector(group_offsets, G + 1, torch.int32, dev, "group_offsets")
+        offs = _vector(group_offsets, G + 1, torch.int32, dev, "group_offsets")
     if gather_rows is not None:
-        args.gather_rows = _vector(gather_rows, total_rows, torch.int32, dev, "gather_rows")
+        gat = _vector(gather_rows, total_rows, torch.int32, dev, "gather_rows")
     elif src_rows < total_rows:
         _refuse("activations of at least total_rows rows")
     if quantized:
         _int8(a, (src_rows, K), dev, "a")
-        args.a_codes, args.a_scales = a.codes.data_ptr(), a.scales.data_ptr()
+        codes, scales = x.data_ptr(), a.scales.data_ptr()
     else:
-        args.x, args.x_dtype = x.data_ptr(), _dtype_code(x)
-        args.ldx = _row_stride(x, "x")
+        xp, xd, ldx = x.data_ptr(), _dtype_code(x), _row_stride(x, "x")
     if validate:
         if group_offsets is None:
             group_offsets = torch.tensor([0, total_rows], dtype=torch.int32)
@@ -729,7 +727,8 @@ def int8_grouped_gemm(a, w: INT8, group_offsets: Optional[torch.Tensor] = None, 
     elif out.shape != (total_rows, cols) or out.dtype != odt or out.device != dev \
             or not out.is_contiguous():
         _refuse(f"out: contiguous {odt} {(total_rows, cols)} on {dev}")
-    args.out = out.data_ptr()
+    args = Int8GemmArgs(G, N, K, total_rows, offs, gat, codes, scales, xp, xd, ldx, src_rows,
+                        w.codes.data_ptr(), w.scales.data_ptr(), epilogue, out.data_ptr())
     L = lib()
     ref = ctypes.byref(args)
     n = L.int8_grouped_gemm_workspace_size(ref)

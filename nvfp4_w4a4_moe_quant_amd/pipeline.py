@@ -407,35 +407,41 @@ def int8_moe_block(x: torch.Tensor, logits: torch.Tensor, wgu: L.INT8, wd: L.INT
 
 # ------------------------------------------------- the router's balance loss
 class _BalanceLoss(torch.autograd.Function):
-    @staticmethod
-    def forward(ctx, logits, topk_ids, mask):
-        r = L.moe_balance_loss(logits, topk_ids, mask=mask)
-        ctx.save_for_backward(logits, mask, r.counts, r.tokens)
-        ctx.k = topk_ids.shape[1]
-        ctx.mark_non_differentiable(r.counts, r.mean_probs, r.tokens)
-        ctx.set_materialize_grads(False)
-        return tuple(r)
+    """The losses, already computed, as a function of the logits."""
 
     @staticmethod
-    def backward(ctx, g_losses, *_):
+    def forward(ctx, logits, k, losses, counts, tokens, mask):
+        ctx.save_for_backward(logits, counts, tokens, mask)
+        ctx.k = k
+        ctx.set_materialize_grads(False)
+        return losses.view(2)
+
+    @staticmethod
+    def backward(ctx, g_losses):
         if torch.is_grad_enabled():  # under create_graph
             raise RuntimeError("moe_balance_loss has no second derivative")
-        logits, mask, counts, tokens = ctx.saved_tensors
         if g_losses is None:
-            return None, None, None
+            return None, None, None, None, None, None
+        logits, counts, tokens, mask = ctx.saved_tensors
         return L.moe_balance_loss_backward(logits, ctx.k, counts, tokens, g_losses.contiguous(),
-                                           mask=mask), None, None
+                                           mask=mask), None, None, None, None, None
 
 
 def moe_balance_loss(logits: torch.Tensor, topk_ids: torch.Tensor,
                      mask: Optional[torch.Tensor] = None) -> L.BalanceOut:
     """The router's balance loss and z-loss (losses [2]) with the gradient of
     logits [T, E], and the counts and mean probabilities, which get none.
-    topk_ids [T, k] is moe_route's choice.  There is no second derivative.  Leaf
+    topk_ids [T, k] is moe_route's choice.  There is no second derivative, and a
+    backward pass fails if the counts were written to before it.  Leaf
     logits that require a gradient are refused under graph capture, where
     another living graph of the same leaf ends the process: capture the two
     library calls instead."""
-    if logits.requires_grad and logits.is_leaf and torch.cuda.is_current_stream_capturing():
+    if not (logits.requires_grad and torch.is_grad_enabled()):
+        return L.moe_balance_loss(logits, topk_ids, mask=mask)
+    if logits.is_leaf and torch.cuda.is_current_stream_capturing():
         raise RuntimeError("leaf logits under capture: use the library's moe_balance_loss and "
                            "moe_balance_loss_backward")
-    return L.BalanceOut(*_BalanceLoss.apply(logits, topk_ids, mask))
+    with torch.no_grad():
+        r = L.moe_balance_loss(logits, topk_ids, mask=mask)
+    losses = _BalanceLoss.apply(logits, topk_ids.shape[1], r.losses, r.counts, r.tokens, mask)
+    return r._replace(losses=losses)
