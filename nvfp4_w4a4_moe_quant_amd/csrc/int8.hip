@@ -167,17 +167,57 @@ __device__ __forceinline__ float i8_silu_mul(float g, float u) {
 }
 
 // Tile of a workgroup, in the order of nv_find_tile<8> (bands of eight m-tiles,
-// contiguous ranges of tiles per XCD).  Without offsets the one group's tiles
-// need no scan.
+// contiguous ranges of tiles per XCD), found with one scan: a lane counts the
+// tiles of consecutive groups.  Without offsets the one group needs none.
 __device__ __forceinline__ NvTile i8_find_tile(const I8Params& p, int bm, int n_tiles) {
-  if (p.offsets) return nv_find_tile<8>(p.offsets, p.G, bm, 0, n_tiles);
-  const int m_tiles = (p.total_rows + bm - 1) / bm, n = m_tiles * n_tiles;
-  const int bid = blockIdx.x, per = n / 8, rem = n % 8, xcd = bid % 8, li = bid / 8;
+  constexpr int KEEP = 4;  // groups of a lane kept in registers
+  const int lane = threadIdx.x & 63, per = (p.G + 63) >> 6;
+  int v[KEEP], sum = 0, inc = 0, m_tiles;
+  if (p.offsets) {
+    if (per <= KEEP) {
+      int o[KEEP + 1];
+#pragma unroll
+      for (int i = 0; i <= KEEP; ++i) o[i] = p.offsets[min(lane * per + min(i, per), p.G)];
+#pragma unroll
+      for (int i = 0; i < KEEP; ++i) sum += v[i] = (o[i + 1] - o[i] + bm - 1) / bm;
+    } else {
+      for (int i = 0; i < per; ++i) sum += nv_group_tiles(p.offsets, p.G, lane * per + i, bm);
+    }
+    inc = sum;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int n = __shfl_up(inc, o, 64);
+      if (lane >= o) inc += n;
+    }
+    m_tiles = __builtin_amdgcn_readlane(inc, 63);
+  } else {
+    m_tiles = (p.total_rows + bm - 1) / bm;
+  }
+  const int n = m_tiles * n_tiles;
+  const int bid = blockIdx.x, share = n / 8, rem = n % 8, xcd = bid % 8, li = bid / 8;
   NvTile t{-1, 0, 0};
-  if (li >= per + (xcd < rem ? 1 : 0)) return t;
-  const int L = xcd * per + (xcd < rem ? xcd : rem) + li;
-  const int band = L / (8 * n_tiles), gm = min(8, m_tiles - band * 8), j = L - band * 8 * n_tiles;
+  if (li >= share + (xcd < rem ? 1 : 0)) return t;
+  const int L = xcd * share + (xcd < rem ? xcd : rem) + li;
+  int first = 0, tiles = m_tiles;  // of the tile's group
   t.grp = 0;
+  if (p.offsets) {
+    const int mt = L / n_tiles;
+    const int hl = __ffsll((long long)__ballot(inc > mt)) - 1;  // the first lane past it
+    first = __builtin_amdgcn_readlane(inc - sum, hl);
+    t.grp = hl * per;
+    for (int i = 0; i < per; ++i, ++t.grp) {
+      if (per <= KEEP) {
+        const int w = i == 0 ? v[0] : i == 1 ? v[1] : i == 2 ? v[2] : v[3];
+        tiles = __builtin_amdgcn_readlane(w, hl);
+      } else {
+        tiles = nv_group_tiles(p.offsets, p.G, t.grp, bm);
+      }
+      if (mt < first + tiles) break;
+      first += tiles;
+    }
+  }
+  const int i = L - first * n_tiles, band = i / (8 * n_tiles);
+  const int gm = min(8, tiles - band * 8), j = i - band * 8 * n_tiles;
   t.local = band * 8 + j % gm;
   t.nt = j / gm;
   return t;
@@ -396,13 +436,7 @@ struct I8Tile {
   }
 
   template <int NL>
-  __device__ __forceinline__ void run(const float* sw) {
-    float sa[NL];
-#pragma unroll
-    for (int a = 0; a < NL; ++a) {
-      const int m = min(beg + (a * WM + wm) * 32 + lr, end - 1);
-      sa[a] = p.a_scales[GATHER ? (int64_t)p.gather[m] : (int64_t)m];
-    }
+  __device__ __forceinline__ void run(const float* sw, const float* sa) {
     int16v acc[NL][FN];
 #pragma unroll
     for (int a = 0; a < NL; ++a)
@@ -506,9 +540,7 @@ struct I8Tile {
   // (FM == 1): calls of their size are over before a long loop's code is fetched.
   // Waves without rows compute on repeated rows and store nothing; the chunk
   // behind the last whole one is masked like every other.
-  __device__ __forceinline__ void run_small(const float* sw) {
-    const int m = min(beg + wm * 32 + lr, end - 1);
-    const float sa = p.a_scales[GATHER ? (int64_t)p.gather[m] : (int64_t)m];
+  __device__ __forceinline__ void run_small(const float* sw, const float* sa) {
     int16v acc[1][FN];
 #pragma unroll
     for (int b = 0; b < FN; ++b)
@@ -556,7 +588,7 @@ struct I8Tile {
       }
       buf = buf + 1 == NS ? 0 : buf + 1;
     }
-    if (beg + wm * 32 < end) store<1>(acc, &sa, sw);
+    if (beg + wm * 32 < end) store<1>(acc, sa, sw);
   }
 
   // Element e of fragment (a, b): tile row (a WM + wm) 32 + lr, tile column
@@ -657,8 +689,17 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_i8_gemm(I8Params p, int n_t
     }
     return min(n0 + i, k.cols - 1);
   };
-  for (int i = threadIdx.x; i < BN; i += Tile::NT)
-    sw[i] = p.w_scales[wrow + column(i) + (Tile::SILU && (i >> 5 & 1) ? k.cols : 0)];
+  // the loads that the copies' addresses do not need are issued before those that
+  // they do, and waited for after them
+  static_assert(BN <= Tile::NT, "a scale for a thread");
+  const int ci = min((int)threadIdx.x, BN - 1);
+  const float my_sw = p.w_scales[wrow + column(ci) + (Tile::SILU && (ci >> 5 & 1) ? k.cols : 0)];
+  int src[FM];
+#pragma unroll
+  for (int a = 0; a < FM; ++a) {
+    const int m = min(k.beg + (a * WM + k.wm) * 32 + k.lr, k.end - 1);
+    src[a] = GATHER ? p.gather[m] : m;
+  }
   k.abase = reinterpret_cast<const uint8_t*>(p.a_codes) + (GATHER ? 0 : (int64_t)k.beg * p.K);
   k.wbase = reinterpret_cast<const uint8_t*>(p.w_codes) + (wrow + n0) * p.K;
   k.ubase = k.wbase + (int64_t)k.cols * p.K;
@@ -678,18 +719,22 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_i8_gemm(I8Params p, int n_t
       k.off[j] = (uint32_t)(column(row - BM) - n0) * (uint32_t)p.K + at;
     }
   }
+  float sa[FM];
+#pragma unroll
+  for (int a = 0; a < FM; ++a) sa[a] = p.a_scales[src[a]];
+  if (threadIdx.x < BN) sw[threadIdx.x] = my_sw;
   if constexpr (FM == 1) {
-    k.run_small(sw);
+    k.run_small(sw, sa);
   } else {
     // fragments of 32 rows that hold rows: frag a of wave row wm starts at row (a
     // WM + wm) 32.  A wave without rows computes on repeated ones.
     const int frags = (min(k.end - k.beg, BM) + 31) >> 5;
     const int nl = (frags - k.wm + WM - 1) / WM;
-    if (nl >= FM) k.template run<FM>(sw);
-    else if (FM > 4 && nl == 4) k.template run<(FM > 4 ? 4 : 1)>(sw);
-    else if (FM > 3 && nl == 3) k.template run<(FM > 3 ? 3 : 1)>(sw);
-    else if (FM > 2 && nl == 2) k.template run<(FM > 2 ? 2 : 1)>(sw);
-    else k.template run<1>(sw);
+    if (nl >= FM) k.template run<FM>(sw, sa);
+    else if (FM > 4 && nl == 4) k.template run<(FM > 4 ? 4 : 1)>(sw, sa);
+    else if (FM > 3 && nl == 3) k.template run<(FM > 3 ? 3 : 1)>(sw, sa);
+    else if (FM > 2 && nl == 2) k.template run<(FM > 2 ? 2 : 1)>(sw, sa);
+    else k.template run<1>(sw, sa);
   }
 }
 
