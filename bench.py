@@ -10,9 +10,9 @@ input already resident in HBM:
 Weights are quantized once before timing (offline, as in rollout).
 
 Comparators (timed after the main measurement, same inputs, same weights):
-the same path with RAC off (naive NVFP4 W4A4), and an FP8 (E4M3) W8A8 step
+the same path with RAC off (naive NVFP4 W4A4), an FP8 (E4M3) W8A8 step
 with per-row activation and per-channel weight scales -- the format the pages
-compare QUADS's rollout throughput against.
+compare QUADS's rollout throughput against -- and an INT8 W8A8 step.
 
 Prints one JSON line.  `value` is the algorithmic GEMM TFLOP/s of the whole
 step (main + residual passes of every GEMM, residual counted over the active
@@ -49,7 +49,7 @@ def parse():
     ap.add_argument("--no-rac", action="store_true", help="naive W4A4 (RAC off)")
     ap.add_argument("--cpu-baseline", type=int, default=1)
     ap.add_argument("--comparators", type=int, default=1,
-                    help="also time RAC-off NVFP4 and FP8 W8A8 steps")
+                    help="also time RAC-off NVFP4, FP8 and INT8 W8A8 steps")
     ap.add_argument("--extras", type=int, default=1,
                     help="MoE workloads: also time the full block (weighted combine), a "
                          "16-token decode call eager vs HIP-graph replay, and the trainer-side "
@@ -102,29 +102,36 @@ def main():
         return L.FP8(torch.empty((G, N, K), dtype=torch.uint8, device=dev),
                      torch.empty((G, N), dtype=torch.float32, device=dev)) if cmp_ else None
 
-    def tee(gen, dtype, f8):
-        """Upload each weight matrix once; FP8-quantize it for the comparator
-        while the NVFP4 quantizer takes it."""
+    def int8_buf(G, N, K):
+        return L.INT8(torch.empty((G, N, K), dtype=torch.int8, device=dev),
+                      torch.empty((G, N), dtype=torch.float32, device=dev)) if cmp_ else None
+
+    def tee(gen, dtype, f8, i8):
+        """Upload each weight matrix once; FP8- and INT8-quantize it for the
+        comparators while the NVFP4 quantizer takes it."""
         for e, m in gen:
             t = to_dev(m, dtype)
             if f8 is not None:
                 L.fp8_quantize_rows(t, out=L.FP8(f8.codes[e], f8.scales[e]))
+                L.int8_quantize_rows(t, out=L.INT8(i8.codes[e], i8.scales[e]))
             yield e, t
 
     if w.kind == "moe":
         lg_np = D.router_logits(w)
         lg = torch.from_numpy(lg_np).to(dev)
         f8_gu, f8_d = fp8_buf(w.E, 2 * w.I, w.H), fp8_buf(w.E, w.H, w.I)
-        wgu = P.quantize_weights(tee(D.expert_weights(w, "gate_up"), "bf16", f8_gu),
+        i8_gu, i8_d = int8_buf(w.E, 2 * w.I, w.H), int8_buf(w.E, w.H, w.I)
+        wgu = P.quantize_weights(tee(D.expert_weights(w, "gate_up"), "bf16", f8_gu, i8_gu),
                                  w.E, 2 * w.I, w.H, dev)
-        wd = P.quantize_weights(tee(D.expert_weights(w, "down"), "bf16", f8_d),
+        wd = P.quantize_weights(tee(D.expert_weights(w, "down"), "bf16", f8_d, i8_d),
                                 w.E, w.H, w.I, dev)
         nsh = w.n_select_h if rac else None
         rows = w.T * w.topk
         amax_h = torch.zeros(1, dtype=torch.float32, device=dev)
     else:
-        f8_w = fp8_buf(1, w.N, w.K)
-        wq = P.quantize_weights(tee([(0, D.dense_weight(w))], w.x_dtype, f8_w), 1, w.N, w.K, dev)
+        f8_w, i8_w = fp8_buf(1, w.N, w.K), int8_buf(1, w.N, w.K)
+        wq = P.quantize_weights(tee([(0, D.dense_weight(w))], w.x_dtype, f8_w, i8_w), 1, w.N, w.K,
+                                dev)
         offs = torch.tensor([0, w.rows], dtype=torch.int32, device=dev)
     torch.cuda.synchronize()
     t_setup = time.time() - t_setup
@@ -194,6 +201,26 @@ def main():
         ev[1].record()
         y = L.fp8_grouped_gemm(xq, f8_w, offs, N=w.N, K=w.K, total_rows=w.rows)
         ev[2].record()
+        return y
+
+    def step_int8(ev):
+        """INT8 W8A8 comparator: the same routing, rows quantized by the products."""
+        if w.kind == "moe":
+            ev[0].record()
+            rt = L.moe_route(lg, w.topk)
+            ev[1].record()
+            h = L.int8_grouped_gemm(x, i8_gu, rt.expert_offsets, N=2 * w.I, K=w.H,
+                                    total_rows=rows, gather_rows=rt.gather_rows,
+                                    epilogue=L.NVFP4_EPI_SILU_MUL_BF16)
+            ev[2].record()
+            y = L.int8_grouped_gemm(h, i8_d, rt.expert_offsets, N=w.H, K=w.I, total_rows=rows)
+            for e in ev[3:]:
+                e.record()
+            return y
+        ev[0].record()
+        y = P.int8_linear(x, i8_w, out_dtype=torch.float32)
+        for e in ev[1:]:
+            e.record()
         return y
 
     mk = lambda: [torch.cuda.Event(enable_timing=True) for _ in range(NEV)]
@@ -285,7 +312,7 @@ def main():
     value = flops / (ms_step * 1e-3) / 1e12
     if cmp_:
         res["comparators"] = comparators(w, timed, step, step_fp8, seg, ms_step, rac, NEV,
-                                         step_pe if w.kind == "moe" else None)
+                                         step_pe if w.kind == "moe" else None, step_int8)
         if args.fp8_library_reference:
             lib = library_fp8_reference(w, dev)
             f8 = res["comparators"]["fp8_w8a8"]
@@ -340,8 +367,8 @@ def main():
     print(json.dumps(line), flush=True)
 
 
-def comparators(w, timed, step, step_fp8, seg, ms_step, rac, nev, step_pe=None):
-    """RAC-off NVFP4 and FP8 W8A8 steps on the same inputs and weights."""
+def comparators(w, timed, step, step_fp8, seg, ms_step, rac, nev, step_pe=None, step_int8=None):
+    """RAC-off NVFP4, FP8 and INT8 W8A8 steps on the same inputs and weights."""
     out = {}
     if rac:
         _, ms_naive, ev_n = timed(lambda ev: step(ev, None, None))
@@ -376,6 +403,13 @@ def comparators(w, timed, step, step_fp8, seg, ms_step, rac, nev, step_pe=None):
                                gemm_us=round(t[1] * 1e3, 2),
                                gemm_tflops=round(f / t[1] / 1e9, 1),
                                nvfp4_rac_step_over_fp8_step=round(ms_step / ms_f8, 4))
+    if step_int8 is not None:
+        _, ms_i8, ev_i = timed(step_int8)
+        out["int8_w8a8"] = dict(ms_per_step=round(ms_i8, 4),
+                                nvfp4_rac_step_over_int8_step=round(ms_step / ms_i8, 4))
+        if w.kind == "moe":
+            out["int8_w8a8"].update(quant_and_gate_up_us=round(seg(1, ev_i) * 1e3, 2),
+                                    quant_and_down_us=round(seg(2, ev_i) * 1e3, 2))
     return out
 
 

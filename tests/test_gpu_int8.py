@@ -7,6 +7,7 @@ import torch
 
 from nvfp4_w4a4_moe_quant_amd import _lib as L
 from nvfp4_w4a4_moe_quant_amd import datagen as D
+from nvfp4_w4a4_moe_quant_amd import logprob_gap
 from nvfp4_w4a4_moe_quant_amd import pipeline as P
 import int8_ref as R
 
@@ -292,6 +293,17 @@ def test_moe_block_together():
             e = P.int8_moe_block(sx.clone(), sl.clone(), wgu, wd, w.topk)["out"]
             torch.cuda.synchronize()
             assert torch.equal(o, e)
+
+
+def test_command_and_router():
+    """The log-prob gap command with the INT8 rollout, which lies nearer to its
+    trainer than naive W4A4 to its own, and the router's figures."""
+    say("int8 in the log-prob gap command")
+    res = dict(logprob_gap.gaps(3, vocab=2000, int8=True))
+    assert len(res) == 4
+    assert 0 < res["INT8 W8A8"]["mean"] < res["naive W4A4"]["mean"]
+    r = logprob_gap.router(3)
+    assert 0 <= r["emptiest"] <= 1 <= r["fullest"] and r["balance"] > 0 and r["z"] > 0
 
 
 def test_offsets_beyond_32_bits():
