@@ -507,6 +507,8 @@ struct I8Tile {
             for (int j = i * PART / NM; j < (i + 1) * PART / NM; ++j)
               issue1(j0 + j, nx, to, back);
           }
+          if (i == 0) __builtin_amdgcn_s_setprio(1);
+          if (i == NM - 1) __builtin_amdgcn_s_setprio(0);
           const int a = i / FN, b = i % FN;
           acc[a][b] = __builtin_amdgcn_mfma_i32_32x32x32_i8(wf[cur][b], af[cur][a], acc[a][b], 0, 0, 0);
           __builtin_amdgcn_sched_barrier(0);
