@@ -277,18 +277,15 @@ __global__ __launch_bounds__(64 * kFwdWaves) void k_balance(BalParams p) {
 // workgroup that comes last adds up the loss, from all workgroups' shares in
 // their order.  The counter was cleared by the launch before.
 __global__ __launch_bounds__(kJoinCols* kJoinParts) void k_balance_join(BalParams p, int nblk) {
-  __shared__ double rs[kJoinParts][kJoinCols];
-  __shared__ int32_t rc[kJoinParts][kJoinCols];
-  __shared__ double wz[16];
-  __shared__ int64_t wn[16];
+  // two parts to a wave, whose sums meet in registers
+  constexpr int WAVES = kJoinCols * kJoinParts / 64;
+  static_assert(kJoinCols == 32 && WAVES == 16 && kFwdBlocks <= 256, "lanes below");
+  __shared__ double rs[WAVES][kJoinCols];
+  __shared__ int32_t rc[WAVES][kJoinCols];
+  __shared__ double wz[4];
+  __shared__ int32_t wn[4];
   const int tid = threadIdx.x, col = tid % kJoinCols, part = tid / kJoinCols;
   const int e = blockIdx.x * kJoinCols + col;
-  double z = 0.0;
-  int64_t n = 0;
-  if (tid < nblk) {  // nblk <= 256: four waves
-    z = p.part_z[tid];
-    n = p.part_n[tid];
-  }
   double s = 0.0;
   int c = 0;
   if (e < p.E) {
@@ -301,34 +298,43 @@ __global__ __launch_bounds__(kJoinCols* kJoinParts) void k_balance_join(BalParam
       }
     }
   }
-  rs[part][col] = s;
-  rc[part][col] = c;
+  if (tid < 256) {  // nblk <= 256
+    double z = tid < nblk ? p.part_z[tid] : 0.0f;
+    int n = tid < nblk ? p.part_n[tid] : 0;
 #pragma unroll
-  for (int o = 32; o > 0; o >>= 1) {
-    z += __shfl_xor(z, o, 64);
-    n += __shfl_xor(n, o, 64);
+    for (int o = 32; o > 0; o >>= 1) {
+      z += __shfl_xor(z, o, 64);
+      n += __shfl_xor(n, o, 64);
+    }
+    if ((tid & 63) == 0) {
+      wz[tid >> 6] = z;
+      wn[tid >> 6] = n;
+    }
   }
-  if ((tid & 63) == 0) {
-    wz[tid >> 6] = z;
-    wn[tid >> 6] = n;
+  s += __shfl_xor(s, 32, 64);
+  c += __shfl_xor(c, 32, 64);
+  if ((tid & 32) == 0) {
+    rs[tid >> 6][col] = s;
+    rc[tid >> 6][col] = c;
   }
   __syncthreads();
   if (tid >= 64) return;
-  n = wn[0] + wn[1] + wn[2] + wn[3];
+  const int64_t n = (int64_t)wn[0] + wn[1] + wn[2] + wn[3];
   const double inv = n > 0 ? 1.0 / (double)n : 0.0;
+  s = 0.0;
+  c = 0;
+#pragma unroll
+  for (int i = 0; i < WAVES / 2; ++i) {
+    s += rs[part * (WAVES / 2) + i][col];
+    c += rc[part * (WAVES / 2) + i][col];
+  }
+  s += __shfl_xor(s, 32, 64);
+  c += __shfl_xor(c, 32, 64);
   double dot = 0.0;
-  if (part == 0) {
-    s = 0.0;
-    c = 0;
-    for (int i = 0; i < kJoinParts; ++i) {
-      s += rs[i][col];
-      c += rc[i][col];
-    }
-    if (e < p.E) {
-      p.counts[e] = c;
-      if (p.mean) p.mean[e] = (float)(s * inv);
-      dot = (double)c * (s * inv);
-    }
+  if (part == 0 && e < p.E) {
+    p.counts[e] = c;
+    if (p.mean) p.mean[e] = (float)(s * inv);
+    dot = (double)c * (s * inv);
   }
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) dot += __shfl_xor(dot, o, 64);
