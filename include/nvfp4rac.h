@@ -546,7 +546,8 @@ int int8_quantize_rows(const void* x, int in_dtype, int64_t rows, int64_t K, int
  * 16 <= K <= 131056 (no sum of 8-bit products can leave 32 bits), num_groups <=
  * 2^20, total_rows <= 2^30; codes and x 16-byte aligned, out aligned to its
  * elements, ws 16-byte aligned.  Without a gather, src_rows >= total_rows;
- * src_rows K <= 2^36.  Calls that may overlap need workspaces of their own. */
+ * src_rows K <= 2^36.  A call that needs a grid of 2^32 threads (some 2^23 tiles
+ * of 64 x 128 or larger) is refused.  Calls that may overlap need workspaces of their own. */
 typedef struct {
   int64_t num_groups;           /* G >= 1 */
   int64_t N;                    /* output columns (2I for SILU_MUL) */

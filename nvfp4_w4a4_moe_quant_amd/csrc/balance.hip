@@ -6,11 +6,18 @@
 // with the next ones in flight.  Forward, a lane keeps the sums of its experts'
 // probabilities over the rows of its wave; workgroups write partial sums, and a
 // second launch joins them, a workgroup for 32 experts each, the last of them
-// adding up the loss.  At most 128 rows take one launch of one workgroup.
+// adding up the loss.  Few rows take one launch of one workgroup.
 // Backward needs the counts alone besides the row itself:
 //   grad_j = p_j (a (c_j - sum_e c_e p_e) + b lse).
 // The counts enter centred, c_j - (sum c) / E, which changes nothing since the p
 // sum to one and keeps the difference small where the experts are balanced.
+//
+// What bounds it: few rows the latency of a chain of loads, reductions and the
+// join (8192 x 256 FP32: forward 5.4 + 7.7 us, backward 7.8 us, for 8 MB read
+// once), many rows HBM (backward of 65536 x 256 FP32: 25 us for 134 MB, 5.4
+// TB/s; of 65536 x 128 bf16 15 us for 34 MB).  A wave for a row with one logit to
+// a load, and one workgroup to join: 10.5 + 80 us for the first forward, 77 + 83
+// us for the last, against 9.1 + 6.9 us.
 
 #include <type_traits>
 
@@ -22,7 +29,11 @@ constexpr int kMaxE = 1024;
 constexpr float kLog2E = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
 constexpr int kFwdWaves = 16;
 constexpr int kFwdBlocks = 256;   // workgroups (partial sums) at most
-constexpr int64_t kOneBlock = 128;  // rows that one workgroup takes alone
+// One workgroup alone takes rows that are at most so many lanes' work, five rows
+// of a lane (128 experts: 64 rows 5.0 us for 7.9 in two launches, 128 rows 6.7 for
+// 8.0, 192 rows 8.6 for 8.0; 256 experts: 64 rows 7.1 for 8.5, 128 rows 11.1 for
+// 8.7; 32 experts: 512 rows 6.4 for 7.7).
+constexpr int64_t kOneBlock = 5 * 64 * kFwdWaves;
 constexpr int kJoinCols = 32, kJoinParts = 32;
 
 struct BalParams {
@@ -422,9 +433,8 @@ __global__ __launch_bounds__(256) void k_balance_bwd(BalParams p) {
 }
 
 int fwd_blocks(int64_t T, int rpw) {
-  if (T <= kOneBlock) return 1;
   const int64_t n = (T + kFwdWaves * rpw - 1) / (kFwdWaves * rpw);
-  return (int)(n < kFwdBlocks ? n : kFwdBlocks);
+  return (int)(n < 1 ? 1 : n < kFwdBlocks ? n : kFwdBlocks);
 }
 
 template <bool BF16, int V, int LPR, int PER>
@@ -432,8 +442,8 @@ int launch(const BalParams& p, bool backward, bool vout, hipStream_t s) {
   if (!backward) {
     const int nblk = fwd_blocks(p.T, 64 / LPR);
     const dim3 grid((unsigned)nblk), block(64 * kFwdWaves);
-    if (p.T <= kOneBlock) {
-      hipLaunchKernelGGL((k_balance<BF16, V, LPR, PER, true>), grid, block, 0, s, p);
+    if (p.T * LPR <= kOneBlock) {
+      hipLaunchKernelGGL((k_balance<BF16, V, LPR, PER, true>), dim3(1), block, 0, s, p);
       return nv_launch_status();
     }
     hipLaunchKernelGGL((k_balance<BF16, V, LPR, PER, false>), grid, block, 0, s, p);
@@ -487,7 +497,7 @@ extern "C" {
 size_t moe_balance_loss_workspace_size(int64_t T, int64_t E) {
   if (T < 0 || E < 1 || E > kMaxE) return 0;
   // the loss's shares and the counter, then the partial sums
-  return nv_round256(512 + (T <= kOneBlock ? 0 : 8 * (size_t)fwd_blocks(T, 1) * (size_t)(E + 1)));
+  return nv_round256(512 + (T * 64 <= kOneBlock ? 0 : 8 * (size_t)fwd_blocks(T, 1) * (size_t)(E + 1)));
 }
 
 int moe_balance_loss(const void* logits, int dtype, int64_t T, int64_t E, int64_t ld,

@@ -3,7 +3,32 @@
 // One FP32 scale per activation row (at run time) and per weight output
 // channel: s = RN32(amax / 127), r = RN32(1 / s), code = the nearest integer to
 // RN32(x r).  A product is y = s_a s_w sum_k a_k w_k with the sum exact in 32-bit
-// integers (K <= 131056), whatever its order.
+// integers (K <= 131056), whatever its order, so K may be split over waves freely.
+//
+// MI355X design:
+//  * k_i8_rows: a row stays in the registers of one to eight waves between its
+//    maximum and its codes.  HBM-bound when large (8192 x 7168 bf16 32 us, 5.5
+//    TB/s), 2 to 4 us when small.
+//  * k_i8_few: a few rows against W that streams once, straight into registers;
+//    the waves of a workgroup split K.  4.7 us for one row of 4096 x 4096 (3.6 TB/s
+//    of codes), 40 us for the 8 rows of a token at K 7168, N 4096 (5.9 TB/s).
+//  * k_i8_gemm: tiles of 64 x 128 to 320 x 256.  Rows of 128 k go into LDS by DMA,
+//    two or three chunks deep, at uniform bases and 32-bit offsets; fragments of
+//    the next 32 k are read while those in registers are multiplied; the D tiles
+//    are W by rows, so that a lane holds four neighbouring columns, and go out
+//    through LDS as whole rows of 16-byte pieces (as they come, a store of 2 or 4
+//    bytes each, 65536 x 4096 x 1024 took 548 us for 361).  The smallest tile
+//    streams W for many experts of few rows: 483 us for 16 tokens of 256 experts
+//    (K 7168, N 4096, 102 experts' 2.95 GB: 6.1 TB/s).
+//  * What bounds the large products is power: 65536 x 4096 x 8192 runs its matrix
+//    cores 80% of the cycles at 1.3 GHz, 256 experts of 256 rows 65% at 1.33
+//    GHz (2.4 GHz when light; the same call on zeros is 22% faster).  Where the
+//    time goes otherwise (parts left out for timing, 1836 us then): the copies
+//    into LDS 20%, the fragment reads 4%, waits and barriers nothing.  Tried and
+//    slower: 16 x 16 x 64 products (1883 for 1836 us); four waves of 128 x 128
+//    (K 1024: 373 for 346 us; K 8192: 1729-1766 for 1780-1815); W fetched into
+//    the L2 a few chunks ahead (256 experts 2239 for 2102 us); copies of rows
+//    behind a group's end left out (2173 for 2137 us).
 
 #include <type_traits>
 
@@ -507,6 +532,7 @@ struct I8Tile {
             for (int j = i * PART / NM; j < (i + 1) * PART / NM; ++j)
               issue1(j0 + j, nx, to, back);
           }
+          // the wave that multiplies goes first (1695 for 1759 us, K 8192)
           if (i == 0) __builtin_amdgcn_s_setprio(1);
           if (i == NM - 1) __builtin_amdgcn_s_setprio(0);
           const int a = i / FN, b = i % FN;
@@ -740,21 +766,28 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_i8_gemm(I8Params p, int n_t
   }
 }
 
-template <int WM, int WN, int FM, int FN, int NS, int EPI>
+// The tile shapes, and the workgroups of a call on one of them (an upper bound:
+// every group's last tile may be part of one).
+struct I8Shape {
+  int bm, bn, threads;
+};
+constexpr I8Shape kTiles[4] = {{64, 128, 256}, {128, 256, 512}, {256, 256, 512}, {320, 256, 512}};
+
+int64_t i8_workgroups(const I8Shape& t, int64_t rows, int64_t N, int64_t groups) {
+  return ((rows + t.bm - 1) / t.bm + groups) * ((N + t.bn - 1) / t.bn);
+}
+
+template <int TILE, int WM, int WN, int FM, int FN, int NS, int EPI>
 int launch_tiles(const I8Params& p, hipStream_t s) {
-  constexpr int BM = WM * FM * 32, BN = WN * FN * 32;
-  const int cols = EPI == NVFP4_EPI_SILU_MUL_BF16 ? p.N / 2 : p.N;
-  const int per = EPI == NVFP4_EPI_SILU_MUL_BF16 ? BN / 2 : BN;
-  const int n_tiles = (cols + per - 1) / per;
-  const int64_t m_slots = ((int64_t)p.total_rows + BM - 1) / BM + (p.offsets ? p.G : 0);
-  const int64_t nb = m_slots * n_tiles;
-  if (nb * 64 * WM * WN > 0xffffffffLL) return NVFP4_ERR_SHAPE;
+  constexpr I8Shape t = kTiles[TILE];
+  constexpr int NT = 64 * WM * WN;
+  static_assert(t.bm == WM * FM * 32 && t.bn == WN * FN * 32 && t.threads == NT, "tile shape");
+  const int n_tiles = (p.N + t.bn - 1) / t.bn;  // SiLU: as many gate as up columns in a tile
+  const dim3 grid((unsigned)i8_workgroups(t, p.total_rows, p.N, p.offsets ? p.G : 0));
   if (p.gather)
-    hipLaunchKernelGGL((k_i8_gemm<WM, WN, FM, FN, NS, EPI, true>), dim3((unsigned)nb),
-                       dim3(64 * WM * WN), 0, s, p, n_tiles);
+    hipLaunchKernelGGL((k_i8_gemm<WM, WN, FM, FN, NS, EPI, true>), grid, dim3(NT), 0, s, p, n_tiles);
   else
-    hipLaunchKernelGGL((k_i8_gemm<WM, WN, FM, FN, NS, EPI, false>), dim3((unsigned)nb),
-                       dim3(64 * WM * WN), 0, s, p, n_tiles);
+    hipLaunchKernelGGL((k_i8_gemm<WM, WN, FM, FN, NS, EPI, false>), grid, dim3(NT), 0, s, p, n_tiles);
   return nv_launch_status();
 }
 
@@ -775,7 +808,7 @@ struct I8Plan {
   int few;        // k_i8_few with so many waves to a block of columns, or 0
   int rt;         // its row tiles of 16 to a workgroup
   int64_t tiles;  // workgroups' row tiles at most
-  int tile;       // else: the tile shape of launch_gemm
+  int tile;       // else: which of kTiles
 };
 
 // Times below are those of the product alone, from quantized rows, in a graph of
@@ -803,11 +836,10 @@ I8Plan plan_of(const int8_gemm_args_t* a) {
     // rounds over the chip times a tile's time beside the 256 x 256 tile's (N = K =
     // 4096: 512 rows 20, 24, 41 us for tiles 0, 1, 2; 1024 rows 25, 26, 43; 2048
     // rows 54, 36, 48; 4096 rows 98, 70, 60 and 64 for tile 3)
-    auto rounds = [&](int64_t bm, int64_t bn) {
-      return (double)((((rows + bm - 1) / bm) * ((a->N + bn - 1) / bn) + 255) / 256);
+    auto rounds = [&](int i) {
+      return (double)((i8_workgroups(kTiles[i], rows, a->N, 0) + 255) / 256);
     };
-    const double c[4] = {rounds(64, 128) * 0.19 + 0.1, rounds(128, 256) * 0.62, rounds(256, 256),
-                         rounds(320, 256) * 1.25};
+    const double c[4] = {rounds(0) * 0.19 + 0.1, rounds(1) * 0.62, rounds(2), rounds(3) * 1.25};
     for (int i = 1; i < 4; ++i)
       if (c[i] < c[pl.tile]) pl.tile = i;
   } else if (mean <= 48) {
@@ -840,10 +872,10 @@ int launch_gemm(const I8Params& p, const I8Plan& pl, hipStream_t s) {
     if (pl.rt == 2) return launch_few_of<EPI, 2>(p, pl, s);
     return launch_few_of<EPI, 4>(p, pl, s);
   }
-  if (pl.tile == 0) return launch_tiles<2, 2, 1, 2, 2, EPI>(p, s);  // 64 x 128, three to a CU
-  if (pl.tile == 1) return launch_tiles<2, 4, 2, 2, 3, EPI>(p, s);  // 128 x 256
-  if (pl.tile == 2) return launch_tiles<4, 2, 2, 4, 2, EPI>(p, s);  // 256 x 256
-  return launch_tiles<2, 4, 5, 2, 2, EPI>(p, s);                    // 320 x 256
+  if (pl.tile == 0) return launch_tiles<0, 2, 2, 1, 2, 2, EPI>(p, s);  // three to a CU
+  if (pl.tile == 1) return launch_tiles<1, 2, 4, 2, 2, 3, EPI>(p, s);
+  if (pl.tile == 2) return launch_tiles<2, 4, 2, 2, 4, 2, EPI>(p, s);
+  return launch_tiles<3, 2, 4, 5, 2, 2, EPI>(p, s);
 }
 
 template <bool BF16, int RW, int VPL>
@@ -856,8 +888,12 @@ int launch_rows_of(const void* x, int64_t rows, int K, int64_t ldx, int8_t* code
   return nv_launch_status();
 }
 
+// A workgroup for a row where rows are few (one wave a row before: 128 x 7168 8.6
+// us, now 3.9; 512 x 4096 6.2 and 4.0; 1 x 4096 5.1 and 3.9); else as many waves as
+// hold it in registers (8192 x 7168 read twice 44 us, from registers 32; 65536 x
+// 2048 89 and 76).
 template <bool BF16>
-int launch_rows_bf16(const void* x, int64_t rows, int K, int64_t ldx, int8_t* codes, float* scales,
+int launch_rows_by_size(const void* x, int64_t rows, int K, int64_t ldx, int8_t* codes, float* scales,
                      hipStream_t s) {
   const int nv = K / 8;
   if (rows <= 512 && nv > 64) {
@@ -874,8 +910,8 @@ int launch_rows_bf16(const void* x, int64_t rows, int K, int64_t ldx, int8_t* co
 
 int launch_rows(const void* x, int64_t dtype, int64_t rows, int K, int64_t ldx, int8_t* codes,
                 float* scales, hipStream_t s) {
-  return dtype == NVFP4_IN_BF16 ? launch_rows_bf16<true>(x, rows, K, ldx, codes, scales, s)
-                                : launch_rows_bf16<false>(x, rows, K, ldx, codes, scales, s);
+  return dtype == NVFP4_IN_BF16 ? launch_rows_by_size<true>(x, rows, K, ldx, codes, scales, s)
+                                : launch_rows_by_size<false>(x, rows, K, ldx, codes, scales, s);
 }
 
 bool misaligned(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) != 0; }
@@ -957,6 +993,10 @@ int int8_grouped_gemm(const int8_gemm_args_t* a, void* ws, size_t ws_bytes, void
   const int64_t cols = a->epilogue == NVFP4_EPI_SILU_MUL_BF16 ? a->N / 2 : a->N;
   p.vec = !misaligned(a->out, 16) && cols * esize % 16 == 0;
   const I8Plan pl = plan_of(a);
+  // the grid holds fewer than 2^32 threads
+  NV_RETURN_IF(!pl.few && i8_workgroups(kTiles[pl.tile], a->total_rows, a->N, a->num_groups) *
+                                  kTiles[pl.tile].threads > 0xffffffffLL,
+               NVFP4_ERR_SHAPE);
   if (a->x) {
     int8_t* codes = reinterpret_cast<int8_t*>(ws);
     float* scales = reinterpret_cast<float*>(codes + nv_round256((size_t)a->src_rows * p.K));

@@ -142,6 +142,7 @@ GROUPS = [
     (3, [0], 32, 48), (4, [64, 0, 1, 200, 16], 384, 256), (5, [2] * 70, 96, 208),
     (6, [300, 12], 514, 1040), (7, [0] * 63 + [9] + [0] * 64 + [20], 64, 128),
     (8, [1000, 0, 600, 24], 768, 320), (9, [30] * 40, 256, 2048), (10, [0, 2, 1, 0, 4] * 60, 48, 96),
+    (18, [20] * 300, 64, 64), (19, ([0] * 9 + [2]) * 100, 2050, 48), (20, ([0] * 30 + [41]) * 33, 130, 80),
     (13, [256, 240, 288, 250, 230], 300, 1104), (14, [1200, 0, 0, 0, 50], 514, 400),
     (15, [100, 64, 0, 65, 128, 33], 270, 1104), (16, [200, 190, 129], 258, 1136),
     (17, [321, 200, 33], 260, 272), (11, [15, 16, 17, 31, 32, 33, 47, 48, 49], 320, 624), (12, [127, 128, 129, 255, 256, 257], 260, 176),

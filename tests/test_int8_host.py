@@ -79,6 +79,10 @@ def test_gemm_of_unquantized_rows_validation(lib):
     assert g(src_rows=0, gather_rows=FAKE) == ESHAPE
     assert g(src_rows=-1, gather_rows=FAKE) == ESHAPE
     assert g(x=MIS[8]) == EALIGN
+    # more tiles than a grid holds: refused before the rows are quantized
+    assert g(total_rows=1 << 30, src_rows=1, gather_rows=FAKE, N=1 << 24) == ESHAPE
+    assert g(num_groups=1 << 20, total_rows=1 << 25, src_rows=1, gather_rows=FAKE,
+             N=1 << 20) == ESHAPE
     need = _gemm(lib, size=True, **{**x, "src_rows": 5000, "gather_rows": FAKE, "total_rows": 9999})
     assert need >= 5000 * 52
     assert _gemm(lib, size=True) == 0                   # quantized: none
