@@ -538,11 +538,10 @@ int int8_quantize_rows(const void* x, int in_dtype, int64_t rows, int64_t K, int
  *   y[j, n] = RN32(RN32(a_scales[src] w_scales[g*N + n]) float(sum_k A[src,k] W_g[n,k]))
  * with the sum exact in 32 bits.  Epilogue F32 writes y, BF16 writes bf16(y),
  * SILU_MUL_BF16 h[j, i] = bf16(silu(y[j, i]) * y[j, I + i]) to [total_rows, I].
- * The activations come either quantized (a_codes, a_scales) or as x, which the
- * call quantizes as int8_quantize_rows does: into the workspace, or, for few
- * rows, inside the product's own launch.
- * group_offsets may be NULL with one group.  Rows of out that belong to no
- * group are left alone.  Requires 1 <= N <= 2^24 (even for SiLU), K % 16 == 0,
+ * The activations come either quantized (a_codes, a_scales) or as x, whose
+ * src_rows rows the call quantizes into the workspace first, as int8_quantize_rows
+ * does.  group_offsets may be NULL with one group.  group_offsets[G] may be less
+ * than total_rows; rows of out behind it are left alone.  Requires 1 <= N <= 2^24 (even for SiLU), K % 16 == 0,
  * 16 <= K <= 131056 (no sum of 8-bit products can leave 32 bits), num_groups <=
  * 2^20, total_rows <= 2^30; codes and x 16-byte aligned, out aligned to its
  * elements, ws 16-byte aligned.  Without a gather, src_rows >= total_rows;
@@ -553,7 +552,7 @@ typedef struct {
   int64_t N;                    /* output columns (2I for SILU_MUL) */
   int64_t K;                    /* contraction length */
   int64_t total_rows;           /* rows of the grouped output */
-  const int32_t* group_offsets; /* [G+1], ascending, [0] = 0, [G] = total_rows */
+  const int32_t* group_offsets; /* [G+1], ascending, [0] = 0, [G] <= total_rows */
   const int32_t* gather_rows;   /* [total_rows] or NULL (identity) */
   const int8_t* a_codes;        /* [src_rows, K], or NULL where x is given */
   const float* a_scales;        /* [src_rows] */
