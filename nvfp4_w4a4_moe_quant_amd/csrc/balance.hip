@@ -13,11 +13,11 @@
 // sum to one and keeps the difference small where the experts are balanced.
 //
 // What bounds it: few rows the latency of a chain of loads, reductions and the
-// join (8192 x 256 FP32: forward 5.4 + 7.7 us, backward 7.8 us, for 8 MB read
-// once), many rows HBM (backward of 65536 x 256 FP32: 25 us for 134 MB, 5.4
-// TB/s; of 65536 x 128 bf16 15 us for 34 MB).  A wave for a row with one logit to
-// a load, and one workgroup to join: 10.5 + 80 us for the first forward, 77 + 83
-// us for the last, against 9.1 + 6.9 us.
+// join (8192 x 256 FP32: forward 4.7 + 7.7 us, backward 7.4 us, for 8 MB read
+// once), many rows HBM (65536 x 256 FP32: forward 18 us, backward 24 us for 134
+// MB, 5.7 TB/s) or, in bf16, as much the arithmetic (65536 x 128: 7.6 + 6.9 us and
+// 14 us for 34 MB).  A wave for a row with one logit to a load, and one workgroup
+// to join: 10.5 + 80 us for the first forward, 77 + 83 us for the last.
 
 #include <type_traits>
 
@@ -131,33 +131,41 @@ struct BalRow {
   // l - m comes before the factor log2 e: a mask of the type's lowest value stays
   // the number that it is.
   __device__ __forceinline__ bool softmax(const BalParams& p, int lir, float (&l)[PER * V], float& lse) {
-    float m = -__builtin_inff(), real = 0.0f;
+    const float none = -__builtin_inff();
 #pragma unroll
     for (int j = 0; j < PER; ++j) {
-      if constexpr (V == 4) {
-        const uint32_t w[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) l[j * V + i] = __uint_as_float(w[i]);
-      } else if constexpr (V == 8) {
+      if constexpr (V > 1) {
         const uint32_t w[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          l[j * V + 2 * i] = __uint_as_float(w[i] << 16);
-          l[j * V + 2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+          if constexpr (BF16) {
+            l[j * V + 2 * i] = __uint_as_float(w[i] << 16);
+            l[j * V + 2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+          } else {
+            l[j * V + i] = __uint_as_float(w[i]);
+          }
         }
       } else {
         l[j] = one[j];
       }
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        float& v = l[j * V + i];
-        if ((j * LPR + lir) * V + i >= p.E) v = -__builtin_inff();
-        m = __builtin_fmaxf(m, v);
-        real = v == -__builtin_inff() ? real : 1.0f;
-      }
     }
+    if (p.E != LPR * PER * V)  // uniform: places without an expert
+#pragma unroll
+      for (int j = 0; j < PER; ++j)
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          if ((j * LPR + lir) * V + i >= p.E) l[j * V + i] = none;
+    float m = none;
+#pragma unroll
+    for (int i = 0; i < PER * V; ++i) m = __builtin_fmaxf(m, l[i]);
     m = bal_reduce<LPR>(m, BalMax());
-    real = bal_reduce<LPR>(real, BalMax());
+    float real = 1.0f;
+    if (__ballot(m == none)) {  // a row of nothing but -inf, or of NaN and -inf
+      real = 0.0f;
+#pragma unroll
+      for (int i = 0; i < PER * V; ++i) real = l[i] == none ? real : 1.0f;
+      real = bal_reduce<LPR>(real, BalMax());
+    }
     float s = 0.0f;
 #pragma unroll
     for (int i = 0; i < PER * V; ++i) {
@@ -390,6 +398,8 @@ __global__ __launch_bounds__(256) void k_balance_bwd(BalParams p) {
   const double n = (double)p.tokens[0], inv = n > 0.0 ? 1.0 / n : 0.0;
   const float a = (float)((double)p.grad_losses[0] * (double)p.E / (double)p.k * inv * inv);
   const float b = (float)((double)p.grad_losses[1] * 2.0 * inv);
+#pragma unroll
+  for (int i = 0; i < PER * V; ++i) c[i] *= a;
   for (; t - slot < p.T; t += stride) {
     nxt.load(p, t + stride, lir, false);
     float l[PER * V], lse;
@@ -397,9 +407,14 @@ __global__ __launch_bounds__(256) void k_balance_bwd(BalParams p) {
     float cp = 0.0f;
 #pragma unroll
     for (int i = 0; i < PER * V; ++i) cp += c[i] * l[i];
-    cp = bal_reduce<LPR>(cp, BalAdd());
+    cp = b * lse - bal_reduce<LPR>(cp, BalAdd());
+    if (live) {
 #pragma unroll
-    for (int i = 0; i < PER * V; ++i) l[i] = live ? l[i] * (a * (c[i] - cp) + b * lse) : 0.0f;
+      for (int i = 0; i < PER * V; ++i) l[i] *= c[i] + cp;
+    } else {
+#pragma unroll
+      for (int i = 0; i < PER * V; ++i) l[i] = 0.0f;
+    }
     if (t < p.T) {
       char* out = reinterpret_cast<char*>(p.grad) + t * p.ldg * SIZE;
 #pragma unroll

@@ -118,6 +118,23 @@ def test_nan_and_infinity_stay_in_their_rows(dtype):
     eq(a[~bad], b[~bad], "other rows")
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_rows_of_nan_and_masks_alone(dtype):
+    """A row of NaN and -inf counts and is NaN; one of -inf alone does not."""
+    say(f"balance, rows without a number, {dtype}")
+    for E in (8, 60, 64, 200):
+        z, ids, _ = case(E, 9, E, 2, dtype)
+        z[2], z[5], z[7] = float("-inf"), float("nan"), float("-inf")
+        z[7, E - 1] = float("nan")
+        r = L.moe_balance_loss(z, up(ids))
+        assert int(r.tokens) == 8 and torch.isnan(r.losses).all()
+        eq(host(r.counts), np.bincount(np.delete(ids, 2, 0).ravel(), minlength=E), "counts")
+        g = L.moe_balance_loss_backward(z, 2, r.counts, r.tokens, torch.ones(2, device=DEV))
+        g = host(g.float())
+        assert np.isnan(g[[5, 7]]).any(1).all() and not g[2].any()
+        assert np.isfinite(np.delete(g, [5, 7], 0)).all()
+
+
 def test_repeated_and_dropped_slots():
     say("balance, repeated slots")
     z, ids, _ = case(1, 30, 16, 5)

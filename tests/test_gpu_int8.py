@@ -336,6 +336,19 @@ def test_offsets_beyond_32_bits():
     assert not q.codes[:-3].any()
 
 
+def test_empty_layers():
+    say("int8, no rows")
+    w = L.INT8(torch.zeros(4, 64, 32, dtype=torch.int8, device=DEV), torch.zeros(4, 64, device=DEV))
+    d = L.INT8(torch.zeros(4, 32, 32, dtype=torch.int8, device=DEV), torch.zeros(4, 32, device=DEV))
+    x = torch.zeros(0, 32, device=DEV, dtype=torch.bfloat16)
+    o = P.int8_moe_block(x, torch.zeros(0, 4, device=DEV), w, d, 2)["out"]
+    assert o.shape == (0, 32)
+    one = L.INT8(w.codes[:1], w.scales[:1])
+    assert P.int8_linear(x, one).shape == (0, 64)
+    with pytest.raises(ValueError):
+        P.int8_linear(x, w)                                 # four groups are not a layer
+
+
 def test_deterministic():
     say("int8 deterministic")
     rng = np.random.default_rng(3)
