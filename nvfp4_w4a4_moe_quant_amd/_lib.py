@@ -693,12 +693,12 @@ def int8_grouped_gemm(a, w: INT8, group_offsets: Optional[torch.Tensor] = None, 
     [G, N].  group_offsets [G + 1] may be None for one group.  epilogue F32,
     SILU_MUL_BF16 or BF16.  validate=True checks the offsets and gather indices
     on the host first (check_groups; synchronizes)."""
-    quantized = isinstance(a, INT8)
+    quantized = type(a) is INT8
     x = a.codes if quantized else a
-    if x.dim() != 2 or x.shape[1] != K:
+    shape, dev = x.shape, x.device
+    if len(shape) != 2 or shape[1] != K:
         _refuse("activations [src_rows, K]")
-    src_rows = x.shape[0]
-    dev = x.device
+    src_rows = shape[0]
     if dev.type != "cuda":
         _refuse("activations on a GPU")
     G = 1 if group_offsets is None else group_offsets.numel() - 1

@@ -7,7 +7,7 @@
 //
 // MI355X design:
 //  * k_i8_rows: a row stays in the registers of one to eight waves between its
-//    maximum and its codes.  HBM-bound when large (8192 x 7168 bf16 32 us, 5.5
+//    maximum and its codes.  HBM-bound when large (8192 x 7168 bf16 29 us, 6.0
 //    TB/s), 2 to 4 us when small.
 //  * k_i8_few: a few rows against W that streams once, straight into registers;
 //    the waves of a workgroup split K.  4.7 us for one row of 4096 x 4096 (3.6 TB/s
@@ -889,9 +889,10 @@ int launch_rows_of(const void* x, int64_t rows, int K, int64_t ldx, int8_t* code
 }
 
 // A workgroup for a row where rows are few (one wave a row before: 128 x 7168 8.6
-// us, now 3.9; 512 x 4096 6.2 and 4.0; 1 x 4096 5.1 and 3.9); else as many waves as
-// hold it in registers (8192 x 7168 read twice 44 us, from registers 32; 65536 x
-// 2048 89 and 76).
+// us, now 3.9; 512 x 4096 6.2 and 4.0; 1 x 4096 5.1 and 3.9); else waves enough to
+// hold it in registers (8192 x 7168 read twice 44 us, four waves of 4 vectors 32,
+// eight of 2 29; 65536 x 2048 89, one of 4 76, two of 2 73, four of 1 92; 4096 x
+// 4096 two of 4 10.7, four of 2 11.7).
 template <bool BF16>
 int launch_rows_by_size(const void* x, int64_t rows, int K, int64_t ldx, int8_t* codes, float* scales,
                      hipStream_t s) {
@@ -902,9 +903,9 @@ int launch_rows_by_size(const void* x, int64_t rows, int K, int64_t ldx, int8_t*
   }
   if (nv <= 64) return launch_rows_of<BF16, 1, 1>(x, rows, K, ldx, codes, scales, s);
   if (nv <= 128) return launch_rows_of<BF16, 1, 2>(x, rows, K, ldx, codes, scales, s);
-  if (nv <= 256) return launch_rows_of<BF16, 1, 4>(x, rows, K, ldx, codes, scales, s);
+  if (nv <= 256) return launch_rows_of<BF16, 2, 2>(x, rows, K, ldx, codes, scales, s);
   if (nv <= 512) return launch_rows_of<BF16, 2, 4>(x, rows, K, ldx, codes, scales, s);
-  if (nv <= 1024) return launch_rows_of<BF16, 4, 4>(x, rows, K, ldx, codes, scales, s);
+  if (nv <= 1024) return launch_rows_of<BF16, 8, 2>(x, rows, K, ldx, codes, scales, s);
   return launch_rows_of<BF16, 8, 4>(x, rows, K, ldx, codes, scales, s);
 }
 

@@ -369,8 +369,9 @@ def int8_quantize_weights(mats: Iterable[Tuple[int, torch.Tensor]], G: int, N: i
     return w
 
 
-def _int8_no_gradient(*tensors: torch.Tensor):
-    if torch.is_grad_enabled() and any(t.requires_grad for t in tensors):
+def _int8_no_gradient(x: torch.Tensor, logits: Optional[torch.Tensor] = None):
+    if (x.requires_grad or (logits is not None and logits.requires_grad)) \
+            and torch.is_grad_enabled():
         raise RuntimeError("the INT8 layers have no gradient: detach their inputs or call them "
                            "under torch.no_grad()")
 
@@ -380,12 +381,14 @@ def int8_linear(x: torch.Tensor, w: L.INT8,
     """y = x W^T of x [rows, K] (bf16 or FP32), quantized per row by the call, and
     w (codes [1, N, K], scales [1, N]), as bf16 or FP32 [rows, N]."""
     _int8_no_gradient(x)
-    if out_dtype not in (torch.bfloat16, torch.float32):
+    if out_dtype is torch.bfloat16:
+        epilogue = L.NVFP4_EPI_BF16
+    elif out_dtype is torch.float32:
+        epilogue = L.NVFP4_EPI_F32
+    else:
         raise TypeError(f"unsupported dtype {out_dtype}")
-    N, K = w.codes.shape[-2:]
-    return L.int8_grouped_gemm(
-        x, w, N=N, K=K, total_rows=x.shape[0],
-        epilogue=L.NVFP4_EPI_F32 if out_dtype == torch.float32 else L.NVFP4_EPI_BF16)
+    _, N, K = w.codes.shape
+    return L.int8_grouped_gemm(x, w, N=N, K=K, total_rows=x.shape[0], epilogue=epilogue)
 
 
 def int8_moe_block(x: torch.Tensor, logits: torch.Tensor, wgu: L.INT8, wd: L.INT8, topk: int,
