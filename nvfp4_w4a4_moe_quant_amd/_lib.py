@@ -693,7 +693,7 @@ def int8_grouped_gemm(a, w: INT8, group_offsets: Optional[torch.Tensor] = None, 
     [G, N].  group_offsets [G + 1] may be None for one group.  epilogue F32,
     SILU_MUL_BF16 or BF16.  validate=True checks the offsets and gather indices
     on the host first (check_groups; synchronizes)."""
-    quantized = type(a) is INT8
+    quantized = isinstance(a, INT8)
     x = a.codes if quantized else a
     shape, dev = x.shape, x.device
     if len(shape) != 2 or shape[1] != K:

@@ -410,24 +410,26 @@ def int8_moe_block(x: torch.Tensor, logits: torch.Tensor, wgu: L.INT8, wd: L.INT
 
 # ------------------------------------------------- the router's balance loss
 class _BalanceLoss(torch.autograd.Function):
-    """The losses, already computed, as a function of the logits."""
+    """The losses; what else the call gives goes into the list `rest`."""
 
     @staticmethod
-    def forward(ctx, logits, k, losses, counts, tokens, mask):
-        ctx.save_for_backward(logits, counts, tokens, mask)
-        ctx.k = k
+    def forward(ctx, logits, topk_ids, mask, rest):
+        r = L.moe_balance_loss(logits, topk_ids, mask=mask)
+        ctx.save_for_backward(logits, r.counts, r.tokens, mask)
+        ctx.k = topk_ids.shape[1]
         ctx.set_materialize_grads(False)
-        return losses.view(2)
+        rest.append(r)
+        return r.losses
 
     @staticmethod
     def backward(ctx, g_losses):
         if torch.is_grad_enabled():  # under create_graph
             raise RuntimeError("moe_balance_loss has no second derivative")
         if g_losses is None:
-            return None, None, None, None, None, None
+            return None, None, None, None
         logits, counts, tokens, mask = ctx.saved_tensors
         return L.moe_balance_loss_backward(logits, ctx.k, counts, tokens, g_losses.contiguous(),
-                                           mask=mask), None, None, None, None, None
+                                           mask=mask), None, None, None
 
 
 def moe_balance_loss(logits: torch.Tensor, topk_ids: torch.Tensor,
@@ -444,7 +446,6 @@ def moe_balance_loss(logits: torch.Tensor, topk_ids: torch.Tensor,
     if logits.is_leaf and torch.cuda.is_current_stream_capturing():
         raise RuntimeError("leaf logits under capture: use the library's moe_balance_loss and "
                            "moe_balance_loss_backward")
-    with torch.no_grad():
-        r = L.moe_balance_loss(logits, topk_ids, mask=mask)
-    losses = _BalanceLoss.apply(logits, topk_ids.shape[1], r.losses, r.counts, r.tokens, mask)
-    return r._replace(losses=losses)
+    rest = []
+    losses = _BalanceLoss.apply(logits, topk_ids, mask, rest)
+    return rest[0]._replace(losses=losses)

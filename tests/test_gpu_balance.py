@@ -224,6 +224,15 @@ def test_autograd_with_the_router():
     eq(host(full.counts), np.diff(offs), "counts are the products' group sizes")
     leaf = z.detach().requires_grad_()
     r = P.moe_balance_loss(leaf, rt.topk_ids)
+    r.losses.mul_(2.0)                                  # an output like any other
+    g2, = torch.autograd.grad(r.losses[0], leaf)
+    g1, = torch.autograd.grad(P.moe_balance_loss(leaf, rt.topk_ids).losses[0], leaf)
+    assert torch.equal(g2, 2 * g1)
+    r = P.moe_balance_loss(leaf, rt.topk_ids)
+    r.counts.zero_()                                    # the backward pass needs them
+    with pytest.raises(RuntimeError, match="inplace"):
+        torch.autograd.grad(r.losses.sum(), leaf)
+    r = P.moe_balance_loss(leaf, rt.topk_ids)
     with pytest.raises(RuntimeError, match="second derivative"):
         torch.autograd.grad(r.losses.sum(), leaf, create_graph=True)
     g, = torch.autograd.grad(r.losses[1], leaf, allow_unused=True)

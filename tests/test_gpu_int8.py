@@ -336,6 +336,25 @@ def test_offsets_beyond_32_bits():
     assert not q.codes[:-3].any()
 
 
+def test_outputs_off_16_bytes():
+    """Outputs that start anywhere; what lies beside them stays."""
+    say("int8, outputs off 16 bytes")
+    rng = np.random.default_rng(21)
+    for rows in (3, 40, 100, 500):
+        x = rows_of(rng, rows, 272, "bf16")
+        w, sw = weights_of(rng, 1, 64, 272)
+        a, sa = R.quantize(x)
+        y = R.product(a, sa, w, sw, [0, rows])
+        for epi, n, dt in (("f32", 64, torch.float32), ("bf16", 64, torch.bfloat16),
+                           ("silu", 32, torch.bfloat16)):
+            buf = torch.full((rows * n + 8,), 5.0, dtype=dt, device=DEV)
+            out = buf[1:1 + rows * n].view(rows, n)
+            L.int8_grouped_gemm(to_dev(x, "bf16"), L.INT8(up(w), up(sw)), N=64, K=272,
+                                total_rows=rows, epilogue=EPIS[epi], out=out)
+            check_out(out, y, epi)
+            assert buf[0] == 5 and (buf[1 + rows * n:] == 5).all()
+
+
 def test_empty_layers():
     say("int8, no rows")
     w = L.INT8(torch.zeros(4, 64, 32, dtype=torch.int8, device=DEV), torch.zeros(4, 64, device=DEV))
