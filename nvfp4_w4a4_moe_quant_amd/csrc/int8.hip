@@ -184,7 +184,11 @@ struct I8Params {
   const float* w_scales;
   void* out;
   int vec;  // rows of out start on 16 bytes and hold whole 16-byte pieces
+  int32_t* part;  // kPartial: sums over a part of K, [parts][total_rows][pitch]
+  int pitch;      // columns, a multiple of four
 };
+
+constexpr int kPartial = 3;  // an epilogue of the kernel's own, joined by k_i8_join
 
 // silu(g) * u in FP32 with the hardware exp and reciprocal.
 __device__ __forceinline__ float i8_silu_mul(float g, float u) {
@@ -575,20 +579,23 @@ struct I8Tile {
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[0][b][e] = 0;
     const int total = nfull + (rem ? 1 : 0);
+    // the workgroup's chunks: all, or its part of them
+    const int c0 = EPI == kPartial ? total * (int)blockIdx.y / (int)gridDim.y : 0;
+    const int c1 = EPI == kPartial ? total * ((int)blockIdx.y + 1) / (int)gridDim.y : total;
 #pragma unroll 1
-    for (int c = 0; c < NS && c < total; ++c) {
-      const uint32_t back = step_back(c);
+    for (int c = 0; c < NS && c0 + c < c1; ++c) {
+      const uint32_t back = step_back(c0 + c);
 #pragma unroll
-      for (int j = 0; j < NPI; ++j) issue1(j, c, c, back);
+      for (int j = 0; j < NPI; ++j) issue1(j, c0 + c, c, back);
     }
     const uint32_t x = (lh ^ i8_swz((uint32_t)lr)) << 4;
     const uint8_t* al = lds + (wm * 32 + lr) * KC;
     const uint8_t* wl = lds + (BM + wn * FN * 32 + lr) * KC;
     int buf = 0;
 #pragma unroll 1
-    for (int ch = 0; ch < total; ++ch) {
+    for (int ch = c0; ch < c1; ++ch) {
       // this wave's pieces of chunk ch have landed, and every wave's behind the barrier
-      if (ch + NS <= total)
+      if (ch + NS <= c1)
         asm volatile("s_waitcnt vmcnt(%0)" ::"n"((NS - 1) * NPI) : "memory");
       else
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
@@ -609,14 +616,28 @@ struct I8Tile {
           acc[0][b] = __builtin_amdgcn_mfma_i32_32x32x32_i8(wf[s][b], af[s], acc[0][b], 0, 0, 0);
       }
       barrier();  // every wave holds its fragments
-      if (ch + NS < total) {
+      if (ch + NS < c1) {
         const uint32_t back = step_back(ch + NS);
 #pragma unroll
         for (int j = 0; j < NPI; ++j) issue1(j, ch + NS, buf, back);
       }
       buf = buf + 1 == NS ? 0 : buf + 1;
     }
-    if (beg + wm * 32 < end) store<1>(acc, sa, sw);
+    if constexpr (EPI == kPartial) {
+      const int m = beg + wm * 32 + lr;
+      int32_t* out = p.part + ((int64_t)blockIdx.y * p.total_rows + m) * p.pitch;
+#pragma unroll
+      for (int b = 0; b < FN; ++b)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int n = nt * BN + (wn * FN + b) * 32 + q * 8 + lh * 4;
+          if (m < end && n < p.pitch)
+            *reinterpret_cast<int4v*>(out + n) =
+                int4v{acc[0][b][4 * q], acc[0][b][4 * q + 1], acc[0][b][4 * q + 2], acc[0][b][4 * q + 3]};
+        }
+    } else if (beg + wm * 32 < end) {
+      store<1>(acc, sa, sw);
+    }
   }
 
   // Element e of fragment (a, b): tile row (a WM + wm) 32 + lr, tile column
@@ -766,6 +787,41 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_i8_gemm(I8Params p, int n_t
   }
 }
 
+// Adds the parts of K (whole numbers: their order does not matter), four columns
+// to a thread.
+template <int EPI, bool GATHER>
+__global__ __launch_bounds__(256) void k_i8_join(I8Params p, int parts) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int per = p.pitch >> 2;
+  const int64_t m = i / per;
+  if (m >= p.total_rows) return;
+  const int n = (int)(i - m * per) * 4;
+  const int32_t* at = p.part + m * p.pitch + n;
+  int4v sum = *reinterpret_cast<const int4v*>(at);
+  for (int z = 1; z < parts; ++z)
+    sum += *reinterpret_cast<const int4v*>(at + (int64_t)z * p.total_rows * p.pitch);
+  const float sa = p.a_scales[GATHER ? (int64_t)p.gather[m] : m];
+  float y[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) y[e] = (sa * p.w_scales[min(n + e, p.N - 1)]) * (float)sum[e];
+  using OutT = std::conditional_t<EPI == NVFP4_EPI_F32, float, uint16_t>;
+  OutT* out = reinterpret_cast<OutT*>(p.out) + m * p.N + n;
+  if (p.vec) {  // whole pieces of four columns
+    if constexpr (EPI == NVFP4_EPI_F32)
+      *reinterpret_cast<float4*>(out) = make_float4(y[0], y[1], y[2], y[3]);
+    else
+      *reinterpret_cast<uint2*>(out) = make_uint2(i8_bf16(y[0]) | (uint32_t)i8_bf16(y[1]) << 16,
+                                                  i8_bf16(y[2]) | (uint32_t)i8_bf16(y[3]) << 16);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (n + e < p.N) {
+        if constexpr (EPI == NVFP4_EPI_F32) out[e] = y[e];
+        else out[e] = i8_bf16(y[e]);
+      }
+  }
+}
+
 // The tile shapes, and the workgroups of a call on one of them (an upper bound:
 // every group's last tile may be part of one).
 struct I8Shape {
@@ -791,6 +847,22 @@ int launch_tiles(const I8Params& p, hipStream_t s) {
   return nv_launch_status();
 }
 
+// 64 x 128 tiles over `parts` parts of K, and their join.
+template <int EPI>
+int launch_split(const I8Params& p, int parts, hipStream_t s) {
+  const int n_tiles = (p.N + kTiles[0].bn - 1) / kTiles[0].bn;
+  const dim3 grid((unsigned)i8_workgroups(kTiles[0], p.total_rows, p.N, 0), (unsigned)parts);
+  const dim3 join((unsigned)(((int64_t)p.total_rows * (p.pitch >> 2) + 255) / 256));
+  if (p.gather) {
+    hipLaunchKernelGGL((k_i8_gemm<2, 2, 1, 2, 2, kPartial, true>), grid, dim3(256), 0, s, p, n_tiles);
+    hipLaunchKernelGGL((k_i8_join<EPI, true>), join, dim3(256), 0, s, p, parts);
+  } else {
+    hipLaunchKernelGGL((k_i8_gemm<2, 2, 1, 2, 2, kPartial, false>), grid, dim3(256), 0, s, p, n_tiles);
+    hipLaunchKernelGGL((k_i8_join<EPI, false>), join, dim3(256), 0, s, p, parts);
+  }
+  return nv_launch_status();
+}
+
 template <int EPI, int KW, int RT>
 int launch_few(const I8Params& p, int64_t tiles, hipStream_t s) {
   const int cols = EPI == NVFP4_EPI_SILU_MUL_BF16 ? p.N / 2 : p.N;
@@ -809,6 +881,7 @@ struct I8Plan {
   int rt;         // its row tiles of 16 to a workgroup
   int64_t tiles;  // workgroups' row tiles at most
   int tile;       // else: which of kTiles
+  int parts;      // parts of K that its workgroups share, or 0
 };
 
 // Times below are those of the product alone, from quantized rows, in a graph of
@@ -842,6 +915,23 @@ I8Plan plan_of(const int8_gemm_args_t* a) {
     const double c[4] = {rounds(0) * 0.19 + 0.1, rounds(1) * 0.62, rounds(2), rounds(3) * 1.25};
     for (int i = 1; i < 4; ++i)
       if (c[i] < c[pl.tile]) pl.tile = i;
+    // Where one workgroup a CU does not fill the chip, K is split if that saves
+    // more than its sums cost: a chunk of 128 k takes 0.44 us, the join 3 us and
+    // 3 bytes a picosecond for the sums' way out and back (N 4096: 128 rows, K 4096
+    // 17.9 us whole, 15.2 in four parts; 256 rows 18.4, and 19.7 in two; 200 rows, K
+    // 8192 32.8 and 23.9, K 2048 10.6 and 13.9; 100 rows, N 2048, K 7168 28.5 and
+    // 13.9).
+    const int64_t wgs = i8_workgroups(kTiles[0], rows, a->N, 0);
+    double best = 0;
+    if (pl.tile == 0 && !a->group_offsets && a->epilogue != NVFP4_EPI_SILU_MUL_BF16)
+      for (int parts = 2; parts <= 8 && wgs * parts <= 256 && a->K >= 512 * parts; parts *= 2) {
+        const double saved = (double)a->K / 128 * 0.44 * (1 - 1.0 / parts) - 3 -
+                             (double)rows * (double)a->N * 8 * parts / 3e6;
+        if (saved > best) {
+          best = saved;
+          pl.parts = parts;
+        }
+      }
   } else if (mean <= 48) {
     // 128 experts, N 1536, K 2048: 32 rows each 77 us (tile 1: 79), 64 rows 92
     // (87); 256 experts, N 4096, K 7168: 64 rows 1522 (1316)
@@ -872,6 +962,8 @@ int launch_gemm(const I8Params& p, const I8Plan& pl, hipStream_t s) {
     if (pl.rt == 2) return launch_few_of<EPI, 2>(p, pl, s);
     return launch_few_of<EPI, 4>(p, pl, s);
   }
+  if constexpr (EPI != NVFP4_EPI_SILU_MUL_BF16)
+    if (pl.parts) return launch_split<EPI>(p, pl.parts, s);
   if (pl.tile == 0) return launch_tiles<0, 2, 2, 1, 2, 2, EPI>(p, s);  // three to a CU
   if (pl.tile == 1) return launch_tiles<1, 2, 4, 2, 2, 3, EPI>(p, s);
   if (pl.tile == 2) return launch_tiles<2, 4, 2, 2, 4, 2, EPI>(p, s);
@@ -958,8 +1050,11 @@ int int8_quantize_rows(const void* x, int in_dtype, int64_t rows, int64_t K, int
 }
 
 size_t int8_grouped_gemm_workspace_size(const int8_gemm_args_t* a) {
-  if (check_gemm(a) != NVFP4_OK || !a->x || a->total_rows == 0) return 0;
-  return nv_round256((size_t)a->src_rows * (size_t)a->K) + nv_round256(4 * (size_t)a->src_rows);
+  if (check_gemm(a) != NVFP4_OK || a->total_rows == 0) return 0;
+  const I8Plan pl = plan_of(a);
+  // quantized rows and their scales, sums over parts of K
+  return (a->x ? nv_round256((size_t)a->src_rows * (size_t)a->K) + nv_round256(4 * (size_t)a->src_rows) : 0) +
+         4 * (size_t)pl.parts * (size_t)a->total_rows * (size_t)((a->N + 3) & ~3);
 }
 
 int int8_grouped_gemm(const int8_gemm_args_t* a, void* ws, size_t ws_bytes, void* stream) {
@@ -1003,9 +1098,12 @@ int int8_grouped_gemm(const int8_gemm_args_t* a, void* ws, size_t ws_bytes, void
     float* scales = reinterpret_cast<float*>(codes + nv_round256((size_t)a->src_rows * p.K));
     p.a_codes = codes;
     p.a_scales = scales;
+    ws = scales + nv_round256(4 * (size_t)a->src_rows) / 4;
     const int st = launch_rows(a->x, a->x_dtype, a->src_rows, p.K, a->ldx, codes, scales, s);
     if (st != NVFP4_OK) return st;
   }
+  p.part = reinterpret_cast<int32_t*>(ws);
+  p.pitch = (p.N + 3) & ~3;
   if (a->epilogue == NVFP4_EPI_SILU_MUL_BF16)
     return launch_gemm<NVFP4_EPI_SILU_MUL_BF16>(p, pl, s);
   if (a->epilogue == NVFP4_EPI_BF16) return launch_gemm<NVFP4_EPI_BF16>(p, pl, s);

@@ -125,7 +125,8 @@ def test_rows_strided_and_given_out():
 DENSE = [(1, 16, 16), (1, 1, 32), (1, 4096, 4096), (2, 100, 48), (3, 65, 64), (7, 384, 1024),
          (16, 512, 2048), (17, 130, 1040), (31, 96, 7168), (33, 250, 80), (64, 1999, 512),
          (65, 256, 128), (100, 255, 272), (128, 384, 384), (200, 1000, 1056), (256, 512, 640),
-         (300, 260, 4112), (700, 1028, 208), (2300, 512, 256), (1, 128, 131056)]
+         (300, 260, 4112), (700, 1028, 208), (2300, 512, 256), (1, 128, 131056), (70, 1030, 4112), (100, 2048, 7168),
+         (129, 384, 8192), (200, 67, 16384), (65, 128, 131056), (300, 1024, 4096)]
 
 
 @pytest.mark.parametrize("rows,N,K", DENSE)
@@ -181,6 +182,23 @@ def test_rows_that_are_not_finite_stay_alone():
         ref = R.product(a, sa, w, sw, [0, rows])
         assert np.isnan(y[4]).all()
         eq(np.delete(y, 4, 0), np.delete(ref, 4, 0), "other rows")
+
+
+def test_split_rows_gathered():
+    """One group without offsets, its rows gathered, K split over workgroups."""
+    say("int8 dense, gathered")
+    rng = np.random.default_rng(4)
+    for rows, N, K in ((90, 200, 6160), (20, 64, 512), (400, 129, 4096)):
+        x = rows_of(rng, 50, K, "f32")
+        w, sw = weights_of(rng, 1, N, K)
+        gat = rng.integers(0, 50, rows).astype(np.int32)
+        a, sa = R.quantize(x)
+        y = R.product(a, sa, w, sw, [0, rows], gat)
+        for epi in ("f32", "bf16"):
+            for act in (to_dev(x, "f32"), L.INT8(up(a), up(sa))):
+                out = L.int8_grouped_gemm(act, L.INT8(up(w), up(sw)), N=N, K=K, total_rows=rows,
+                                          gather_rows=up(gat), epilogue=EPIS[epi])
+                check_out(out, y, epi)
 
 
 def test_extreme_codes():

@@ -86,6 +86,14 @@ def test_gemm_of_unquantized_rows_validation(lib):
     need = _gemm(lib, size=True, **{**x, "src_rows": 5000, "gather_rows": FAKE, "total_rows": 9999})
     assert need >= 5000 * 52
     assert _gemm(lib, size=True) == 0                   # quantized: none
+    # a long K split over workgroups needs room for its sums, quantized rows or not
+    one = dict(num_groups=1, group_offsets=None, N=2048, K=7168, total_rows=100)
+    split = _gemm(lib, size=True, src_rows=100, **one)
+    assert split >= 2 * 4 * 100 * 2048
+    assert _gemm(lib, size=True, **{**x, **one, "src_rows": 100, "ldx": 7168}) >= split + 100 * 7172
+    assert _gemm(lib, src_rows=100, **one) == EWS
+    assert _gemm(lib, src_rows=100, ws=FAKE, wsb=split - 1, **one) == EWS
+    assert _gemm(lib, size=True, src_rows=100, epilogue=1, **one) == 0
     big = dict(src_rows=5000, gather_rows=FAKE, total_rows=9999)
     assert g(ws=None, **big) == EWS and g(wsb=need - 1, **big) == EWS and g(ws=MIS[4], **big) == EWS
     assert g(total_rows=0, out=None, ws=None) == OK
