@@ -545,7 +545,8 @@ int int8_quantize_rows(const void* x, int in_dtype, int64_t rows, int64_t K, int
  * 16 <= K <= 131056 (no sum of 8-bit products can leave 32 bits), num_groups <=
  * 2^20, total_rows <= 2^30; codes and x 16-byte aligned, out aligned to its
  * elements, ws 16-byte aligned.  Without a gather, src_rows >= total_rows;
- * src_rows K <= 2^36.  A call that needs a grid of 2^32 threads (some 2^23 tiles
+ * src_rows < 2^31 and src_rows K <= 2^36, with a gather (src_rows - 1) K / 16 + 7 <
+ * 2^32 too (the copies count 16-byte units in 32 bits).  A call that needs a grid of 2^32 threads (some 2^23 tiles
  * of 64 x 128 or larger) is refused.  Calls that may overlap need workspaces of their own. */
 typedef struct {
   int64_t num_groups;           /* G >= 1 */

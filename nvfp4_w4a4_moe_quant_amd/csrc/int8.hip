@@ -1020,8 +1020,10 @@ int check_gemm(const int8_gemm_args_t* a) {
                    a->K % 16 || a->K > kMaxK ||
                    (a->epilogue == NVFP4_EPI_SILU_MUL_BF16 && a->N % 2),
                NVFP4_ERR_SHAPE);
-  // gathered rows are addressed by 32 bits of 16-byte units
+  // a gathered row is addressed by 32 bits of 16-byte units, up to seven behind its
+  // start before a short chunk's step back
   NV_RETURN_IF(a->src_rows < 0 || a->src_rows > 0x7fffffff || a->src_rows * a->K > (1LL << 36) ||
+                   (a->gather_rows && (a->src_rows - 1) * (a->K >> 4) + 7 > 0xffffffffLL) ||
                    (!a->gather_rows && a->src_rows < a->total_rows) ||
                    (a->src_rows == 0 && a->total_rows > 0),
                NVFP4_ERR_SHAPE);
