@@ -30,6 +30,7 @@ from __future__ import annotations
 from typing import Dict, Iterable, NamedTuple, Optional, Tuple
 
 import torch
+from torch.autograd import forward_ad
 
 from . import _lib as L
 
@@ -148,6 +149,12 @@ def moe_block(x: torch.Tensor, logits: torch.Tensor, wgu: QuantWeights, wd: Quan
     d["out"] = L.moe_combine(d["y"], d["route"].row_of, d["route"].topk_weights,
                              out_dtype=out_dtype)
     return d
+
+
+def _is_dual(t: torch.Tensor) -> bool:
+    """Whether t carries a tangent of forward-mode differentiation; its
+    requires_grad does not say so, and no_grad does not end it."""
+    return forward_ad._current_level >= 0 and forward_ad.unpack_dual(t).tangent is not None
 
 
 def _no_gradient(x: Optional[torch.Tensor], logits: Optional[torch.Tensor]):
@@ -436,11 +443,13 @@ def moe_balance_loss(logits: torch.Tensor, topk_ids: torch.Tensor,
                      mask: Optional[torch.Tensor] = None) -> L.BalanceOut:
     """The router's balance loss and z-loss (losses [2]) with the gradient of
     logits [T, E], and the counts and mean probabilities, which get none.
-    topk_ids [T, k] is moe_route's choice.  There is no second derivative, and a
-    backward pass fails if the counts were written to before it.  Leaf
-    logits that require a gradient are refused under graph capture, where
-    another living graph of the same leaf ends the process: capture the two
-    library calls instead."""
+    topk_ids [T, k] is moe_route's choice.  There is no second derivative and no
+    forward-mode one (a dual tensor is refused), and a backward pass fails if the
+    counts were written to before it.  Leaf logits that require a gradient are
+    refused under graph capture, where another living graph of the same leaf ends
+    the process: capture the two library calls instead."""
+    if _is_dual(logits):
+        raise RuntimeError("moe_balance_loss has no forward-mode derivative: detach the logits")
     if not (logits.requires_grad and torch.is_grad_enabled()):
         return L.moe_balance_loss(logits, topk_ids, mask=mask)
     if logits.is_leaf and torch.cuda.is_current_stream_capturing():
