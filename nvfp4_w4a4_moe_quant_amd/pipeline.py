@@ -381,6 +381,8 @@ def _int8_no_gradient(x: torch.Tensor, logits: Optional[torch.Tensor] = None):
             and torch.is_grad_enabled():
         raise RuntimeError("the INT8 layers have no gradient: detach their inputs or call them "
                            "under torch.no_grad()")
+    if _is_dual(x) or (logits is not None and _is_dual(logits)):
+        raise RuntimeError("the INT8 layers have no forward-mode derivative: detach their inputs")
 
 
 def int8_linear(x: torch.Tensor, w: L.INT8,

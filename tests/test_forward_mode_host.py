@@ -36,3 +36,29 @@ def test_balance_loss_in_a_transform():
     z = torch.zeros(4, 8)
     with pytest.raises(RuntimeError, match="forward-mode"):
         torch.func.jvp(lambda t: balance(None, t), (z,), (z,))
+
+
+INT8 = L.INT8(torch.zeros(1, 8, 32, dtype=torch.int8), torch.zeros(1, 8))
+
+
+def int8_linear(x, z):
+    P.int8_linear(x, INT8)
+
+
+def int8_block(x, z):
+    P.int8_moe_block(x, z, INT8, INT8, 2)
+
+
+@pytest.mark.parametrize("layer", [int8_linear, int8_block])
+@pytest.mark.parametrize("no_grad", [False, True])
+def test_int8_layers(layer, no_grad):
+    x, z = torch.zeros(4, 32), torch.zeros(4, 8)
+    with forward_ad.dual_level(), torch.set_grad_enabled(not no_grad):
+        with pytest.raises(RuntimeError, match="forward-mode"):
+            layer(dual(x), z)
+        if layer is int8_block:
+            with pytest.raises(RuntimeError, match="forward-mode"):
+                layer(x, dual(z))
+        else:
+            with pytest.raises(ValueError, match="GPU"):
+                layer(dual(x).detach(), z)
