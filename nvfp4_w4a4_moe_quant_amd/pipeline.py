@@ -162,6 +162,8 @@ def _no_gradient(x: Optional[torch.Tensor], logits: Optional[torch.Tensor]):
                                     (logits is not None and logits.requires_grad)):
         raise RuntimeError("the decode-step layer has no gradient: detach its inputs or call it "
                            "under torch.no_grad()")
+    if (x is not None and _is_dual(x)) or (logits is not None and _is_dual(logits)):
+        raise RuntimeError("the decode-step layer has no forward-mode derivative: detach its inputs")
 
 
 def moe_decode(x: torch.Tensor, logits: torch.Tensor, wgu: QuantWeights, wd: QuantWeights,

@@ -62,3 +62,12 @@ def test_int8_layers(layer, no_grad):
         else:
             with pytest.raises(ValueError, match="GPU"):
                 layer(dual(x).detach(), z)
+
+
+def test_decode_step_layer():
+    x, z = torch.zeros(4, 32), torch.zeros(4, 8)
+    w = P.QuantWeights(None, 64, 32)
+    with forward_ad.dual_level():
+        for a in ((dual(x), z), (x, dual(z))):
+            with pytest.raises(RuntimeError, match="forward-mode"):
+                P.moe_decode(*a, w, w, 2)
