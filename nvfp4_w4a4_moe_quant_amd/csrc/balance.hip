@@ -47,8 +47,8 @@ struct BalParams {
   float* mean;
   float* losses;
   // partial sums of nblk workgroups, and what the joining ones share
+  double* part_z;    // [nblk]
   float* part_p;     // [nblk][E]
-  float* part_z;     // [nblk]
   int32_t* part_c;   // [nblk][E]
   int32_t* part_n;   // [nblk]
   double* dots;      // [E / 32]
@@ -195,7 +195,7 @@ __global__ __launch_bounds__(64 * kFwdWaves) void k_balance(BalParams p) {
   constexpr int COLS = LPR * PER * V, NT = 64 * kFwdWaves;
   __shared__ int32_t hist[COLS];
   __shared__ float sp[kFwdWaves][COLS];
-  __shared__ float sz[kFwdWaves];
+  __shared__ double sz[kFwdWaves];
   __shared__ int32_t sn[kFwdWaves];
   __shared__ double sd[kFwdWaves];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -203,7 +203,8 @@ __global__ __launch_bounds__(64 * kFwdWaves) void k_balance(BalParams p) {
   for (int e = tid; e < COLS; e += NT) hist[e] = 0;
   if (!ONE && blockIdx.x == 0 && tid == 0) *p.joined = 0u;
   __syncthreads();
-  float sum[PER * V], z = 0.0f;
+  float sum[PER * V];
+  double z = 0.0;  // an lse of 2^64 has a square beyond FP32's range
   int n = 0;
 #pragma unroll
   for (int i = 0; i < PER * V; ++i) sum[i] = 0.0f;
@@ -218,7 +219,7 @@ __global__ __launch_bounds__(64 * kFwdWaves) void k_balance(BalParams p) {
 #pragma unroll
       for (int i = 0; i < PER * V; ++i) sum[i] += l[i];
       if (lir == 0) {
-        z += lse * lse;
+        z = __builtin_fma((double)lse, (double)lse, z);
         ++n;
       }
       if ((uint32_t)cur.id < (uint32_t)p.E) atomicAdd(&hist[cur.id], 1);
@@ -280,7 +281,7 @@ __global__ __launch_bounds__(64 * kFwdWaves) void k_balance(BalParams p) {
       p.part_c[b * p.E + e] = hist[e];
     }
     if (tid == 0) {
-      float s = sz[0];
+      double s = sz[0];
       int c = sn[0];
       for (int w = 1; w < kFwdWaves; ++w) {
         s += sz[w];
@@ -318,7 +319,7 @@ __global__ __launch_bounds__(kJoinCols* kJoinParts) void k_balance_join(BalParam
     }
   }
   if (tid < 256) {  // nblk <= 256
-    double z = tid < nblk ? p.part_z[tid] : 0.0f;
+    double z = tid < nblk ? p.part_z[tid] : 0.0;
     int n = tid < nblk ? p.part_n[tid] : 0;
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) {
@@ -512,7 +513,7 @@ extern "C" {
 size_t moe_balance_loss_workspace_size(int64_t T, int64_t E) {
   if (T < 0 || E < 1 || E > kMaxE) return 0;
   // the loss's shares and the counter, then the partial sums
-  return nv_round256(512 + (T * 64 <= kOneBlock ? 0 : 8 * (size_t)fwd_blocks(T, 1) * (size_t)(E + 1)));
+  return nv_round256(512 + (T * 64 <= kOneBlock ? 0 : (size_t)fwd_blocks(T, 1) * (size_t)(8 * E + 12)));
 }
 
 int moe_balance_loss(const void* logits, int dtype, int64_t T, int64_t E, int64_t ld,
@@ -543,9 +544,9 @@ int moe_balance_loss(const void* logits, int dtype, int64_t T, int64_t E, int64_
   p.losses = losses;
   p.dots = reinterpret_cast<double*>(ws);
   p.joined = reinterpret_cast<uint32_t*>(p.dots + kMaxE / kJoinCols);
-  p.part_p = reinterpret_cast<float*>(p.dots + 64);
-  p.part_z = p.part_p + nblk * E;
-  p.part_c = reinterpret_cast<int32_t*>(p.part_z + nblk);
+  p.part_z = p.dots + 64;
+  p.part_p = reinterpret_cast<float*>(p.part_z + nblk);
+  p.part_c = reinterpret_cast<int32_t*>(p.part_p + nblk * E);
   p.part_n = p.part_c + nblk * E;
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   return dtype == NVFP4_IN_BF16 ? launch_by_experts<true>(p, false, s)
