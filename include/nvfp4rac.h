@@ -598,9 +598,10 @@ int int8_grouped_gemm(const int8_gemm_args_t* args, void* ws, size_t ws_bytes, v
  * 16-byte pieces).  topk_ids int32 [T, k] (moe_route's), mask uint8 [T] or
  * NULL.  mean_probs is nullable.  grad_logits has row stride ldg >= E and may
  * be the logits themselves (same ld).  Requires 1 <= E <= 1024, 1 <= k <= E, T k <
- * 2^31.  Sums of probabilities over rows are FP32 over the rows of a workgroup (16
- * to 128 until T is some 256 times that, T / 256 beyond) and FP64 above that, the
- * sum of lse^2 is FP64; exponentials and logarithms are the hardware's.  The results are
+ * 2^31.  Sums of probabilities over rows are FP32 over at most 64 rows of a lane and
+ * then over the lanes of a workgroup (chains of at most 84 roundings), FP64 above
+ * that, and the sum of lse^2 is FP64 throughout; exponentials and logarithms are the
+ * hardware's.  The results are
  * deterministic.  Calls that may overlap need workspaces of their own.
  * ------------------------------------------------------------------------ */
 size_t moe_balance_loss_workspace_size(int64_t T, int64_t E);

@@ -35,6 +35,9 @@ constexpr int kFwdBlocks = 256;   // workgroups (partial sums) at most
 // 8.7; 32 experts: 512 rows 6.4 for 7.7).
 constexpr int64_t kOneBlock = 5 * 64 * kFwdWaves;
 constexpr int kJoinCols = 32, kJoinParts = 32;
+// Probabilities are added in FP32 over so many rows of a lane, then in FP64: 2^24
+// rows of five experts, 1024 to a lane, drift by 161 half-steps in FP32 alone.
+constexpr int kChain = 64;
 
 struct BalParams {
   const void* logits;
@@ -204,10 +207,15 @@ __global__ __launch_bounds__(64 * kFwdWaves) void k_balance(BalParams p) {
   if (!ONE && blockIdx.x == 0 && tid == 0) *p.joined = 0u;
   __syncthreads();
   float sum[PER * V];
+  double far[PER * V];  // of the chains behind
   double z = 0.0;  // an lse of 2^64 has a square beyond FP32's range
   int n = 0;
 #pragma unroll
-  for (int i = 0; i < PER * V; ++i) sum[i] = 0.0f;
+  for (int i = 0; i < PER * V; ++i) {
+    sum[i] = 0.0f;
+    far[i] = 0.0;
+  }
+  int chain = 0;
   const int64_t stride = (int64_t)gridDim.x * kFwdWaves * Row::RPW;
   int64_t t = ((int64_t)blockIdx.x * kFwdWaves + wave) * Row::RPW + slot;
   Row cur, nxt;
@@ -229,7 +237,18 @@ __global__ __launch_bounds__(64 * kFwdWaves) void k_balance(BalParams p) {
       }
     }
     cur = nxt;
+    if (!ONE && ++chain == kChain) {  // ONE: five rows of a lane
+      chain = 0;
+#pragma unroll
+      for (int i = 0; i < PER * V; ++i) {
+        far[i] += (double)sum[i];
+        sum[i] = 0.0f;
+      }
+    }
   }
+  if constexpr (!ONE)
+#pragma unroll
+    for (int i = 0; i < PER * V; ++i) sum[i] = (float)(far[i] + (double)sum[i]);
   // the wave's row slots, then the waves
 #pragma unroll
   for (int o = LPR; o < 64; o <<= 1) {

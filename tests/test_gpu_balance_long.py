@@ -54,3 +54,22 @@ def test_z_loss_of_large_logits():
         z[9] = 1e30
         r = L.moe_balance_loss(z, torch.from_numpy(ids).to(DEV))
         assert torch.isinf(r.losses[1]) and torch.isfinite(r.losses[0])
+
+
+@pytest.mark.parametrize("T,E,pitch,dtype", LONG)
+def test_mean_probabilities_of_equal_rows(T, E, pitch, dtype):
+    """A mean probability is a sum in FP32 over up to 64 rows of a lane, three row
+    slots and 16 waves, rounded once between them, and in FP64 above that: at most
+    64 + 3 + 15 + 2 roundings, beside two of the probability itself."""
+    r = equal_rows(T, E, pitch, dtype)
+    eq(host(r.counts), np.bincount(np.arange(T) % E, minlength=E), "counts")
+    near(r.mean_probs, np.full(E, 1.0 / E), 86 * B.U / E, "mean probabilities")
+    near(r.losses[0], 1.0, 87 * B.U, "balance loss")
+
+
+@pytest.mark.parametrize("T,E,dtype", [
+    (262144, 130, "f32"), (262145, 130, "f32"), (300007, 130, "f32"), (270001, 600, "bf16")])
+def test_more_rows_than_a_chain(T, E, dtype):
+    """64 rows of a lane, and more; masks, padding, dropped slots."""
+    say(f"balance, {T}x{E} {dtype}")
+    check(*case(T + E, T, E, 4, dtype, masked=0.2, padded=0.1, dropped=0.1))
