@@ -6,12 +6,13 @@ import ctypes
 
 import numpy as np
 import pytest
+import torch
 
 from nvfp4_w4a4_moe_quant_amd import _lib as L
 import int8_ref as R
 
 pytestmark = pytest.mark.gpu
-from gpu_util import say, to_dev
+from gpu_util import DEV, eq, host, say, to_dev
 from test_gpu_int8 import EPIS, check_out, rows_of, up, weights_of
 
 
@@ -86,3 +87,34 @@ def test_few_rows_of_wide_layers(rows, N, K):
     out = L.int8_grouped_gemm(to_dev(x, "bf16"), L.INT8(up(w), up(sw)), N=2 * N, K=K,
                               total_rows=rows, epilogue=EPIS["silu"])
     check_out(out, R.product(a, sa, w, sw, [0, rows]), "silu")
+
+
+@pytest.mark.parametrize("K,src", [(64, (1 << 30) - 1), (48, 1431655763), (32, (1 << 31) - 3)])
+def test_last_rows_that_a_gather_reaches(K, src):
+    """The largest tensors of rows shorter than a chunk that a gather may take: the
+    last rows' 16-byte units end at 2^32."""
+    say(f"int8 gathered from {src} rows of {K}")
+    g = torch.Generator(device=DEV)
+    g.manual_seed(K)
+    codes = torch.empty((src, K), dtype=torch.int8, device=DEV)
+    near, far = 50, src - 50
+    for at in (0, far):
+        codes[at:at + 50] = torch.randint(-127, 128, (50, K), generator=g, device=DEV,
+                                          dtype=torch.int8)
+    sa = torch.empty(src, device=DEV)
+    sa[:near] = 1.5
+    sa[far:] = 0.75
+    w = torch.randint(-127, 128, (2, 200, K), generator=g, device=DEV, dtype=torch.int8)
+    sw = torch.rand(2, 200, generator=g, device=DEV) + 0.5
+    rng = np.random.default_rng(K)
+    for rows in (20, 400):                              # the kernel for few rows, and tiles
+        gat = np.concatenate([rng.integers(0, near, rows // 2), rng.integers(far, src, rows // 2)])
+        gat[-1] = src - 1
+        off = np.array([0, rows // 2 + 3, rows], np.int32)
+        y = L.int8_grouped_gemm(L.INT8(codes, sa), L.INT8(w, sw), up(off), N=200, K=K,
+                                total_rows=rows, gather_rows=up(gat.astype(np.int32)))
+        idx = up(gat)
+        eq(host(y), R.product(host(codes[idx]), host(sa[idx]), host(w), host(sw), off),
+           f"{rows} gathered rows")
+    del codes, sa
+    torch.cuda.empty_cache()
