@@ -691,8 +691,9 @@ def int8_grouped_gemm(a, w: INT8, group_offsets: Optional[torch.Tensor] = None, 
     """a: INT8 rows, or x [src_rows, K] (bf16 or FP32, row stride honoured), which
     the call quantizes as int8_quantize_rows does.  w: codes [G, N, K], scales
     [G, N].  group_offsets [G + 1] may be None for one group.  epilogue F32,
-    SILU_MUL_BF16 or BF16.  validate=True checks the offsets and gather indices
-    on the host first (check_groups; synchronizes)."""
+    SILU_MUL_BF16 or BF16.  validate=True checks the offsets, which may end before
+    total_rows, and the groups' gather indices on the host first (check_groups;
+    synchronizes)."""
     quantized = isinstance(a, INT8)
     x = a.codes if quantized else a
     shape, dev = x.shape, x.device
@@ -717,9 +718,12 @@ def int8_grouped_gemm(a, w: INT8, group_offsets: Optional[torch.Tensor] = None, 
     else:
         xp, xd, ldx = x.data_ptr(), _dtype_code(x), _row_stride(x, "x")
     if validate:
-        if group_offsets is None:
-            group_offsets = torch.tensor([0, total_rows], dtype=torch.int32)
-        check_groups(group_offsets, total_rows, gather_rows, src_rows)
+        ends = torch.tensor([0, total_rows], dtype=torch.int32) if group_offsets is None \
+            else group_offsets.cpu()
+        rows = int(ends[-1])  # those behind the last group are not touched
+        if rows > total_rows:
+            raise NVFP4Error(f"group_offsets end at {rows}, total_rows is {total_rows}")
+        check_groups(ends, rows, None if gather_rows is None else gather_rows[:rows], src_rows)
     odt = torch.float32 if epilogue == NVFP4_EPI_F32 else torch.bfloat16
     cols = N // 2 if epilogue == NVFP4_EPI_SILU_MUL_BF16 else N
     if out is None:
