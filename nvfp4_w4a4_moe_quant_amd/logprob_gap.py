@@ -8,10 +8,11 @@ it sampled with and the trainer's (blog post, section "What it buys").  Here,
 on a small seeded layer and vocabulary head: the trainer's forward takes the
 fake-quantized weights (nvfp4_qdq) and unquantized activations; the rollout
 is naive W4A4, W4A4 with RAC, the decode-step layer, which leaves the
-activations alone too, or an INT8 layer (W8A8) on the trainer's plain weights,
-against which it is measured.  Prints, per rollout, the mean and largest absolute
-difference of the sampled tokens' log-probabilities and the mean entropy, and
-how evenly the layer's router spreads the tokens.
+activations alone too, or an INT8 layer (W8A8) on the plain weights, which is
+measured against a trainer on those: the gaps to the two trainers do not compare.
+Prints, per rollout, the mean and largest absolute difference of the sampled
+tokens' log-probabilities, the mean entropy and which trainer, and how evenly
+the layer's router spreads the tokens.
 """
 from __future__ import annotations
 
@@ -99,7 +100,10 @@ def main() -> None:
     seed = int(sys.argv[1]) if len(sys.argv) > 1 else 1
     for name, f in gaps(seed, int8=True):
         print(f"{name:20s} |log-prob gap| mean {f['mean']:.5f}  max {f['max']:.5f}  "
-              f"entropy {f['entropy']:.3f}")
+              f"entropy {f['entropy']:.3f}  trainer on "
+              f"{'plain' if name == 'INT8 W8A8' else 'fake-quantized'} weights")
+    print("The two trainers' gaps do not compare: INT8's holds the rounding of its weights, the "
+          "others' do not.")
     r = router(seed)
     print(f"router: balance loss {r['balance']:.4f}, z-loss {r['z']:.3f}, experts from "
           f"{r['emptiest']:.2f} to {r['fullest']:.2f} of the mean load")
