@@ -4,7 +4,8 @@
 // Per counted row, p = softmax(l) and lse = m + ln sum e^(l - m).  A row is held by
 // LPR lanes, V logits to a load, so that a wave works on 64 / LPR rows at a time
 // with the next ones in flight.  Forward, a lane keeps the sums of its experts'
-// probabilities over the rows of its wave; workgroups write partial sums, and a
+// probabilities over the rows of its wave, in FP32 over 64 rows at a time and in
+// FP64 beyond, and lse^2 in FP64; workgroups write partial sums, and a
 // second launch joins them, a workgroup for 32 experts each, the last of them
 // adding up the loss.  Few rows take one launch of one workgroup.
 // Backward needs the counts alone besides the row itself:
@@ -12,12 +13,15 @@
 // The counts enter centred, c_j - (sum c) / E, which changes nothing since the p
 // sum to one and keeps the difference small where the experts are balanced.
 //
-// What bounds it: few rows the latency of a chain of loads, reductions and the
-// join (8192 x 256 FP32: forward 4.7 + 7.7 us, backward 7.4 us, for 8 MB read
-// once), many rows HBM (65536 x 256 FP32: forward 18 us, backward 24 us for 134
-// MB, 5.7 TB/s) or, in bf16, as much the arithmetic (65536 x 128: 7.6 + 6.9 us and
-// 14 us for 34 MB).  A wave for a row with one logit to a load, and one workgroup
-// to join: 10.5 + 80 us for the first forward, 77 + 83 us for the last.
+// What bounds it (times of a trace, which adds about a microsecond to a kernel): few
+// rows the latency of a chain of loads, reductions and the join (8192 x 256 FP32:
+// forward 5.1 + 7.7 us, backward 7.6 us, for 8 MB read once; in a graph 11.6 and
+// 6.3), many rows memory (65536 x 256 FP32 with inputs beyond the last-level cache
+// in turn: forward 22 + 6 us for 67 MB, backward 24 us for 134 MB, of which the
+// forward call left the logits in that cache) or, in bf16, as much the arithmetic
+// (65536 x 128: 8.8 + 6.1 us and 15 us for 34 MB).  A wave for a row with one logit
+// to a load, and one workgroup to join: 10.5 + 80 us for the forward of 8192 x 256,
+// 77 + 83 us for that of 65536 x 128.
 
 #include <type_traits>
 

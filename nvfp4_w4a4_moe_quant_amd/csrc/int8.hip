@@ -7,25 +7,27 @@
 //
 // MI355X design:
 //  * k_i8_rows: a row stays in the registers of one to eight waves between its
-//    maximum and its codes.  HBM-bound when large (8192 x 7168 bf16 29 us, 6.0
-//    TB/s), 2 to 4 us when small.
+//    maximum and its codes.  HBM-bound when large (8192 x 7168 bf16, 176 MB: 34 us
+//    and 5.1 TB/s with inputs beyond the last-level cache in turn, 28 us where one
+//    input stays in it), 2 to 5 us when small.
 //  * k_i8_few: a few rows against W that streams once, straight into registers;
-//    the waves of a workgroup split K.  4.7 us for one row of 4096 x 4096 (3.6 TB/s
-//    of codes), 40 us for the 8 rows of a token at K 7168, N 4096 (5.9 TB/s).
+//    the waves of a workgroup split K.  4.9 us for one row of 4096 x 4096 (3.4 TB/s
+//    of codes, which the last-level cache holds), 40 us for the 8 rows of a token
+//    at K 7168, N 4096 (5.9 TB/s).
 //  * k_i8_gemm: tiles of 64 x 128 to 320 x 256.  Rows of 128 k go into LDS by DMA,
 //    two or three chunks deep, at uniform bases and 32-bit offsets; fragments of
 //    the next 32 k are read while those in registers are multiplied; the D tiles
 //    are W by rows, so that a lane holds four neighbouring columns, and go out
 //    through LDS as whole rows of 16-byte pieces (as they come, a store of 2 or 4
 //    bytes each, 65536 x 4096 x 1024 took 548 us for 361).  The smallest tile
-//    streams W for many experts of few rows: 483 us for 16 tokens of 256 experts
+//    streams W for many experts of few rows: 479 us for 16 tokens of 256 experts
 //    (K 7168, N 4096, 102 experts' 2.95 GB: 6.1 TB/s).
-//  * What bounds the large products is power: 65536 x 4096 x 8192 runs its matrix
-//    cores 80% of the cycles at 1.3 GHz, 256 experts of 256 rows 65% at 1.33
-//    GHz (2.4 GHz when light; the same call on zeros is 22% faster).  Where the
-//    time goes otherwise (parts left out for timing, 1836 us then): the copies
-//    into LDS 20%, the fragment reads 4%, waits and barriers nothing.  Tried and
-//    slower: 16 x 16 x 64 products (1883 for 1836 us); four waves of 128 x 128
+//  * What bounds the large products is power: 65536 x 4096 x 8192 (1674 us) runs its
+//    matrix cores 79% of the cycles at 1.4 GHz, 256 experts of 256 rows 67% at 1.3
+//    GHz, where the 16 tokens' call runs at 2.1 GHz; on zeros the first of them
+//    takes 1409 us.  Where the time goes otherwise (parts left out for timing, 1836
+//    us then): the copies into LDS 20%, the fragment reads 4%, waits and barriers
+//    nothing.  Tried and slower: 16 x 16 x 64 products (1883 for 1836 us); four waves of 128 x 128
 //    (K 1024: 373 for 346 us; K 8192: 1729-1766 for 1780-1815); W fetched into
 //    the L2 a few chunks ahead (256 experts 2239 for 2102 us); copies of rows
 //    behind a group's end left out (2173 for 2137 us).
@@ -980,8 +982,8 @@ int launch_rows_of(const void* x, int64_t rows, int K, int64_t ldx, int8_t* code
   return nv_launch_status();
 }
 
-// A workgroup for a row where rows are few (one wave a row before: 128 x 7168 8.6
-// us, now 3.9; 512 x 4096 6.2 and 4.0; 1 x 4096 5.1 and 3.9); else waves enough to
+// Times of one input again and again, which the last-level cache holds.  A workgroup
+// for a row where rows are few (one wave a row before: 128 x 7168 8.6 us, now 3.9; 512 x 4096 6.2 and 4.0; 1 x 4096 5.1 and 3.9); else waves enough to
 // hold it in registers (8192 x 7168 read twice 44 us, four waves of 4 vectors 32,
 // eight of 2 29; 65536 x 2048 89, one of 4 76, two of 2 73, four of 1 92; 4096 x
 // 4096 two of 4 10.7, four of 2 11.7).

@@ -451,7 +451,9 @@ def moe_balance_loss(logits: torch.Tensor, topk_ids: torch.Tensor,
     forward-mode one (a dual tensor is refused), and a backward pass fails if the
     counts were written to before it.  Leaf logits that require a gradient are
     refused under graph capture, where another living graph of the same leaf ends
-    the process: capture the two library calls instead."""
+    the process: capture the two library calls instead.  Captured logits that an
+    operation gave are fine as long as no eager graph of their leaves lives, as for
+    any backward pass."""
     if _is_dual(logits):
         raise RuntimeError("moe_balance_loss has no forward-mode derivative: detach the logits")
     if not (logits.requires_grad and torch.is_grad_enabled()):
