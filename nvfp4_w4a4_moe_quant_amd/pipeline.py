@@ -171,7 +171,8 @@ def moe_decode(x: torch.Tensor, logits: torch.Tensor, wgu: QuantWeights, wd: Qua
     """The MoE FFN layer for up to 64 tokens, in token order, on the same
     quantized weights as moe_block but with unquantized activations (the values
     of the trainer's fake-quantized forward).  There is no backward pass: with
-    gradients enabled, x or logits that require one are refused."""
+    gradients enabled, x or logits that require one are refused, and dual tensors
+    of forward-mode differentiation always."""
     _no_gradient(x, logits)
     return L.nvfp4_moe_decode(x, logits, wgu.w, wd.w, topk, out=out)
 
